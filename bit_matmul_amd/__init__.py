@@ -22,6 +22,9 @@ from __future__ import annotations
 import ctypes
 import os
 
+from . import attention as _attention
+from .attention import *  # noqa: F401,F403
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libbitmm.so")
 
@@ -53,6 +56,7 @@ __all__ = [
     "bitmm_gather_qmm_indexed_workspace_bytes", "bitmm_gather_qmm_indexed", "qmv", "qmm",
     "gather_qmm", "gather_qmv", "gather_qmm_indexed", "bitmm_gather_mm_workspace_bytes",
     "bitmm_gather_mm", "gather_mm",
+    *_attention.__all__,
 ]
 
 
@@ -107,6 +111,7 @@ def lib() -> ctypes.CDLL:
         L.bitmm_gather_mm_workspace_bytes.restype = SZ
         L.bitmm_gather_mm.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, I, I, I, P, SZ, P]
         L.bitmm_gather_mm.restype = I
+        _attention.declare(L)
         _lib = L
     return _lib
 

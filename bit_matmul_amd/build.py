@@ -1,6 +1,6 @@
 """Build libbitmm.so for gfx950 with hipcc, in-tree.
 
-Every translation unit under ``csrc/`` is compiled in parallel into ``_build/`` and
+Every translation unit under ``csrc/`` and ``csrc/attn/`` is compiled in parallel into ``_build/`` and
 linked into ``bit_matmul_amd/libbitmm.so``. The benchmark's measurement kernels
 (``probe/probe.hip``: a streaming read and a matrix-core loop, not part of the library)
 are linked into ``bit_matmul_amd/libbitmm_probe.so``. Run ``python -m bit_matmul_amd.build``.
@@ -26,7 +26,7 @@ ARCH = "gfx950"
 # Packed-FP32 VALU instructions are kept out of the device code.
 DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops", "-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-fno-gpu-rdc",
-          "-Wall", "-Wno-unused-function", "-I", os.path.join(ROOT, "include")]
+          "-Wall", "-Wno-unused-function", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
 
 def hipcc() -> str:
@@ -37,7 +37,7 @@ def hipcc() -> str:
 
 
 def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
+    return sorted(os.path.join(d, f) for d in (CSRC, os.path.join(CSRC, "attn")) for f in os.listdir(d)
                   if f.endswith((".hip", ".cpp")))
 
 

@@ -1,0 +1,98 @@
+// Device parts shared by the attention kernels: a sequence's extent, the tokens that a tile
+// of query rows has to go over, masks, and the binary16 form of the 4-bit codes.
+//
+// Units. Keys and values enter the matrix cores as binary16, whose eleven bits hold
+// scale * code + bias with an eighth of the rounding of bf16, but whose range is narrow
+// against a bf16 scale's. So each is taken in units of a power of two 2^E: the first tokens set
+// E so that their largest magnitude is near 2^9 of 2^15, and E grows when later ones need it
+// (a wave-uniform branch that ordinary data takes once). Scores are scaled back by a factor
+// that multiplies them anyway, outputs when they are stored.
+#pragma once
+
+#include "attn.hpp"
+
+namespace bitmm {
+namespace attn {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kUnitLimit = 32768.f;  // largest |scale| * 15 + |bias| in units of 2^E
+
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
+__device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
+
+__device__ __forceinline__ f16x2_t as_f16x2(uint32_t w) { return __builtin_bit_cast(f16x2_t, w); }
+__device__ __forceinline__ uint32_t as_u32(f16x2_t v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ f16x2_t splat_f16(float v) {
+  const _Float16 h = (_Float16)v;
+  return f16x2_t{h, h};
+}
+
+// Codes of bits [0, 4) of each half of w, less eight (exact): 1024 + c in binary16 is
+// 0x6400 | c. And of bits [4, 8): 1024 + 16 c.
+__device__ __forceinline__ f16x2_t codes_low(uint32_t w) {
+  return as_f16x2(and_or_b32(w, 0x000F000Fu, 0x64006400u)) - splat_f16(1032.f);
+}
+__device__ __forceinline__ f16x2_t codes_high(uint32_t w) {
+  return __builtin_elementwise_fma(as_f16x2(and_or_b32(w, 0x00F000F0u, 0x64006400u)),
+                                   splat_f16(0.0625f), splat_f16(-72.f));
+}
+
+// What a sequence has, with lengths and offsets cut to what the host was told.
+struct Extent {
+  int q0;     // first query row
+  int rows;   // query rows of one kv head: queries * share
+  int first;  // position of the first query (may be negative)
+  int kv;     // tokens
+};
+
+__device__ __forceinline__ Extent extent_of(const AttentionParams& p, int b) {
+  Extent e;
+  const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], len = p.kv_lens[b];
+  const int64_t room = p.pages_per_seq << p.cache.page_shift;
+  const int most = (int)(room < p.max_kv ? room : p.max_kv);
+  const int q0 = min(max(c0, 0), p.T);
+  const int q1 = min(max(c1, q0), p.T);
+  const int n = q1 - q0;
+  e.q0 = q0;
+  e.kv = min(max(len, 0), most);
+  e.rows = min(n, p.max_q) * p.share;
+  e.first = e.kv - n;
+  if (p.status && (q0 != c0 || q1 != c1 || n > p.max_q || e.kv != len) && threadIdx.x == 0) *p.status = 1;
+  return e;
+}
+
+// The tokens that rows at positions lo_pos .. hi_pos go over, in steps of STEP tokens that
+// start at multiples of it: first those of the tokens that stay visible, then the window's.
+template <int STEP>
+struct Steps {
+  int sink_steps;
+  int start;  // first token of the window's steps
+  int count;
+
+  __device__ __forceinline__ Steps(int lo_pos, int hi_pos, int window, int sinks) {
+    const int hi = hi_pos + 1;
+    const int lo = window > 0 ? max(0, lo_pos - window + 1) : 0;
+    start = lo / STEP * STEP;
+    sink_steps = window > 0 ? (min(sinks, lo) + STEP - 1) / STEP : 0;
+    if (sink_steps * STEP > start) {
+      sink_steps = 0;
+      start = 0;
+    }
+    count = hi > 0 ? sink_steps + (hi - start + STEP - 1) / STEP : 0;
+  }
+  __device__ __forceinline__ int base(int i) const {
+    return i < sink_steps ? i * STEP : start + (i - sink_steps) * STEP;
+  }
+};
+
+// Whether a step of `n` tokens from base is visible to every row at lo_pos .. hi_pos.
+__device__ __forceinline__ bool all_visible(int base, int n, int lo_pos, int hi_pos, int window) {
+  return base + n - 1 <= lo_pos && (window <= 0 || base > hi_pos - window);
+}
+__device__ __forceinline__ bool visible(int token, int pos, int window, int sinks) {
+  return token <= pos && (window <= 0 || token > pos - window || token < sinks);
+}
+
+}  // namespace attn
+}  // namespace bitmm
