@@ -86,31 +86,6 @@ __device__ __forceinline__ void load_step(const AttentionParams& p, const int32_
   }
 }
 
-__device__ __forceinline__ bool pair_finite(uint32_t pair) {
-  return (pair & 0x7F80u) != 0x7F80u && (pair & 0x7F800000u) != 0x7F800000u;
-}
-__device__ __forceinline__ float pair_size(uint32_t pair) {
-  return fmaf(15.f, fabsf(bf16_lo(pair)), fabsf(bf16_hi(pair)));
-}
-
-// The unit of keys or values: 2^e, and its reciprocal as a factor. Unset until tokens with a
-// nonzero magnitude have come.
-struct Unit {
-  int e;
-  float down;   // 2^-e
-  float limit;  // kUnitLimit, or -1 while unset
-};
-
-// Takes a larger unit for a largest size m (wave-uniform).
-__device__ __forceinline__ void widen(Unit& u, float m) {
-  if (m > 0.f && !(m * u.down <= u.limit)) {
-    // 15 s + |b| of the largest finite s and b is past f32; 2^-120 keeps the factor finite.
-    u.e = max(__builtin_amdgcn_frexp_expf(fminf(m, 3e38f)) - 9, -120);
-    u.down = ldexpf(1.f, -u.e);
-    u.limit = kUnitLimit;
-  }
-}
-
 template <int D, int GS, int DT>
 __global__ __launch_bounds__(256) void attention_rows_kernel(AttentionParams p) {
   using S = StepData<D, GS>;
@@ -468,13 +443,21 @@ hipError_t launch_groups(const AttentionParams& p, int dtype, hipStream_t stream
 
 AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q_heads,
                              int64_t kv_heads, int64_t head_dim, int64_t window, int64_t sinks) {
-  (void)head_dim;
   AttentionPlan plan;
-  const int64_t share = q_heads / kv_heads;
-  plan.row_tiles = (int)((max_q * share + kRows - 1) / kRows);
+  const int64_t rows = max_q * (q_heads / kv_heads);
+  const int64_t span = window > 0 ? std::min(max_kv, window + sinks + max_q) : max_kv;
+  if (rows > 64) {  // tiles of 32 rows a wave
+    plan.waves = head_dim == 256 || B * kv_heads * ((rows + 255) / 256) < 256 ? 4 : 8;
+    plan.row_tiles = (int)((rows + 32 * plan.waves - 1) / (32 * plan.waves));
+    const int64_t groups = B * kv_heads * plan.row_tiles;
+    const int64_t most = std::max<int64_t>(1, span / 512);
+    plan.splits = (int)std::min<int64_t>(std::min((256 + groups - 1) / groups, most), 128);
+    return plan;
+  }
+  plan.waves = 0;
+  plan.row_tiles = (int)((rows + kRows - 1) / kRows);
   // Splits until there are four workgroups a CU, with at least four steps a wave.
   const int64_t groups = B * kv_heads * plan.row_tiles;
-  const int64_t span = window > 0 ? std::min(max_kv, window + sinks + max_q) : max_kv;
   const int64_t steps = (span + kStep - 1) / kStep;
   const int64_t most = std::max<int64_t>(1, steps / (4 * kWaves));
   const int64_t want = (4 * 256 + groups - 1) / std::max<int64_t>(1, groups);
@@ -486,7 +469,8 @@ hipError_t launch_kv_attention(AttentionParams p, const AttentionPlan& plan, int
                                hipStream_t stream) {
   p.row_tiles = plan.row_tiles;
   p.splits = plan.splits;
-  hipError_t err = p.cache.head_dim == 64    ? launch_groups<64>(p, dtype, stream)
+  hipError_t err = plan.waves > 0           ? launch_attention_tiles(p, plan.waves, dtype, stream)
+                   : p.cache.head_dim == 64 ? launch_groups<64>(p, dtype, stream)
                    : p.cache.head_dim == 128 ? launch_groups<128>(p, dtype, stream)
                                              : launch_groups<256>(p, dtype, stream);
   if (err != hipSuccess || p.splits == 1) return err;

@@ -94,5 +94,30 @@ __device__ __forceinline__ bool visible(int token, int pos, int window, int sink
   return token <= pos && (window <= 0 || token > pos - window || token < sinks);
 }
 
+__device__ __forceinline__ bool pair_finite(uint32_t pair) {
+  return (pair & 0x7F80u) != 0x7F80u && (pair & 0x7F800000u) != 0x7F800000u;
+}
+__device__ __forceinline__ float pair_size(uint32_t pair) {
+  return fmaf(15.f, fabsf(bf16_lo(pair)), fabsf(bf16_hi(pair)));
+}
+
+// The unit of keys or values: 2^e, and its reciprocal as a factor. Unset until tokens with a
+// nonzero magnitude have come.
+struct Unit {
+  int e;
+  float down;   // 2^-e
+  float limit;  // kUnitLimit, or -1 while unset
+};
+
+// Takes a larger unit for a largest size m (wave-uniform).
+__device__ __forceinline__ void widen(Unit& u, float m) {
+  if (m > 0.f && !(m * u.down <= u.limit)) {
+    // 15 s + |b| of the largest finite s and b is past f32; 2^-120 keeps the factor finite.
+    u.e = max(__builtin_amdgcn_frexp_expf(fminf(m, 3e38f)) - 9, -120);
+    u.down = ldexpf(1.f, -u.e);
+    u.limit = kUnitLimit;
+  }
+}
+
 }  // namespace attn
 }  // namespace bitmm

@@ -87,6 +87,7 @@ struct AttentionParams {
 // over how many workgroups the tokens of each are split. From sizes alone, so that the
 // workspace query and the call agree.
 struct AttentionPlan {
+  int waves;  // 0: the kernel for few rows; else waves of 32 rows of a workgroup
   int row_tiles;
   int splits;
 };
@@ -94,6 +95,9 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
                              int64_t kv_heads, int64_t head_dim, int64_t window, int64_t sinks);
 hipError_t launch_kv_attention(AttentionParams p, const AttentionPlan& plan, int dtype,
                                hipStream_t stream);
+
+// The kernel for many query rows (prefill.hip).
+hipError_t launch_attention_tiles(const AttentionParams& p, int waves, int dtype, hipStream_t stream);
 
 // ---- device helpers -------------------------------------------------------------------
 

@@ -1,0 +1,454 @@
+// Attention of many query rows (prefill) over the 4-bit cache.
+//
+// A workgroup of NW waves takes 32 NW query rows of one sequence and kv head (its new tokens
+// times the query heads that share the kv head) and goes over the tokens in tiles of 64. The
+// codes of a tile are expanded once a workgroup: each thread keeps the words of the tile after
+// next in registers, turns them into binary16 in LDS for the next one (two buffers, one barrier
+// a tile), and the waves multiply the present one. As in the kernel for few rows, scores and
+// outputs are formed transposed (32x32x16, lane (c, h) = (lane % 32, lane / 32) holds query row
+// c): a lane's sixteen scores of 32 tokens are the next product's operand as they stand.
+//   keys    LDS rows of head_dim values; the 16-byte piece w of row r sits at w ^ swz(r), so
+//           the sixteen rows that a quarter of a wave reads at once hit distinct banks.
+//   values  LDS rows likewise, read by transposing reads (ds_read_b64_tr_b16): within 16 lanes,
+//           lane m points at row m / 4, values 4 (m % 4) .. +3, and lane i receives value i of
+//           the four rows.
+// The eight dims of a word stay in the order in which its codes come out, 0 4 1 5 2 6 3 7, in
+// keys and queries alike; outputs are put in order when they are stored.
+#include "attention.hpp"
+
+namespace bitmm {
+namespace attn {
+namespace {
+
+constexpr int kTile = 64;  // tokens of a tile
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
+
+// What workgroups tell their waves about the tiles, beside keys and values.
+struct TileNotes {
+  uint32_t key_size[2], value_size[2];  // largest sizes (f32 bits) that did not fit, by tile % 2
+  uint64_t bad[4];   // tokens with a scale or bias that is not finite, by tile % 4
+  uint64_t gone[4];  // tokens on pages outside the cache
+};
+
+template <int D, int GS, int NW>
+struct TileLoad {
+  static constexpr int THREADS = 64 * NW;
+  static constexpr int TPT = THREADS / kTile;            // threads of a token
+  static constexpr int W = D / 8 / TPT;                  // words of a thread, of keys and values each
+  static constexpr int PAIRS = (W * 8 + GS - 1) / GS;
+  uint32_t k[W], v[W], kp[PAIRS], vp[PAIRS];
+};
+
+__device__ __forceinline__ void wait_lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <int D, int GS, int DT, int NW>
+__global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kernel(AttentionParams p) {
+  using L = TileLoad<D, GS, NW>;
+  constexpr int ROW = D * 2;                  // bytes of an LDS row
+  constexpr int SIDE = kTile * ROW;           // bytes of a tile's keys or values
+  constexpr int DB = D / 32;                  // blocks of output dims
+  __shared__ __attribute__((aligned(16))) char lds[4 * SIDE];
+  __shared__ TileNotes notes;
+  static_assert(NW * 32 * ROW <= 4 * SIDE, "rows of the epilogue");
+
+  int id = xcd_remap(blockIdx.x, gridDim.x);
+  const int rt = p.row_tiles - 1 - id % p.row_tiles;  // the longest first
+  id /= p.row_tiles;
+  const int split = id % p.splits;
+  id /= p.splits;
+  const int head = id % p.cache.kv_heads;
+  const int b = id / p.cache.kv_heads;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 31, h = lane >> 5;
+
+  const Extent ex = extent_of(p, b);
+  const int r0 = rt * 32 * NW;
+  if (r0 >= ex.rows) return;
+  const int rows = min(32 * NW, ex.rows - r0);
+  const Steps<kTile> steps(ex.first + r0 / p.share, ex.first + (r0 + rows - 1) / p.share, p.window, p.sinks);
+  const int i0 = (int)((int64_t)steps.count * split / p.splits);
+  const int i1 = (int)((int64_t)steps.count * (split + 1) / p.splits);
+  const int32_t* table = p.page_table + (int64_t)b * p.pages_per_seq;
+  if (tid < 10) {
+    if (tid < 2) notes.key_size[tid] = notes.value_size[tid] = 0;
+    if (tid >= 2 && tid < 6) notes.bad[tid - 2] = 0;
+    if (tid >= 6) notes.gone[tid - 6] = 0;
+  }
+
+  // This wave's rows, and this lane's.
+  const int wr = r0 + 32 * wave;
+  const bool wave_live = wr < ex.rows;
+  const int lo_pos = ex.first + min(wr, ex.rows - 1) / p.share;
+  const int hi_pos = ex.first + min(wr + 31, ex.rows - 1) / p.share;
+  const int r = min(wr + c, ex.rows - 1);
+  const int qi = r / p.share;
+  const int q_head = head * p.share + r % p.share;
+  const int pos = ex.first + qi;
+  const uint16_t* qrow = p.q + (int64_t)(ex.q0 + qi) * p.q_stride + (int64_t)q_head * D;
+
+  // The row as binary16, its largest magnitude in [1, 2).
+  f16x8_t q[D / 16];
+  float cq;
+  {
+    u32x4_t raw[D / 16];
+    float big = 0.f;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      raw[s] = load_u128(qrow + 16 * s + 8 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x, y;
+        unpack_half2<DT>(raw[s][e], x, y);
+        big = fmaxf(big, fmaxf(fabsf(x), fabsf(y)));
+      }
+    }
+    big = across32(big, Max());
+    const int e2 = big > 0.f && big < __uint_as_float(0x7F800000u) ? __builtin_amdgcn_frexp_expf(big) - 1 : 0;
+    // The factor stays positive, so that it can wait until after the maximum.
+    cq = p.scale == 0.f ? 1.f : ldexpf(fabsf(p.scale) * kLog2e, e2);
+    const float sign = p.scale < 0.f ? -1.f : p.scale == 0.f ? 0.f : 1.f;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) unpack_half2<DT>(raw[s][e], x[2 * e], x[2 * e + 1]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)(sign * ldexpf(x[(e & 1) * 4 + e / 2], -e2));
+    }
+  }
+
+  // ---- the tile's words: token tid / TPT, words (tid % TPT) W .. --------------------------
+  const int lt = tid / L::TPT, lw = (tid % L::TPT) * L::W;
+  auto page_of = [&](int i) {
+    const int t = steps.base(i) + lt;
+    return i < i1 && t < ex.kv ? table[t >> p.cache.page_shift] : 0;
+  };
+  auto load = [&](int i, int page, L& t) {
+    const int at = steps.base(i) + lt;
+    const bool inside = page >= 0 && page < p.cache.num_pages;
+    const bool live = i < i1 && at < ex.kv && inside;
+    const int64_t row = (((int64_t)(inside ? page : 0) * p.cache.kv_heads + head) << p.cache.page_shift) +
+                        (at & ((1 << p.cache.page_shift) - 1));
+    const uint32_t* kc = p.cache.k_codes + row * (D / 8) + lw;
+    const uint32_t* vc = p.cache.v_codes + row * (D / 8) + lw;
+    if constexpr (L::W == 1) {
+      t.k[0] = kc[0];
+      t.v[0] = vc[0];
+    } else if constexpr (L::W == 2) {
+      const u32x2_t a = *reinterpret_cast<const u32x2_t*>(kc), w = *reinterpret_cast<const u32x2_t*>(vc);
+      t.k[0] = a[0];
+      t.k[1] = a[1];
+      t.v[0] = w[0];
+      t.v[1] = w[1];
+    } else {
+#pragma unroll
+      for (int e = 0; e < L::W; e += 4) {
+        const u32x4_t a = load_u128(kc + e), w = load_u128(vc + e);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          t.k[e + f] = a[f];
+          t.v[e + f] = w[f];
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < L::PAIRS; ++e) {
+      t.kp[e] = p.cache.k_scales[row * (D / GS) + lw * 8 / GS + e];
+      t.vp[e] = p.cache.v_scales[row * (D / GS) + lw * 8 / GS + e];
+    }
+    if (!live) {
+#pragma unroll
+      for (int e = 0; e < L::PAIRS; ++e) t.kp[e] = t.vp[e] = 0;
+      if (i < i1 && at < ex.kv) {
+        atomicOr(reinterpret_cast<unsigned long long*>(&notes.gone[i & 3]), 1ull << lt);
+        if (p.status) *p.status = 1;
+      }
+    }
+  };
+
+  Unit uk = {0, 1.f, -1.f}, uv = {0, 1.f, -1.f};  // of the tile being written
+  // Whether the tile's sizes fit the units, told to the workgroup if not; tokens that are not
+  // finite are marked and emptied first.
+  auto measure = [&](int i, L& t) {
+    float ks = 0.f, vs = 0.f;
+#pragma unroll
+    for (int e = 0; e < L::PAIRS; ++e) {
+      ks = fmaxf(ks, pair_size(t.kp[e]));
+      vs = fmaxf(vs, pair_size(t.vp[e]));
+    }
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < L::PAIRS; ++e) odd = odd || !pair_finite(t.kp[e]) || !pair_finite(t.vp[e]);
+    if (__any(odd || !(ks * uk.down <= uk.limit) || !(vs * uv.down <= uv.limit))) {
+      if (odd) {
+        atomicOr(reinterpret_cast<unsigned long long*>(&notes.bad[i & 3]), 1ull << lt);
+        ks = vs = 0.f;
+#pragma unroll
+        for (int e = 0; e < L::PAIRS; ++e) {
+          if (!pair_finite(t.kp[e])) t.kp[e] = 0;
+          if (!pair_finite(t.vp[e])) t.vp[e] = 0;
+          ks = fmaxf(ks, pair_size(t.kp[e]));
+          vs = fmaxf(vs, pair_size(t.vp[e]));
+        }
+      }
+      ks = reduce_lanes<64>(ks, Max());
+      vs = reduce_lanes<64>(vs, Max());
+      if (lane == 0) {  // not negative: their bits are in order
+        atomicMax(&notes.key_size[i & 1], __float_as_uint(ks));
+        atomicMax(&notes.value_size[i & 1], __float_as_uint(vs));
+      }
+    }
+  };
+  auto expand_side = [&](const uint32_t* words, const uint32_t* pairs, float down, char* row, int swz) {
+#pragma unroll
+    for (int e = 0; e < L::PAIRS; ++e) {
+      const float s = bf16_lo(pairs[e]) * down;
+      const f16x2_t s2 = splat_f16(s), b2 = splat_f16(fmaf(8.f, s, bf16_hi(pairs[e]) * down));
+      constexpr int PER = L::W / L::PAIRS;
+#pragma unroll
+      for (int f = e * PER; f < (e + 1) * PER; ++f) {
+        const uint32_t w = words[f], w8 = w >> 8;
+        const u32x4_t a = {as_u32(__builtin_elementwise_fma(codes_low(w), s2, b2)),
+                           as_u32(__builtin_elementwise_fma(codes_high(w), s2, b2)),
+                           as_u32(__builtin_elementwise_fma(codes_low(w8), s2, b2)),
+                           as_u32(__builtin_elementwise_fma(codes_high(w8), s2, b2))};
+        *reinterpret_cast<u32x4_t*>(row + (((lw + f) ^ swz) << 4)) = a;
+      }
+    }
+  };
+  auto key_swz = [](int row) { return D == 64 ? (row >> 1) & 7 : row & 15; };
+  auto value_swz = [](int row) { return D == 64 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); };
+  auto expand = [&](int i, const L& t) {
+    char* base = lds + (i & 1) * 2 * SIDE;
+    expand_side(t.k, t.kp, uk.down, base + lt * ROW, key_swz(lt));
+    expand_side(t.v, t.vp, uv.down, base + SIDE + lt * ROW, value_swz(lt));
+  };
+  auto read_units = [&](int i) {
+    widen(uk, __uint_as_float(notes.key_size[i & 1]));
+    widen(uv, __uint_as_float(notes.value_size[i & 1]));
+  };
+
+  f32x16_t o[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
+  float m = neg_inf(), l = 0.f;
+  int o_unit = 0;  // exponent of the outputs' unit
+
+  // Read offsets. Keys: row c of a block of 32 tokens, pieces 2 s + h. Values: see above.
+  const int krow = c * ROW, kswz = key_swz(c);
+  const int tm = lane & 15, tg = (lane >> 4) & 1;
+  const int vrow = (4 * h + (tm >> 2)) * ROW;
+  const int vpiece = 2 * tg + ((tm & 3) >> 1), vswz = value_swz(tm >> 2), vhalf = 8 * (tm & 1);
+
+  L t;
+  int page = page_of(i0);
+  if (i0 < i1) {
+    __syncthreads();  // the notes are clear
+    load(i0, page, t);
+    page = page_of(i0 + 1);
+    measure(i0, t);
+    __syncthreads();
+    read_units(i0);
+    expand(i0, t);
+    load(i0 + 1, page, t);
+    page = page_of(i0 + 2);
+    measure(i0 + 1, t);
+  }
+  int k_unit = uk.e, v_unit = uv.e;  // of the tile being multiplied
+  for (int i = i0; i < i1; ++i) {
+    wait_lds_barrier();
+    if (tid == 0) notes.bad[(i + 3) & 3] = notes.gone[(i + 3) & 3] = 0;
+    const char* kb = lds + (i & 1) * 2 * SIDE;
+    const char* vb = kb + SIDE;
+    const uint64_t bad = notes.bad[i & 3], gone = notes.gone[i & 3];
+    read_units(i + 1);
+    const int k_next = uk.e, v_next = uv.e;
+    if (i + 1 < i1) {
+      expand(i + 1, t);
+      load(i + 2, page, t);
+      page = page_of(i + 3);
+    }
+
+    const int base = steps.base(i);
+    if (wave_live && base <= hi_pos) {
+      f32x16_t x[2];
+#pragma unroll
+      for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[tb][e] = 0.f;
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+          const u32x4_t a = *reinterpret_cast<const u32x4_t*>(kb + tb * 32 * ROW + krow + (((2 * s + h) ^ kswz) << 4));
+          x[tb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), q[s], x[tb], 0, 0, 0);
+        }
+      const float ck0 = ldexpf(cq, k_unit);
+      const float ck = ck0 < 1e-37f ? 1e-37f : ck0;  // masked scores times 0 would be NaN
+      if (bad || gone || !all_visible(base, kTile, lo_pos, hi_pos, p.window)) {
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int at = 32 * tb + 8 * (e >> 2) + 4 * h + (e & 3);
+            if (!visible(base + at, pos, p.window, p.sinks) || (gone >> at & 1))
+              x[tb][e] = neg_inf();
+            else if (bad >> at & 1)
+              x[tb][e] = quiet_nan();
+          }
+      }
+      float top = neg_inf();
+#pragma unroll
+      for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, x[tb][e]);
+      top = across32(top, Max()) * ck;
+      if (v_unit != o_unit) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[d][e] = ldexpf(o[d][e], o_unit - v_unit);
+        o_unit = v_unit;
+      }
+      if (__any(top > m + 8.f)) {
+        const float to = fmaxf(m, top);
+        const float alpha = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - to);
+        if (to > neg_inf()) m = to;
+        l *= alpha;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[d][e] *= alpha;
+      }
+      const float off = m == neg_inf() ? 0.f : m;
+      f16x8_t pr[4];
+#pragma unroll
+      for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float y = __builtin_amdgcn_exp2f(fmaf(x[tb][e], ck, -off));
+          l += y;
+          pr[2 * tb + (e >> 3)][e & 7] = (_Float16)y;
+        }
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        const char* at = vb + vrow + (((4 * d + vpiece) ^ vswz) << 4) + vhalf;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + 16 * s * ROW)));
+          const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + (16 * s + 8) * ROW)));
+          const u32x4_t a = {lo[0], lo[1], hi[0], hi[1]};
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), pr[s], o[d], 0, 0, 0);
+        }
+      }
+    }
+    if (i + 2 < i1) measure(i + 2, t);
+    k_unit = k_next;
+    v_unit = v_next;
+  }
+
+  l = across32(l, Add());
+  const int64_t row = (int64_t)(ex.q0 + qi) * p.q_heads + q_head;
+  const bool live = wr + c < ex.rows;
+  const float out_scale = p.splits > 1 ? ldexpf(1.f, o_unit) : (l == 0.f ? 0.f : ldexpf(1.f / l, o_unit));
+  // Dims of a lane's registers: block d, eight dims e / 4, of which (0, 4, 1, 5) for h = 0 and
+  // (2, 6, 3, 7) for h = 1, so that registers (0, 2) and (1, 3) are neighbouring dims.
+  if (p.splits > 1) {
+    if (!live) return;
+    const int64_t at = (int64_t)split * p.T * p.q_heads + row;
+    if (h == 0) {
+      p.part_ml[2 * at] = m;
+      p.part_ml[2 * at + 1] = l;
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        float* to = p.part_o + at * D + 32 * d + 2 * e + 2 * h;
+        *reinterpret_cast<float2*>(to) = make_float2(o[d][e] * out_scale, o[d][e + 2] * out_scale);
+        *reinterpret_cast<float2*>(to + 4) = make_float2(o[d][e + 1] * out_scale, o[d][e + 3] * out_scale);
+      }
+    return;
+  }
+  if (p.lse && live && h == 0) p.lse[row] = kLn2 * (m + __builtin_amdgcn_logf(l));
+  if (p.otype == kOutF32) {
+    if (!live) return;
+    float* to0 = static_cast<float*>(p.out) + (int64_t)(ex.q0 + qi) * p.out_stride + (int64_t)q_head * D;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        float* to = to0 + 32 * d + 2 * e + 2 * h;
+        *reinterpret_cast<float2*>(to) = make_float2(o[d][e] * out_scale, o[d][e + 2] * out_scale);
+        *reinterpret_cast<float2*>(to + 4) = make_float2(o[d][e + 1] * out_scale, o[d][e + 3] * out_scale);
+      }
+    return;
+  }
+  // 16-bit outputs go through LDS, so that a row is stored in 16-byte pieces. The wave's own
+  // region: no barrier but the one that ends the tiles.
+  __syncthreads();
+  char* mine = lds + wave * 32 * ROW;
+#pragma unroll
+  for (int d = 0; d < DB; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      const int dim = 32 * d + 2 * e + 2 * h;
+      const float y0 = o[d][e] * out_scale, y1 = o[d][e + 2] * out_scale;
+      const float y2 = o[d][e + 1] * out_scale, y3 = o[d][e + 3] * out_scale;
+      const uint32_t a = p.otype == kOutBf16 ? pack_half2<0>(y0, y1) : pack_half2<1>(y0, y1);
+      const uint32_t w = p.otype == kOutBf16 ? pack_half2<0>(y2, y3) : pack_half2<1>(y2, y3);
+      char* to = mine + c * ROW + (((dim >> 3) ^ key_swz(c)) << 4);
+      *reinterpret_cast<uint32_t*>(to + 4 * h) = a;
+      *reinterpret_cast<uint32_t*>(to + 8 + 4 * h) = w;
+    }
+  constexpr int PIECES = D / 8;  // of a row
+#pragma unroll
+  for (int e = 0; e < 32 * PIECES / 64; ++e) {
+    const int at = e * 64 + lane, rr = at / PIECES, piece = at % PIECES;
+    const u32x4_t y = *reinterpret_cast<const u32x4_t*>(mine + rr * ROW + ((piece ^ key_swz(rr)) << 4));
+    if (wr + rr < ex.rows) {
+      const int i = (wr + rr) / p.share, qh = head * p.share + (wr + rr) % p.share;
+      *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p.out) + (int64_t)(ex.q0 + i) * p.out_stride +
+                                  (int64_t)qh * D + 8 * piece) = y;
+    }
+  }
+}
+
+template <int D, int GS, int NW>
+hipError_t launch_tiles(const AttentionParams& p, int dtype, hipStream_t stream) {
+  const dim3 grid((unsigned)((int64_t)p.B * p.cache.kv_heads * p.row_tiles * p.splits));
+  if (dtype == 0)
+    hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 0, NW>), grid, dim3(64 * NW), 0, stream, p);
+  else
+    hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 1, NW>), grid, dim3(64 * NW), 0, stream, p);
+  launch_log(grid, dim3(64 * NW), (size_t)(4 * kTile * D * 2 + sizeof(TileNotes)),
+             "attention_tiles_kernel<%d, %d, %d, %d>", D, GS, dtype, NW);
+  return hipGetLastError();
+}
+
+template <int D, int NW>
+hipError_t launch_groups(const AttentionParams& p, int dtype, hipStream_t stream) {
+  if (p.cache.group == 32) return launch_tiles<D, 32, NW>(p, dtype, stream);
+  if (p.cache.group == 64) return launch_tiles<D, 64, NW>(p, dtype, stream);
+  if constexpr (D >= 128) return launch_tiles<D, 128, NW>(p, dtype, stream);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_attention_tiles(const AttentionParams& p, int waves, int dtype, hipStream_t stream) {
+  if (p.cache.head_dim == 256) return launch_groups<256, 4>(p, dtype, stream);
+  if (p.cache.head_dim == 128)
+    return waves == 8 ? launch_groups<128, 8>(p, dtype, stream) : launch_groups<128, 4>(p, dtype, stream);
+  return waves == 8 ? launch_groups<64, 8>(p, dtype, stream) : launch_groups<64, 4>(p, dtype, stream);
+}
+
+}  // namespace attn
+}  // namespace bitmm
