@@ -15,6 +15,8 @@
 //           nibble j of the eight words is the operand of output dims n D/16 + j.
 #include "attention.hpp"
 
+#include <stdlib.h>
+
 #include <algorithm>
 
 namespace bitmm {
@@ -23,75 +25,126 @@ namespace {
 
 constexpr int kRows = 16;   // query rows of a workgroup
 constexpr int kStep = 32;   // tokens of a wave's step
-constexpr int kWaves = 4;
 
-template <int D, int GS>
-struct StepData {
-  static constexpr int KW = D / 32;                          // code words of a key piece
-  static constexpr int KP = (D / 4 + GS - 1) / GS;           // groups it lies in
-  static constexpr int VW = D >= 128 ? D / 128 : 1;          // words of a value piece (64: half a word)
-  uint32_t k[2][KW];
-  uint32_t kp[2][KP];
-  uint32_t v[8][VW];
-  uint32_t vp[8];
+// Where a step's two halves of 16 tokens lie: rows of the cache, the same in every lane.
+struct StepPlace {
+  int64_t row[2];
   bool ok[2];  // the half step's page is in the cache and holds live tokens
-  int base;
 };
 
-template <int D, int GS>
-__device__ __forceinline__ void load_step(const AttentionParams& p, const int32_t* table, int head,
-                                          int kv, int base, int n, int g, StepData<D, GS>& s) {
-  using S = StepData<D, GS>;
-  s.base = base;
+// Pages of the two halves of a step (0 where no token is live).
+struct StepPages {
+  int page[2];
+};
+__device__ __forceinline__ StepPages step_pages(const AttentionParams& p, const int32_t* table, int kv,
+                                                int base) {
+  StepPages s;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) s.page[u] = base + 16 * u < kv ? table[(base + 16 * u) >> p.cache.page_shift] : 0;
+  return s;
+}
+__device__ __forceinline__ StepPlace step_place(const AttentionParams& p, int head, int kv, int base,
+                                                const StepPages& pages) {
+  StepPlace s;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int tb = base + 16 * u;
-    int page = tb < kv ? table[tb >> p.cache.page_shift] : 0;
+    const int page = __builtin_amdgcn_readfirstlane(pages.page[u]);
     const bool inside = page >= 0 && page < p.cache.num_pages;
-    if (!inside && p.status && threadIdx.x % 64 == 0) *p.status = 1;
+    if (!inside && p.status && (threadIdx.x & 63) == 0) *p.status = 1;
     s.ok[u] = tb < kv && inside;
-    page = inside ? page : 0;
-    const int64_t row = (((int64_t)page * p.cache.kv_heads + head) << p.cache.page_shift) +
-                        (tb & ((1 << p.cache.page_shift) - 1));
-    const uint32_t* kc = p.cache.k_codes + (row + n) * (D / 8) + g * S::KW;
-    if constexpr (S::KW == 2) {
-      const u32x2_t w = *reinterpret_cast<const u32x2_t*>(kc);
-      s.k[u][0] = w[0];
-      s.k[u][1] = w[1];
+    s.row[u] = (((int64_t)(inside ? page : 0) * p.cache.kv_heads + head) << p.cache.page_shift) +
+               (tb & ((1 << p.cache.page_shift) - 1));
+  }
+  return s;
+}
+
+// Loads go through descriptors whose bases are those rows: scalar registers hold what moves from
+// step to step, a lane's offset stays what it is, and no 64-bit address is formed in a lane.
+// They span the 16 rows, which lie within one page.
+
+// Pairs of a side of a step: those of a half are 16 NG neighbouring words, and pair 64 e + lane
+// of the step is token (64 e + lane) / NG, group (64 e + lane) % NG.
+template <int NG, int PL>
+__device__ __forceinline__ void load_pairs(const uint32_t* scales, const StepPlace& s, int lane, uint32_t (&to)[PL]) {
+  constexpr int BYTES = 64 * NG;  // of a half step's pairs
+  const __amdgpu_buffer_rsrc_t half[2] = {make_rsrc(scales + s.row[0] * NG, BYTES), make_rsrc(scales + s.row[1] * NG, BYTES)};
+#pragma unroll
+  for (int e = 0; e < PL; ++e) {
+    if constexpr (NG >= 4) {
+      to[e] = __builtin_amdgcn_raw_buffer_load_b32(half[e / (NG / 4)], 4 * lane, 256 * (e % (NG / 4)), 0);
     } else {
-#pragma unroll
-      for (int j = 0; j < S::KW; j += 4) {
-        const u32x4_t w = load_u128(kc + j);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s.k[u][j + e] = w[e];
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < S::KP; ++e)
-      s.kp[u][e] = p.cache.k_scales[(row + n) * (D / GS) + g * (D / 4) / GS + e];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t vr = row + 4 * g + i;
-      if constexpr (D == 64) {
-        s.v[4 * u + i][0] = reinterpret_cast<const uint16_t*>(p.cache.v_codes)[vr * 16 + n];
-      } else if constexpr (D == 128) {
-        s.v[4 * u + i][0] = p.cache.v_codes[vr * 16 + n];
-      } else {
-        const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p.cache.v_codes + vr * 32 + 2 * n);
-        s.v[4 * u + i][0] = w[0];
-        s.v[4 * u + i][1] = w[1];
-      }
-      s.vp[4 * u + i] = p.cache.v_scales[vr * (D / GS) + n * (D / 16) / GS];
+      // Both halves in one wave: each lane's offset is inside one of the two and past the other,
+      // where a load gives zero.
+      const uint32_t at = 4 * lane;
+      to[e] = __builtin_amdgcn_raw_buffer_load_b32(half[0], at, 0, 0) |
+              __builtin_amdgcn_raw_buffer_load_b32(half[1], at - BYTES, 0, 0);
     }
   }
 }
 
-template <int D, int GS, int DT>
-__global__ __launch_bounds__(256) void attention_rows_kernel(AttentionParams p) {
-  using S = StepData<D, GS>;
-  constexpr int J = D / 16;  // output tiles
-  __shared__ float o_lds[kWaves][J * 4][64];
-  __shared__ float ml_lds[kWaves][2][16];
+template <int D, int GS, int KW>
+__device__ __forceinline__ void load_keys(const Cache& c, const StepPlace& s, int lane, uint32_t (&k)[2][KW]) {
+  const uint32_t at = (uint32_t)((lane & 15) * (D / 2) + (lane >> 4) * (GS / 8));
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const __amdgpu_buffer_rsrc_t from = make_rsrc(c.k_codes + s.row[u] * (D / 8), 8 * D);
+#pragma unroll
+    for (int y = 0; y < D / GS; ++y) {
+      if constexpr (GS == 32) {
+        k[u][y] = __builtin_amdgcn_raw_buffer_load_b32(from, at + y * (GS / 2), 0, 0);
+      } else if constexpr (GS == 64) {
+        const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(from, at + y * (GS / 2), 0, 0);
+        k[u][2 * y] = w[0];
+        k[u][2 * y + 1] = w[1];
+      } else {
+        const u32x4_t w = __builtin_amdgcn_raw_buffer_load_b128(from, at + y * (GS / 2), 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k[u][4 * y + e] = w[e];
+      }
+    }
+  }
+}
+template <int D, int VW>
+__device__ __forceinline__ void load_values(const Cache& c, const StepPlace& s, int lane, uint32_t (&v)[8][VW]) {
+  const uint32_t at = (uint32_t)(4 * (lane >> 4) * (D / 2) + (lane & 15) * (D / 32));
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const __amdgpu_buffer_rsrc_t from = make_rsrc(c.v_codes + s.row[u] * (D / 8), 8 * D);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (D == 64) {
+        v[4 * u + i][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(from, at + i * (D / 2), 0, 0);
+      } else if constexpr (D == 128) {
+        v[4 * u + i][0] = __builtin_amdgcn_raw_buffer_load_b32(from, at + i * (D / 2), 0, 0);
+      } else {
+        const u32x2_t w = __builtin_amdgcn_raw_buffer_load_b64(from, at + i * (D / 2), 0, 0);
+        v[4 * u + i][0] = w[0];
+        v[4 * u + i][1] = w[1];
+      }
+    }
+  }
+}
+
+// A pair as binary16 in units of 2^e: (scale, bias + 8 scale), for codes less eight.
+__device__ __forceinline__ uint32_t pair_f16(uint32_t pair, float down) {
+  const float s = bf16_lo(pair) * down;
+  return pack_half2<1>(s, fmaf(8.f, s, bf16_hi(pair) * down));
+}
+
+template <int D, int GS, int DT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_kernel(AttentionParams p) {
+  constexpr int NG = D / GS;                         // groups of a head
+  constexpr int J = D / 16;                          // output tiles
+  constexpr int KW = D / 32, WG = GS / 32;           // a lane's key words, and those of a group
+  constexpr int VW = D >= 128 ? D / 128 : 1;         // words of a value piece (64: half a word)
+  constexpr int PL = NG > 2 ? NG / 2 : 1;            // pairs of a lane
+  // Pairs of each wave's step, [group][token], of the keys and of the values; the joined outputs
+  // afterwards.
+  constexpr int PAIR_BYTES = WAVES * 2 * 32 * NG * 4, JOIN_BYTES = WAVES * J * 4 * 64 * 4;
+  __shared__ __attribute__((aligned(16))) char lds[PAIR_BYTES > JOIN_BYTES ? PAIR_BYTES : JOIN_BYTES];
+  __shared__ float ml_lds[WAVES][2][16];
+  float(*o_lds)[J * 4][64] = reinterpret_cast<float(*)[J * 4][64]>(lds);
 
   int id = blockIdx.x;
   const int rt = id % p.row_tiles;
@@ -102,6 +155,8 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttentionParams p) 
   const int b = id / p.cache.kv_heads;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
+  uint32_t* k_pairs = reinterpret_cast<uint32_t*>(lds) + wave * 64 * NG;
+  uint32_t* v_pairs = k_pairs + 32 * NG;
 
   const Extent ex = extent_of(p, b);
   const int r0 = rt * kRows;
@@ -110,25 +165,40 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttentionParams p) 
   const int lo_pos = ex.first + r0 / p.share;
   const int hi_pos = ex.first + (r0 + rows - 1) / p.share;
   const Steps<kStep> steps(lo_pos, hi_pos, p.window, p.sinks);
-  const int i0 = (int)((int64_t)steps.count * split / p.splits);
-  const int i1 = (int)((int64_t)steps.count * (split + 1) / p.splits);
+  const Part part = part_of(steps.count, split, p.splits);
+  const int i0 = part.first, i1 = part.last;
   const int32_t* table = p.page_table + (int64_t)b * p.pages_per_seq;
 
-  // This lane's query row, as binary16 with its largest magnitude in [1, 2): a bf16 query
-  // keeps every bit that way. The order of a word's eight dims is the codes' (0 4 1 5 ...).
-  const int r = min(r0 + n, ex.rows - 1);
-  const int qi = r / p.share;
-  const int q_head = head * p.share + r % p.share;
-  const int pos = ex.first + qi;
-  const uint16_t* qrow = p.q + (int64_t)(ex.q0 + qi) * p.q_stride + (int64_t)q_head * D + g * (D / 4);
-  f16x8_t q[S::KW];
-  float c;  // scores to base-2 logarithms, but for the keys' unit
+  uint32_t k[2][KW], v[8][VW], kp[PL], vp[PL];
+  StepPages pages = {};
+  StepPlace place = {};
+  const int first = i0 + wave;
+  if (first < i1) {
+    pages = step_pages(p, table, ex.kv, steps.base(first));
+    place = step_place(p, head, ex.kv, steps.base(first), pages);
+    if (first + WAVES < i1) pages = step_pages(p, table, ex.kv, steps.base(first + WAVES));
+    load_keys<D, GS>(p.cache, place, lane, k);
+    load_pairs<NG, PL>(p.cache.k_scales, place, lane, kp);
+    load_values<D>(p.cache, place, lane, v);
+    load_pairs<NG, PL>(p.cache.v_scales, place, lane, vp);
+  }
+
+  // This lane's query row as binary16, its largest magnitude in [2^7, 2^8): a bf16 query keeps
+  // every bit that way. A word's codes come out in the order 0 4 1 5 2 6 3 7, the odd ones
+  // times 16, which the query takes back.
+  const RowOf row_of(p, head, min(r0 + n, ex.rows - 1));
+  const int pos = ex.first + row_of.i;
+  const uint16_t* qrow = p.q + (int64_t)(ex.q0 + row_of.i) * p.q_stride + (int64_t)row_of.head * D + g * (GS / 4);
+  f16x8_t q[KW];
+  float c;            // scores to base-2 logarithms, but for the keys' unit
+  float q_sum[NG];    // sum of the query over each group
+  float centre[NG];   // takes the codes' offsets (1024 + 8, and (1024 + 128) / 16) off a group's sum
   {
-    u32x4_t raw[S::KW];
+    u32x4_t raw[KW];
     float big = 0.f;
 #pragma unroll
-    for (int j = 0; j < S::KW; ++j) {
-      raw[j] = load_u128(qrow + 8 * j);
+    for (int j = 0; j < KW; ++j) {
+      raw[j] = load_u128(qrow + j / WG * GS + 8 * (j % WG));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float x, y;
@@ -137,15 +207,27 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttentionParams p) 
       }
     }
     big = across32(across16(big, Max()), Max());
-    const int e2 = big > 0.f && big < __uint_as_float(0x7F800000u) ? __builtin_amdgcn_frexp_expf(big) - 1 : 0;
+    const int e2 = big > 0.f && big < __uint_as_float(0x7F800000u) ? __builtin_amdgcn_frexp_expf(big) - 8 : 0;
     c = ldexpf(p.scale * kLog2e, e2);
 #pragma unroll
-    for (int j = 0; j < S::KW; ++j) {
-      float x[8];
+    for (int y = 0; y < NG; ++y) {
+      float even = 0.f, odd = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) unpack_half2<DT>(raw[j][e], x[2 * e], x[2 * e + 1]);
+      for (int j = y * WG; j < (y + 1) * WG; ++j) {
+        float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[j][e] = (_Float16)ldexpf(x[(e & 1) * 4 + e / 2], -e2);
+        for (int e = 0; e < 4; ++e) unpack_half2<DT>(raw[j][e], x[2 * e], x[2 * e + 1]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool high = e & 2;
+          q[j][e] = (_Float16)ldexpf(x[(e & 1) * 4 + e / 2], high ? -e2 - 4 : -e2);
+          (high ? odd : even) += (float)q[j][e];
+        }
+      }
+      even = across32(across16(even, Add()), Add());
+      odd = across32(across16(odd, Add()), Add());
+      q_sum[y] = even + 16.f * odd;
+      centre[y] = -fmaf(1032.f, even, 1152.f * odd);
     }
   }
 
@@ -154,60 +236,53 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttentionParams p) 
   for (int j = 0; j < J; ++j) o[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   float m = neg_inf(), l = 0.f;
   Unit uk = {0, 1.f, -1.f}, uv = {0, 1.f, -1.f};
+  // 1024 twice in binary16, in a register, so that mask and OR are one instruction. (No inline
+  // assembly next to the matrix cores: the compiler keeps the distance that their operands and
+  // results need only for instructions that it knows.)
+  uint32_t k1024 = 0x64006400u;
+  asm("" : "+v"(k1024));
 
-  S next;
-  if (i0 + wave < i1) load_step<D, GS>(p, table, head, ex.kv, steps.base(i0 + wave), n, g, next);
-  for (int i = i0 + wave; i < i1; i += kWaves) {
-    S s = next;
-    if (i + kWaves < i1) load_step<D, GS>(p, table, head, ex.kv, steps.base(i + kWaves), n, g, next);
+  for (int i = first; i < i1; i += WAVES) {
+    const int base = steps.base(i);
+    const bool ok0 = place.ok[0], ok1 = place.ok[1], more = i + WAVES < i1;
+    if (more) {
+      place = step_place(p, head, ex.kv, steps.base(i + WAVES), pages);
+      if (i + 2 * WAVES < i1) pages = step_pages(p, table, ex.kv, steps.base(i + 2 * WAVES));
+    }
 
     // Slots that hold no live token may hold anything.
-    const bool whole = s.ok[0] && s.ok[1] && s.base + kStep <= ex.kv;
+    const bool whole = ok0 && ok1 && base + kStep <= ex.kv;
+    uint32_t bad = 0;  // tokens of the step with a scale or bias that is not finite
     if (!whole) {
+      const int at = opaque(lane);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (!s.ok[u] || s.base + 16 * u + n >= ex.kv)
-#pragma unroll
-          for (int e = 0; e < S::KP; ++e) s.kp[u][e] = 0;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          if (!s.ok[u] || s.base + 16 * u + 4 * g + t >= ex.kv) s.vp[4 * u + t] = 0;
+      for (int e = 0; e < PL; ++e) {
+        const int token = (64 * e + at) / NG;
+        const bool ok = (token < 16 ? ok0 : ok1) && base + token < ex.kv && token < 32;
+        kp[e] = ok ? kp[e] : 0;
+        vp[e] = ok ? vp[e] : 0;
       }
     }
-    uint32_t bad = 0;  // tokens of the step with a scale or bias that is not finite
     float ksize = 0.f, vsize = 0.f;
     auto sizes = [&] {
       ksize = vsize = 0.f;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int e = 0; e < S::KP; ++e) ksize += pair_size(s.kp[u][e]);
-#pragma unroll
-      for (int t = 0; t < 8; ++t) vsize += pair_size(s.vp[t]);
+      for (int e = 0; e < PL; ++e) {
+        ksize += pair_size(kp[e]);
+        vsize += pair_size(vp[e]);
+      }
     };
     sizes();
     if (__any(!(ksize * uk.down <= uk.limit) || !(vsize * uv.down <= uv.limit))) {
+      const int at = opaque(lane);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        bool odd = false;
-#pragma unroll
-        for (int e = 0; e < S::KP; ++e)
-          if (!pair_finite(s.kp[u][e])) {
-            s.kp[u][e] = 0;
-            odd = true;
-          }
-        const uint64_t who = __ballot(odd);
-        bad |= (uint32_t)((who | who >> 16 | who >> 32 | who >> 48) & 0xFFFFu) << (16 * u);
+      for (int e = 0; e < PL; ++e) {
+        const bool odd_k = !pair_finite(kp[e]), odd_v = !pair_finite(vp[e]);
+        if (odd_k) kp[e] = 0;
+        if (odd_v) vp[e] = 0;
+        if (odd_k || odd_v) bad |= 1u << ((64 * e + at) / NG % 32);
       }
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const bool odd = !pair_finite(s.vp[t]);
-        if (odd) s.vp[t] = 0;
-        const uint64_t who = __ballot(odd);
-#pragma unroll
-        for (int gg = 0; gg < 4; ++gg)
-          if ((who >> (16 * gg)) & 0xFFFFu) bad |= 1u << (16 * (t / 4) + 4 * gg + t % 4);
-      }
+      bad = __float_as_uint(reduce_lanes<64>(__uint_as_float(bad), Or()));
       sizes();
       widen(uk, reduce_lanes<64>(ksize, Max()));
       const int before = uv.e;
@@ -219,46 +294,63 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttentionParams p) 
           for (int e = 0; e < 4; ++e) o[j][e] = ldexpf(o[j][e], before - uv.e);
       }
     }
+    // The wave's own part of LDS: its operations are in order.
+#pragma unroll
+    for (int e = 0; e < PL; ++e) {
+      const int f = 64 * e + lane;
+      if (NG >= 2 || lane < 32) {
+        k_pairs[f % NG * 32 + f / NG] = pair_f16(kp[e], uk.down);
+        v_pairs[f % NG * 32 + f / NG] = pair_f16(vp[e], uv.down);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
 
-    // Scores.
+    // Scores: the products with the bare codes less eight, group by group, times the scales.
     f32x4_t x[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       x[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      f16x2_t ks[S::KP], kb[S::KP];
 #pragma unroll
-      for (int e = 0; e < S::KP; ++e) {
-        const float sc = bf16_lo(s.kp[u][e]) * uk.down;
-        ks[e] = splat_f16(sc);
-        kb[e] = splat_f16(fmaf(8.f, sc, bf16_hi(s.kp[u][e]) * uk.down));
-      }
+      for (int y = 0; y < NG; ++y) {
+        float at = centre[y];
+        asm volatile("" : "+v"(at));  // made four of here, not kept as four
+        f32x4_t sum = {at, at, at, at};
 #pragma unroll
-      for (int j = 0; j < S::KW; ++j) {
-        const int e = j * 8 / GS;
-        const uint32_t w = s.k[u][j], w8 = w >> 8;
-        const u32x4_t a = {as_u32(__builtin_elementwise_fma(codes_low(w), ks[e], kb[e])),
-                           as_u32(__builtin_elementwise_fma(codes_high(w), ks[e], kb[e])),
-                           as_u32(__builtin_elementwise_fma(codes_low(w8), ks[e], kb[e])),
-                           as_u32(__builtin_elementwise_fma(codes_high(w8), ks[e], kb[e]))};
-        x[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), q[j], x[u], 0, 0, 0);
+        for (int j = y * WG; j < (y + 1) * WG; ++j) {
+          const uint32_t w = k[u][j], w8 = w >> 8;
+          const u32x4_t a = {(w & 0x000F000Fu) | k1024, (w & 0x00F000F0u) | k1024, (w8 & 0x000F000Fu) | k1024,
+                             (w8 & 0x00F000F0u) | k1024};
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), q[j], sum, 0, 0, 0);
+        }
+        const u32x4_t pairs = *reinterpret_cast<const u32x4_t*>(k_pairs + 32 * y + 16 * u + 4 * g);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const f16x2_t sb = as_f16x2(pairs[t]);
+          x[u][t] = fmaf(sum[t], (float)sb[0], fmaf(q_sum[y], (float)sb[1], x[u][t]));
+        }
+        // Done here: moved past the loads below, the sums and pairs of all groups would stay.
+        asm volatile("" : "+v"(x[u]));
       }
+    }
+    if (more) {
+      load_keys<D, GS>(p.cache, place, lane, k);
+      load_pairs<NG, PL>(p.cache.k_scales, place, lane, kp);
     }
     const float ck = ldexpf(c, uk.e);
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int t = 0; t < 4; ++t) x[u][t] *= ck;
-    if (!whole || bad || !all_visible(s.base, kStep, lo_pos, hi_pos, p.window)) {
+    if (!whole || bad || !all_visible(base, kStep, lo_pos, hi_pos, p.window)) {
+      const int g4 = 4 * opaque(g);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const int at = 16 * u + 4 * g + t;
-          const bool see = s.ok[u] && s.base + at < ex.kv && visible(s.base + at, pos, p.window, p.sinks);
-          if (!see)
-            x[u][t] = neg_inf();
-          else if (bad >> at & 1)
-            x[u][t] = quiet_nan();
+          const int at = 16 * u + g4 + t;
+          const bool see = (u ? ok1 : ok0) & (base + at < ex.kv) & visible(base + at, pos, p.window, p.sinks);
+          const float y = bad >> at & 1 ? quiet_nan() : x[u][t];
+          x[u][t] = see ? y : neg_inf();
         }
     }
 
@@ -278,25 +370,28 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttentionParams p) 
         for (int e = 0; e < 4; ++e) o[j][e] *= alpha;
     }
     const float off = m == neg_inf() ? 0.f : m;
-    f16x8_t pr;
+    u32x4_t pr;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float e = __builtin_amdgcn_exp2f(x[u][t] - off);
-        l += e;
-        pr[4 * u + t] = (_Float16)e;
+      for (int t = 0; t < 4; t += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(x[u][t] - off), e1 = __builtin_amdgcn_exp2f(x[u][t + 1] - off);
+        l += e0 + e1;
+        pr[2 * u + t / 2] = pack_half2<1>(e0, e1);
       }
+    const f16x8_t prob = __builtin_bit_cast(f16x8_t, pr);
 
     // Outputs.
     f16x2_t vs[4], vb[4];
+    const uint32_t* v_read = v_pairs + n * (D / 16) / GS * 32 + 4 * g;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const float s0 = bf16_lo(s.vp[2 * t]) * uv.down, s1 = bf16_lo(s.vp[2 * t + 1]) * uv.down;
-      const float b0 = fmaf(8.f, s0, bf16_hi(s.vp[2 * t]) * uv.down);
-      const float b1 = fmaf(8.f, s1, bf16_hi(s.vp[2 * t + 1]) * uv.down);
-      vs[t] = f16x2_t{(_Float16)s0, (_Float16)s1};
-      vb[t] = f16x2_t{(_Float16)b0, (_Float16)b1};
+    for (int u = 0; u < 2; ++u) {
+      const u32x4_t w = *reinterpret_cast<const u32x4_t*>(v_read + 16 * u);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        vs[2 * u + t] = as_f16x2(perm_b32(w[2 * t + 1], w[2 * t], 0x05040100u));
+        vb[2 * u + t] = as_f16x2(perm_b32(w[2 * t + 1], w[2 * t], 0x07060302u));
+      }
     }
 #pragma unroll
     for (int j = 0; j < J; j += 2) {
@@ -304,17 +399,22 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttentionParams p) 
       const uint32_t sel = 0x0c000c00u | (uint32_t)((j / 2) % 4) * 0x00010001u | 0x00040000u;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const uint32_t w = perm_b32(s.v[2 * t + 1][j / 8], s.v[2 * t][j / 8], sel);
+        const uint32_t w = perm_b32(v[2 * t + 1][j / 8], v[2 * t][j / 8], sel);
         lo[t] = as_u32(__builtin_elementwise_fma(codes_low(w), vs[t], vb[t]));
         hi[t] = as_u32(__builtin_elementwise_fma(codes_high(w), vs[t], vb[t]));
       }
-      o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, lo), pr, o[j], 0, 0, 0);
-      o[j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, hi), pr, o[j + 1], 0, 0, 0);
+      o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, lo), prob, o[j], 0, 0, 0);
+      o[j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, hi), prob, o[j + 1], 0, 0, 0);
     }
+    if (more) {
+      load_values<D>(p.cache, place, lane, v);
+      load_pairs<NG, PL>(p.cache.v_scales, place, lane, vp);
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 
-  // The four waves' results joined: each brings its own to the common maximum, and wave w
-  // stores dims (4 g + w) D/16 .. of its lanes' rows.
+  // The waves' results joined: each brings its own to the common maximum, and wave w stores
+  // every WAVES / 4-th part of dims (4 g + w % 4) D/16 .. of its lanes' rows.
   l = across32(across16(l, Add()), Add());
   if (g == 0) {
     ml_lds[wave][0][n] = m;
@@ -323,9 +423,9 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttentionParams p) 
   __syncthreads();
   float mt = neg_inf(), lt = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) mt = fmaxf(mt, ml_lds[w][0][n]);
+  for (int w = 0; w < WAVES; ++w) mt = fmaxf(mt, ml_lds[w][0][n]);
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     const float mw = ml_lds[w][0][n];
     // A sum that is NaN has a maximum of -infinity if it met nothing else.
     lt += ml_lds[w][1][n] * (mw == mt ? 1.f : __builtin_amdgcn_exp2f(mw - mt));
@@ -337,105 +437,114 @@ __global__ __launch_bounds__(256) void attention_rows_kernel(AttentionParams p) 
     for (int e = 0; e < 4; ++e) o_lds[wave][4 * j + e][lane] = o[j][e] * mine;
   __syncthreads();
   if (r0 + n >= ex.rows) return;
-  float y[J];
+  constexpr int PARTS = WAVES / 4 < J / 4 ? WAVES / 4 : J / 4;  // of a lane's J dims, four or more each
+  constexpr int JP = J / PARTS;
+  if (wave >= 4 * PARTS) return;
+  const int i4 = wave & 3, j0 = (wave >> 2) * JP;
+  float y[JP];
 #pragma unroll
-  for (int j = 0; j < J; ++j) {
+  for (int j = 0; j < JP; ++j) {
     y[j] = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) y[j] += o_lds[w][4 * j + wave][lane];
+    for (int w = 0; w < WAVES; ++w) y[j] += o_lds[w][4 * (j0 + j) + i4][lane];
   }
-  const int dim0 = (4 * g + wave) * J;
-  const int64_t row = (int64_t)(ex.q0 + qi) * p.q_heads + q_head;
+  const int dim0 = (4 * g + i4) * J + j0;
+  const bool speaker = g == 0 && wave == 0;
+  const RowOf out_row(p, head, opaque(r0 + n));
+  const int64_t row = (int64_t)(ex.q0 + out_row.i) * p.q_heads + out_row.head;
   if (p.splits > 1) {
     const int64_t at = (int64_t)split * p.T * p.q_heads + row;
-    if (g == 0 && wave == 0) {
+    if (speaker) {
       p.part_ml[2 * at] = mt;
       p.part_ml[2 * at + 1] = lt;
     }
 #pragma unroll
-    for (int j = 0; j < J; j += 4)
+    for (int j = 0; j < JP; j += 4)
       *reinterpret_cast<f32x4_t*>(p.part_o + at * D + dim0 + j) = f32x4_t{y[j], y[j + 1], y[j + 2], y[j + 3]};
     return;
   }
   const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  if (p.lse && g == 0 && wave == 0) p.lse[row] = kLn2 * (mt + __builtin_amdgcn_logf(lt));
-  const int64_t at = (int64_t)(ex.q0 + qi) * p.out_stride + (int64_t)q_head * D + dim0;
-  if (p.otype == kOutF32) {
+  if (p.lse && speaker) p.lse[row] = kLn2 * (mt + __builtin_amdgcn_logf(lt));
+  const int64_t at = (int64_t)(ex.q0 + out_row.i) * p.out_stride + (int64_t)out_row.head * D + dim0;
 #pragma unroll
-    for (int j = 0; j < J; j += 4)
-      *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + at + j) =
-          f32x4_t{y[j] * inv, y[j + 1] * inv, y[j + 2] * inv, y[j + 3] * inv};
-  } else {
-#pragma unroll
-    for (int j = 0; j < J; j += 4) {
-      const u32x2_t w = p.otype == kOutBf16 ? u32x2_t{pack_half2<0>(y[j] * inv, y[j + 1] * inv),
-                                                      pack_half2<0>(y[j + 2] * inv, y[j + 3] * inv)}
-                                            : u32x2_t{pack_half2<1>(y[j] * inv, y[j + 1] * inv),
-                                                      pack_half2<1>(y[j + 2] * inv, y[j + 3] * inv)};
-      *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p.out) + at + j) = w;
-    }
-  }
+  for (int j = 0; j < JP; j += 4) store4(p, at + j, y[j] * inv, y[j + 1] * inv, y[j + 2] * inv, y[j + 3] * inv);
 }
 
-// Joins the partial results of the splits: each thread four dims of one query row, the
-// splits in order.
+// Joins the partial results of the splits. A workgroup takes one query row: 256 / (D / 4)
+// groups of threads go round its splits, four dims a thread, and are added up in LDS.
+template <int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) {
-  const int D = p.cache.head_dim;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int d = (int)(id % (D / 4)) * 4;
-  const int64_t unit = id / (D / 4);
+  constexpr int TPR = D / 4, GROUPS = 256 / TPR;
+  __shared__ f32x4_t sums[GROUPS][TPR];
+  __shared__ float part_l[GROUPS];
+  const int64_t unit = blockIdx.x;
   const int q_head = (int)(unit % p.q_heads);
   const int64_t rest = unit / p.q_heads;
   const int i = (int)(rest % p.max_q);
-  const int64_t b = rest / p.max_q;
-  if (b >= p.B) return;
-  const Extent ex = extent_of(p, (int)b);
+  const Extent ex = extent_of(p, (int)(rest / p.max_q));
   if (i * p.share >= ex.rows) return;
   const int64_t row = (int64_t)(ex.q0 + i) * p.q_heads + q_head;
   const int64_t all = (int64_t)p.T * p.q_heads;
-  float mt = neg_inf();
-  for (int s = 0; s < p.splits; ++s) mt = fmaxf(mt, p.part_ml[2 * (s * all + row)]);
-  float lt = 0.f;
+  const int lane = threadIdx.x & 63;
+  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  // At most 128 splits: two a lane.
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  float2 a = make_float2(neg_inf(), 0.f), b = a;
+  if (lane < p.splits) a = ml[lane * all + row];
+  if (lane + 64 < p.splits) b = ml[(lane + 64) * all + row];
+  const float mt = reduce_lanes<64>(fmaxf(a.x, b.x), Max());
   f32x4_t y = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < p.splits; ++s) {
+  float lt = 0.f;
+#pragma unroll 4
+  for (int s = grp; s < p.splits; s += GROUPS) {
     const int64_t at = s * all + row;
-    const float m = p.part_ml[2 * at], l = p.part_ml[2 * at + 1];
-    if (l == 0.f) continue;
-    const float w = m == mt ? 1.f : __builtin_amdgcn_exp2f(m - mt);
-    const f32x4_t o = *reinterpret_cast<const f32x4_t*>(p.part_o + at * D + d);
-    lt += l * w;
+    const float2 part = ml[at];
+    const f32x4_t o = *reinterpret_cast<const f32x4_t*>(p.part_o + at * D + 4 * t);
+    if (part.y == 0.f) continue;  // saw nothing: the outputs were not written
+    const float w = part.x == mt ? 1.f : __builtin_amdgcn_exp2f(part.x - mt);
+    lt += part.y * w;
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] += o[e] * w;
   }
+  sums[grp][t] = y;
+  if (t == 0) part_l[grp] = lt;
+  __syncthreads();
+  if (grp != 0) return;
+  lt = 0.f;
+  y = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < GROUPS; ++w) {
+    lt += part_l[w];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] += sums[w][t][e];
+  }
   const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  if (p.lse && d == 0) p.lse[row] = kLn2 * (mt + __builtin_amdgcn_logf(lt));
-  const int64_t at = (int64_t)(ex.q0 + i) * p.out_stride + (int64_t)q_head * D + d;
-  if (p.otype == kOutF32)
-    *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + at) =
-        f32x4_t{y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv};
-  else
-    *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p.out) + at) =
-        p.otype == kOutBf16
-            ? u32x2_t{pack_half2<0>(y[0] * inv, y[1] * inv), pack_half2<0>(y[2] * inv, y[3] * inv)}
-            : u32x2_t{pack_half2<1>(y[0] * inv, y[1] * inv), pack_half2<1>(y[2] * inv, y[3] * inv)};
+  if (p.lse && t == 0) p.lse[row] = kLn2 * (mt + __builtin_amdgcn_logf(lt));
+  store4(p, (int64_t)(ex.q0 + i) * p.out_stride + (int64_t)q_head * D + 4 * t, y[0] * inv, y[1] * inv, y[2] * inv,
+         y[3] * inv);
 }
 
-template <int D, int GS>
+template <int D, int GS, int WAVES>
 hipError_t launch_rows(const AttentionParams& p, int dtype, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)p.B * p.cache.kv_heads * p.row_tiles * p.splits));
+  const dim3 grid((unsigned)((int64_t)p.B * p.cache.kv_heads * p.row_tiles * p.splits)), block(64 * WAVES);
   if (dtype == 0)
-    hipLaunchKernelGGL((attention_rows_kernel<D, GS, 0>), grid, dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((attention_rows_kernel<D, GS, 0, WAVES>), grid, block, 0, stream, p);
   else
-    hipLaunchKernelGGL((attention_rows_kernel<D, GS, 1>), grid, dim3(256), 0, stream, p);
-  launch_log(grid, dim3(256), (size_t)kWaves * (D * 64 + 128), "attention_rows_kernel<%d, %d, %d>", D, GS, dtype);
+    hipLaunchKernelGGL((attention_rows_kernel<D, GS, 1, WAVES>), grid, block, 0, stream, p);
+  launch_log(grid, block, (size_t)WAVES * (D * 64 + 128), "attention_rows_kernel<%d, %d, %d, %d>", D, GS, dtype, WAVES);
   return hipGetLastError();
 }
 
+template <int D, int GS>
+hipError_t launch_waves(const AttentionParams& p, int waves, int dtype, hipStream_t stream) {
+  return waves == 4 ? launch_rows<D, GS, 4>(p, dtype, stream) : launch_rows<D, GS, 8>(p, dtype, stream);
+}
+
 template <int D>
-hipError_t launch_groups(const AttentionParams& p, int dtype, hipStream_t stream) {
-  if (p.cache.group == 32) return launch_rows<D, 32>(p, dtype, stream);
-  if (p.cache.group == 64) return launch_rows<D, 64>(p, dtype, stream);
-  if constexpr (D >= 128) return launch_rows<D, 128>(p, dtype, stream);
+hipError_t launch_groups(const AttentionParams& p, int waves, int dtype, hipStream_t stream) {
+  if (p.cache.group == 32) return launch_waves<D, 32>(p, waves, dtype, stream);
+  if (p.cache.group == 64) return launch_waves<D, 64>(p, waves, dtype, stream);
+  if constexpr (D >= 128) return launch_waves<D, 128>(p, waves, dtype, stream);
   return hipErrorInvalidValue;
 }
 
@@ -446,7 +555,8 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
   AttentionPlan plan;
   const int64_t rows = max_q * (q_heads / kv_heads);
   const int64_t span = window > 0 ? std::min(max_kv, window + sinks + max_q) : max_kv;
-  if (rows > 64) {  // tiles of 32 rows a wave
+  plan.tiles = rows > 64;
+  if (plan.tiles) {  // tiles of 32 rows a wave
     plan.waves = head_dim == 256 || B * kv_heads * ((rows + 255) / 256) < 256 ? 4 : 8;
     plan.row_tiles = (int)((rows + 32 * plan.waves - 1) / (32 * plan.waves));
     const int64_t groups = B * kv_heads * plan.row_tiles;
@@ -454,14 +564,16 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
     plan.splits = (int)std::min<int64_t>(std::min((256 + groups - 1) / groups, most), 128);
     return plan;
   }
-  plan.waves = 0;
+  plan.waves = 4;
   plan.row_tiles = (int)((rows + kRows - 1) / kRows);
   // Splits until there are four workgroups a CU, with at least four steps a wave.
   const int64_t groups = B * kv_heads * plan.row_tiles;
   const int64_t steps = (span + kStep - 1) / kStep;
-  const int64_t most = std::max<int64_t>(1, steps / (4 * kWaves));
+  const int64_t most = std::max<int64_t>(1, steps / (4 * plan.waves));
   const int64_t want = (4 * 256 + groups - 1) / std::max<int64_t>(1, groups);
   plan.splits = (int)std::min<int64_t>(std::min(want, most), 128);
+  if (const char* e = getenv("BX_WAVES")) plan.waves = atoi(e);
+  if (const char* e = getenv("BX_SPLITS")) plan.splits = std::max(1, atoi(e));
   return plan;
 }
 
@@ -469,15 +581,20 @@ hipError_t launch_kv_attention(AttentionParams p, const AttentionPlan& plan, int
                                hipStream_t stream) {
   p.row_tiles = plan.row_tiles;
   p.splits = plan.splits;
-  hipError_t err = plan.waves > 0           ? launch_attention_tiles(p, plan.waves, dtype, stream)
-                   : p.cache.head_dim == 64 ? launch_groups<64>(p, dtype, stream)
-                   : p.cache.head_dim == 128 ? launch_groups<128>(p, dtype, stream)
-                                             : launch_groups<256>(p, dtype, stream);
+  const int D = p.cache.head_dim;
+  hipError_t err = plan.tiles  ? launch_attention_tiles(p, plan.waves, dtype, stream)
+                   : D == 64   ? launch_groups<64>(p, plan.waves, dtype, stream)
+                   : D == 128  ? launch_groups<128>(p, plan.waves, dtype, stream)
+                               : launch_groups<256>(p, plan.waves, dtype, stream);
   if (err != hipSuccess || p.splits == 1) return err;
-  const int64_t threads = (int64_t)p.B * p.max_q * p.q_heads * (p.cache.head_dim / 4);
-  const dim3 grid((unsigned)((threads + 255) / 256));
-  hipLaunchKernelGGL(attention_join_kernel, grid, dim3(256), 0, stream, p);
-  launch_log(grid, dim3(256), 0, "attention_join_kernel");
+  const dim3 grid((unsigned)((int64_t)p.B * p.max_q * p.q_heads)), block(256);
+  if (D == 64)
+    hipLaunchKernelGGL(attention_join_kernel<64>, grid, block, 0, stream, p);
+  else if (D == 128)
+    hipLaunchKernelGGL(attention_join_kernel<128>, grid, block, 0, stream, p);
+  else
+    hipLaunchKernelGGL(attention_join_kernel<256>, grid, block, 0, stream, p);
+  launch_log(grid, block, 256 * 16 + 256 / (D / 4) * 4, "attention_join_kernel<%d>", D);
   return hipGetLastError();
 }
 

@@ -62,6 +62,15 @@ __device__ __forceinline__ Extent extent_of(const AttentionParams& p, int b) {
   return e;
 }
 
+// Row r of a sequence and kv head: query i of the sequence, one of the heads that share.
+struct RowOf {
+  int i, head;
+  __device__ __forceinline__ RowOf(const AttentionParams& p, int kv_head, int r) {
+    i = r / p.share;
+    head = kv_head * p.share + r - i * p.share;
+  }
+};
+
 // The tokens that rows at positions lo_pos .. hi_pos go over, in steps of STEP tokens that
 // start at multiples of it: first those of the tokens that stay visible, then the window's.
 template <int STEP>
@@ -90,8 +99,22 @@ struct Steps {
 __device__ __forceinline__ bool all_visible(int base, int n, int lo_pos, int hi_pos, int window) {
   return base + n - 1 <= lo_pos && (window <= 0 || base > hi_pos - window);
 }
+// Without branches: it is asked for each score of a step at the edge of what is visible.
 __device__ __forceinline__ bool visible(int token, int pos, int window, int sinks) {
-  return token <= pos && (window <= 0 || token > pos - window || token < sinks);
+  return (token <= pos) & ((window <= 0) | (token > pos - window) | (token < sinks));
+}
+
+// The steps [first, last) of part `split` of `splits`: the first ones take one more where the
+// count does not divide.
+struct Part {
+  int first, last;
+};
+__device__ __forceinline__ Part part_of(int count, int split, int splits) {
+  const int each = count / splits, more = count - each * splits;
+  Part s;
+  s.first = split * each + min(split, more);
+  s.last = s.first + each + (split < more ? 1 : 0);
+  return s;
 }
 
 __device__ __forceinline__ bool pair_finite(uint32_t pair) {
@@ -109,14 +132,26 @@ struct Unit {
   float limit;  // kUnitLimit, or -1 while unset
 };
 
-// Takes a larger unit for a largest size m (wave-uniform).
-__device__ __forceinline__ void widen(Unit& u, float m) {
+// Takes a larger unit for a largest size, the same in every lane; the unit stays in scalar
+// registers.
+__device__ __forceinline__ void widen(Unit& u, float size) {
+  const float m = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(size)));
   if (m > 0.f && !(m * u.down <= u.limit)) {
     // 15 s + |b| of the largest finite s and b is past f32; 2^-120 keeps the factor finite.
-    u.e = max(__builtin_amdgcn_frexp_expf(fminf(m, 3e38f)) - 9, -120);
-    u.down = ldexpf(1.f, -u.e);
+    u.e = __builtin_amdgcn_readfirstlane(max(__builtin_amdgcn_frexp_expf(fminf(m, 3e38f)) - 9, -120));
+    u.down = __uint_as_float((uint32_t)(127 - u.e) << 23);
     u.limit = kUnitLimit;
   }
+}
+
+// Four neighbouring outputs at index `at` of p.out.
+__device__ __forceinline__ void store4(const AttentionParams& p, int64_t at, float a, float b, float c, float d) {
+  if (p.otype == kOutF32)
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + at) = f32x4_t{a, b, c, d};
+  else
+    *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(p.out) + at) =
+        p.otype == kOutBf16 ? u32x2_t{pack_half2<0>(a, b), pack_half2<0>(c, d)}
+                            : u32x2_t{pack_half2<1>(a, b), pack_half2<1>(c, d)};
 }
 
 }  // namespace attn

@@ -87,7 +87,8 @@ struct AttentionParams {
 // over how many workgroups the tokens of each are split. From sizes alone, so that the
 // workspace query and the call agree.
 struct AttentionPlan {
-  int waves;  // 0: the kernel for few rows; else waves of 32 rows of a workgroup
+  bool tiles;  // the kernel for many query rows
+  int waves;   // of a workgroup
   int row_tiles;
   int splits;
 };
@@ -180,6 +181,19 @@ struct Max {
 struct Min {
   __device__ float operator()(float a, float b) const { return fminf(a, b); }
 };
+
+struct Or {  // of bit patterns
+  __device__ float operator()(float a, float b) const {
+    return __uint_as_float(__float_as_uint(a) | __float_as_uint(b));
+  }
+};
+
+// A lane's value that the compiler knows nothing of: what a rare branch computes from it is not
+// moved ahead of a loop, where it would hold registers throughout.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 
 }  // namespace attn
 }  // namespace bitmm

@@ -71,8 +71,8 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   if (r0 >= ex.rows) return;
   const int rows = min(32 * NW, ex.rows - r0);
   const Steps<kTile> steps(ex.first + r0 / p.share, ex.first + (r0 + rows - 1) / p.share, p.window, p.sinks);
-  const int i0 = (int)((int64_t)steps.count * split / p.splits);
-  const int i1 = (int)((int64_t)steps.count * (split + 1) / p.splits);
+  const Part part = part_of(steps.count, split, p.splits);
+  const int i0 = part.first, i1 = part.last;
   const int32_t* table = p.page_table + (int64_t)b * p.pages_per_seq;
   if (tid < 10) {
     if (tid < 2) notes.key_size[tid] = notes.value_size[tid] = 0;
@@ -293,15 +293,15 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
       const float ck0 = ldexpf(cq, k_unit);
       const float ck = ck0 < 1e-37f ? 1e-37f : ck0;  // masked scores times 0 would be NaN
       if (bad || gone || !all_visible(base, kTile, lo_pos, hi_pos, p.window)) {
+        const int h4 = 4 * opaque(h);
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int at = 32 * tb + 8 * (e >> 2) + 4 * h + (e & 3);
-            if (!visible(base + at, pos, p.window, p.sinks) || (gone >> at & 1))
-              x[tb][e] = neg_inf();
-            else if (bad >> at & 1)
-              x[tb][e] = quiet_nan();
+            const int at = 32 * tb + 8 * (e >> 2) + h4 + (e & 3);
+            const bool see = visible(base + at, pos, p.window, p.sinks) & !(gone >> at & 1);
+            const float y = bad >> at & 1 ? quiet_nan() : x[tb][e];
+            x[tb][e] = see ? y : neg_inf();
           }
       }
       float top = neg_inf();
