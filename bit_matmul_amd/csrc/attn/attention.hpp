@@ -16,7 +16,6 @@ namespace attn {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
-constexpr float kUnitLimit = 32768.f;  // largest |scale| * 15 + |bias| in units of 2^E
 
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 __device__ __forceinline__ float quiet_nan() { return __uint_as_float(0x7FC00000u); }
@@ -124,23 +123,23 @@ __device__ __forceinline__ float pair_size(uint32_t pair) {
   return fmaf(15.f, fabsf(bf16_lo(pair)), fabsf(bf16_hi(pair)));
 }
 
-// The unit of keys or values: 2^e, and its reciprocal as a factor. Unset until tokens with a
-// nonzero magnitude have come.
+// The unit of keys or values: 2^e, its reciprocal as a factor, and the largest size that fits
+// it. Unset (nothing fits) until tokens with a nonzero magnitude have come.
 struct Unit {
-  int e;
-  float down;   // 2^-e
-  float limit;  // kUnitLimit, or -1 while unset
+  int e = 0;
+  float down = 1.f;
+  float most = -1.f;
 };
 
 // Takes a larger unit for a largest size, the same in every lane; the unit stays in scalar
 // registers.
 __device__ __forceinline__ void widen(Unit& u, float size) {
   const float m = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(size)));
-  if (m > 0.f && !(m * u.down <= u.limit)) {
+  if (m > 0.f && !(m <= u.most)) {
     // 15 s + |b| of the largest finite s and b is past f32; 2^-120 keeps the factor finite.
     u.e = __builtin_amdgcn_readfirstlane(max(__builtin_amdgcn_frexp_expf(fminf(m, 3e38f)) - 9, -120));
     u.down = __uint_as_float((uint32_t)(127 - u.e) << 23);
-    u.limit = kUnitLimit;
+    u.most = __uint_as_float((uint32_t)(127 + min(u.e + 15, 127)) << 23);  // 2^15 units
   }
 }
 

@@ -17,7 +17,7 @@ struct Cache {
   uint32_t* k_scales;  // (scale, bias) pairs: scale in the low half
   uint32_t* v_codes;
   uint32_t* v_scales;
-  int64_t num_pages;
+  int num_pages;
   int page_shift;  // log2 of the page size
   int kv_heads;
   int head_dim;

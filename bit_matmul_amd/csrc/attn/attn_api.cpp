@@ -64,7 +64,7 @@ bitmm::attn::Cache view(const bitmm_kv_cache* c) {
   v.k_scales = static_cast<uint32_t*>(c->k_scales);
   v.v_codes = static_cast<uint32_t*>(c->v_codes);
   v.v_scales = static_cast<uint32_t*>(c->v_scales);
-  v.num_pages = c->num_pages;
+  v.num_pages = (int)c->num_pages;
   v.page_shift = __builtin_ctz((unsigned)c->page_size);
   v.kv_heads = c->kv_heads;
   v.head_dim = c->head_dim;

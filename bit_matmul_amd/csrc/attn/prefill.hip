@@ -171,7 +171,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
     }
   };
 
-  Unit uk = {0, 1.f, -1.f}, uv = {0, 1.f, -1.f};  // of the tile being written
+  Unit uk, uv;  // of the tile being written
   // Whether the tile's sizes fit the units, told to the workgroup if not; tokens that are not
   // finite are marked and emptied first.
   auto measure = [&](int i, L& t) {
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
     bool odd = false;
 #pragma unroll
     for (int e = 0; e < L::PAIRS; ++e) odd = odd || !pair_finite(t.kp[e]) || !pair_finite(t.vp[e]);
-    if (__any(odd || !(ks * uk.down <= uk.limit) || !(vs * uv.down <= uv.limit))) {
+    if (__any(odd || !(ks <= uk.most) || !(vs <= uv.most))) {
       if (odd) {
         atomicOr(reinterpret_cast<unsigned long long*>(&notes.bad[i & 3]), 1ull << lt);
         ks = vs = 0.f;
