@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import sys
 
 __all__ = [
     "KVCache", "rope_frequencies", "bitmm_qk_norm_rope", "qk_norm_rope", "bitmm_kv_append",
@@ -51,71 +52,80 @@ def declare(L) -> None:
     L.bitmm_kv_attention.restype = I
 
 
-def _lib():
-    import bit_matmul_amd as bm
-    return bm.lib()
+# A small call's time is mostly its marshalling, so the checks below are written for the case in
+# which everything is right: one pass over what a call needs, and the reason looked for only when
+# something is wrong.
 
-
-def _raise(status: int, where: str):
-    import bit_matmul_amd as bm
-    raise bm.BitmmError(status, where)
+_torch_module = None
+_current_stream = None  # the current HIP stream of a device index, as an integer
 
 
 def _torch():
-    import torch
-    return torch
+    global _torch_module, _current_stream
+    if _torch_module is None:
+        import torch
+        _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _torch_module = torch
+    return _torch_module
 
 
-def _stream(stream, device):
+def _lib():
+    return sys.modules[__package__].lib()
+
+
+def _raise(status: int, where: str):
+    raise sys.modules[__package__].BitmmError(status, where)
+
+
+def _stream(stream, index):
     if stream is None:
-        stream = _torch().cuda.current_stream(device)
+        if index < 0:
+            raise ValueError("tensors must be on the GPU")
+        return _current_stream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dtype_code(t, name):
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return 0
-    if t.dtype == torch.float16:
+    if t.dtype is torch.float16:
         return 1
     raise TypeError(f"{name} must be bfloat16 or float16, got {t.dtype}")
 
 
-def _expect(t, name, dtype, shape, device):
-    """A contiguous tensor of exactly this type, shape and device."""
-    if t.dtype != dtype:
+def _expect(t, name, dtype, shape, index):
+    """The address of a contiguous tensor of exactly this type, shape and device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} is on {t.device}, not where the call's other tensors are")
 
 
-def _rows(t, name, dtype, shape, device):
+def _rows(t, name, dtype, shape, index):
     """Values between tokens of a [tokens, heads, head_dim] tensor whose heads lie side by side."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
     st = t.stride()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and st[2] == 1 and st[1] == shape[2] and shape[0] > 1:
+        return st[0]
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not where the call's other tensors are")
     if (shape[2] > 1 and st[2] != 1) or (shape[1] > 1 and st[1] != shape[2]):
         raise ValueError(f"{name}: the heads of a token must lie side by side (strides {st})")
-    return st[0] if shape[0] > 1 else max(shape[1] * shape[2], 8)
+    return st[0] if shape[0] > 1 else max(shape[1] * shape[2], 8)  # the stride of one token says nothing
 
 
-def _address(t):
-    return t.data_ptr() if t is not None and t.numel() > 0 else None
-
-
-def _status_word(status, device):
-    if status is None:
-        return None
-    _expect(status, "status", _torch().int32, (1,), device)
-    return status.data_ptr()
+def _status_word(status, index):
+    return None if status is None else _expect(status, "status", _torch().int32, (1,), index)
 
 
 class KVCache:
@@ -134,17 +144,17 @@ class KVCache:
         groups = k_scales.shape[3]
         if groups < 1 or (8 * words) % groups:
             raise ValueError(f"{groups} groups do not divide a head of {8 * words} dims")
-        dev = k_codes.device
-        for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
-            _expect(t, name, torch.int32, (pages, heads, size, words), dev)
-        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-            _expect(t, name, torch.bfloat16, (pages, heads, size, groups, 2), dev)
+        index = k_codes.get_device()
+        codes, scales = (pages, heads, size, words), (pages, heads, size, groups, 2)
+        at = [_expect(k_codes, "k_codes", torch.int32, codes, index),
+              _expect(k_scales, "k_scales", torch.bfloat16, scales, index),
+              _expect(v_codes, "v_codes", torch.int32, codes, index),
+              _expect(v_scales, "v_scales", torch.bfloat16, scales, index)]
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.num_pages, self.kv_heads, self.page_size = pages, heads, size
         self.head_dim, self.group_size = 8 * words, 8 * words // groups
-        self.device = dev
-        self.desc = _CacheDesc(_address(k_codes), _address(k_scales), _address(v_codes), _address(v_scales), pages,
-                               size, heads, self.head_dim, self.group_size)
+        self.device, self.device_index = k_codes.device, index
+        self.desc = _CacheDesc(*at, pages, size, heads, self.head_dim, self.group_size)
 
     @classmethod
     def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, group_size: int = 64, device="cuda"):
@@ -208,28 +218,29 @@ def bitmm_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out, k_o
     if one is None:
         raise ValueError("q and k are both None")
     T, _, D = one.shape
-    dev, code = one.device, _dtype_code(one, "q" if q is not None else "k")
-    args = []
-    for name, x, w, y in (("q", q, q_weight, q_out), ("k", k, k_weight, k_out)):
-        if (x is None) != (y is None):
-            raise ValueError(f"{name} and {name}_out go together")
-        heads = 0 if x is None else x.shape[1]
-        s = so = 0
-        if x is not None:
-            s = _rows(x, name, one.dtype, (T, heads, D), dev)
-            so = _rows(y, name + "_out", one.dtype, (T, heads, D), dev)
-            if w is not None:
-                _expect(w, name + "_weight", one.dtype, (D,), dev)
-        args.append((_address(x), s, _address(w) if x is not None else None, _address(y), so, heads))
-    rot = 0
-    if inv_freq is not None and inv_freq.numel():
-        rot = 2 * inv_freq.numel()
-        _expect(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev)
-        _expect(positions, "positions", torch.int32, (T,), dev)
-    (qa, qs, qw, qo, qos, hq), (ka, ks, kw, ko, kos, hk) = args
-    st = _lib().bitmm_qk_norm_rope(qa, qs, ka, ks, qw, kw, _address(positions) if rot else None,
-                                   _address(inv_freq) if rot else None, qo, qos, ko, kos, T, hq, hk, D, rot,
-                                   int(bool(interleaved)), eps, weight_offset, rope_scale, code, _stream(stream, dev))
+    dtype, index = one.dtype, one.get_device()
+    code = _dtype_code(one, "q" if q is not None else "k")
+
+    def side(name, x, weight, out):
+        """(address, stride, weight's address, output's address, its stride, heads)"""
+        if x is None or out is None:
+            if x is not out:
+                raise ValueError(f"{name} and {name}_out go together")
+            return None, 0, None, None, 0, 0
+        shape = (T, x.shape[1], D)
+        stride, out_stride = _rows(x, name, dtype, shape, index), _rows(out, name + "_out", dtype, shape, index)
+        w = None if weight is None else _expect(weight, name + "_weight", dtype, (D,), index)
+        return x.data_ptr(), stride, w, out.data_ptr(), out_stride, shape[1]
+
+    qa, qs, qw, qo, qos, hq = side("q", q, q_weight, q_out)
+    ka, ks, kw, ko, kos, hk = side("k", k, k_weight, k_out)
+    rot, freq, pos = 0, None, None
+    if inv_freq is not None and inv_freq.shape != (0,):
+        rot = 2 * inv_freq.shape[0]
+        freq = _expect(inv_freq, "inv_freq", torch.float32, (rot // 2,), index)
+        pos = _expect(positions, "positions", torch.int32, (T,), index)
+    st = _lib().bitmm_qk_norm_rope(qa, qs, ka, ks, qw, kw, pos, freq, qo, qos, ko, kos, T, hq, hk, D, rot,
+                                   1 if interleaved else 0, eps, weight_offset, rope_scale, code, _stream(stream, index))
     if st:
         _raise(st, "bitmm_qk_norm_rope")
     return q_out, k_out
@@ -237,22 +248,19 @@ def bitmm_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out, k_o
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, **options):
     """Returns (q_out, k_out), new tensors."""
-    torch = _torch()
-    fresh = [None if x is None else torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k)]
-    return bitmm_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, *fresh, **options)
+    return bitmm_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, None if q is None else q.new_empty(q.shape),
+                              None if k is None else k.new_empty(k.shape), **options)
 
 
 def bitmm_kv_append(k, v, slots, cache: KVCache, status=None, stream=None):
     """Quantizes k and v [T, kv_heads, D] into the cache's slots [T] (int64; -1 skips a token).
     `status` (optional int32 tensor of one element) is set to 1 by a slot outside the cache."""
-    dev = cache.device
+    index = cache.device_index
     shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
     code = _dtype_code(k, "k")
-    ks = _rows(k, "k", k.dtype, shape, dev)
-    vs = _rows(v, "v", k.dtype, shape, dev)
-    _expect(slots, "slots", _torch().int64, shape[:1], dev)
-    st = _lib().bitmm_kv_append(_address(k), ks, _address(v), vs, _address(slots), shape[0], cache.desc, code,
-                                _status_word(status, dev), _stream(stream, dev))
+    ks, vs = _rows(k, "k", k.dtype, shape, index), _rows(v, "v", k.dtype, shape, index)
+    st = _lib().bitmm_kv_append(k.data_ptr(), ks, v.data_ptr(), vs, _expect(slots, "slots", _torch().int64, shape[:1], index),
+                                shape[0], cache.desc, code, _status_word(status, index), _stream(stream, index))
     if st:
         _raise(st, "bitmm_kv_append")
 
@@ -260,17 +268,20 @@ def bitmm_kv_append(k, v, slots, cache: KVCache, status=None, stream=None):
 def bitmm_kv_read(cache: KVCache, slots, k_out, v_out, status=None, stream=None):
     """The keys and values held at slots [T], into k_out and v_out [T, kv_heads, D] (either may
     be None); zeros for slots of -1 and for slots outside the cache, which set `status`."""
-    dev = cache.device
+    index = cache.device_index
     shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
     one = k_out if k_out is not None else v_out
     if one is None:
         raise ValueError("k_out and v_out are both None")
     code = _dtype_code(one, "k_out" if k_out is not None else "v_out")
-    ks = _rows(k_out, "k_out", one.dtype, shape, dev) if k_out is not None else 0
-    vs = _rows(v_out, "v_out", one.dtype, shape, dev) if v_out is not None else 0
-    _expect(slots, "slots", _torch().int64, shape[:1], dev)
-    st = _lib().bitmm_kv_read(cache.desc, _address(slots), shape[0], _address(k_out), ks, _address(v_out), vs, code,
-                              _status_word(status, dev), _stream(stream, dev))
+    ka = va = None
+    ks = vs = 0
+    if k_out is not None:
+        ka, ks = k_out.data_ptr(), _rows(k_out, "k_out", one.dtype, shape, index)
+    if v_out is not None:
+        va, vs = v_out.data_ptr(), _rows(v_out, "v_out", one.dtype, shape, index)
+    st = _lib().bitmm_kv_read(cache.desc, _expect(slots, "slots", _torch().int64, shape[:1], index), shape[0], ka, ks, va,
+                              vs, code, _status_word(status, index), _stream(stream, index))
     if st:
         _raise(st, "bitmm_kv_read")
     return k_out, v_out
@@ -280,8 +291,8 @@ def kv_read(cache: KVCache, slots, dtype=None, status=None, stream=None):
     """Returns (k, v), new tensors of `dtype` (bfloat16 by default)."""
     torch = _torch()
     shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
-    fresh = [torch.empty(shape, dtype=dtype or torch.bfloat16, device=cache.device) for _ in range(2)]
-    return bitmm_kv_read(cache, slots, *fresh, status=status, stream=stream)
+    k, v = (cache.k_scales.new_empty(shape, dtype=dtype or torch.bfloat16) for _ in range(2))
+    return bitmm_kv_read(cache, slots, k, v, status=status, stream=stream)
 
 
 def bitmm_kv_attention_workspace_bytes(T, B, max_q, max_kv, q_heads, kv_heads, head_dim, window=0, sinks=0) -> int:
@@ -297,34 +308,31 @@ def bitmm_kv_attention(q, cache: KVCache, page_table, kv_lens, cu_q, out, worksp
     None; workspace: uint8 of at least bitmm_kv_attention_workspace_bytes(...), or None if that
     is 0. scale: 1 / sqrt(D) by default."""
     torch = _torch()
-    T, heads, D = q.shape
+    T, heads, D = shape = q.shape
     B = kv_lens.shape[0]
-    dev = cache.device
+    index, int32 = cache.device_index, torch.int32
     if D != cache.head_dim:
         raise ValueError(f"q has heads of {D} dims, the cache of {cache.head_dim}")
     code = _dtype_code(q, "q")
-    qs = _rows(q, "q", q.dtype, (T, heads, D), dev)
-    kinds = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
-    if out.dtype not in kinds:
+    out_code = 0 if out.dtype is torch.bfloat16 else 2 if out.dtype is torch.float16 else 1
+    if out_code == 1 and out.dtype is not torch.float32:
         raise TypeError(f"out must be bfloat16, float16 or float32, got {out.dtype}")
-    os = _rows(out, "out", out.dtype, (T, heads, D), dev)
+    q_stride, out_stride = _rows(q, "q", q.dtype, shape, index), _rows(out, "out", out.dtype, shape, index)
     if page_table.dim() != 2:
         raise ValueError("page_table must have two dims (sequences, pages)")
-    _expect(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev)
-    _expect(kv_lens, "kv_lens", torch.int32, (B,), dev)
-    _expect(cu_q, "cu_q", torch.int32, (B + 1,), dev)
-    if lse is not None:
-        _expect(lse, "lse", torch.float32, (T, heads), dev)
-    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev or
-                                  not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    st = _lib().bitmm_kv_attention(_address(q), qs, cache.desc, _address(page_table), page_table.shape[1],
-                                   _address(kv_lens), _address(cu_q), _address(out), os, _address(lse), T, B, heads,
-                                   max_q, max_kv, scale, window, sinks, code, kinds[out.dtype], _address(workspace),
-                                   workspace.numel() if workspace is not None else 0, _status_word(status, dev),
-                                   _stream(stream, dev))
+    pages = page_table.shape[1]
+    table = _expect(page_table, "page_table", int32, (B, pages), index)
+    lens, cu = _expect(kv_lens, "kv_lens", int32, (B,), index), _expect(cu_q, "cu_q", int32, (B + 1,), index)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
+    st = _lib().bitmm_kv_attention(
+        q.data_ptr(), q_stride, cache.desc, table, pages, lens, cu, out.data_ptr(), out_stride,
+        None if lse is None else _expect(lse, "lse", torch.float32, (T, heads), index), T, B, heads, max_q, max_kv,
+        1.0 / math.sqrt(D) if scale is None else scale, window, sinks, code, out_code, ws, ws_bytes,
+        _status_word(status, index), _stream(stream, index))
     if st:
         _raise(st, "bitmm_kv_attention")
     return out
@@ -334,12 +342,11 @@ def kv_attention(q, cache: KVCache, page_table, kv_lens, cu_q, *, max_q: int, ma
                  window: int = 0, sinks: int = 0, out_dtype=None, workspace=None, lse=None, status=None, stream=None):
     """Returns the output, a new tensor of q's type unless out_dtype is given. Rows of q that
     belong to no sequence are left uninitialised."""
-    torch = _torch()
-    out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    out = q.new_empty(q.shape, dtype=out_dtype) if out_dtype is not None else q.new_empty(q.shape)
     if workspace is None:
         need = bitmm_kv_attention_workspace_bytes(q.shape[0], kv_lens.shape[0], max_q, max_kv, q.shape[1],
                                                   cache.kv_heads, cache.head_dim, window, sinks)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(need, dtype=_torch().uint8)
     return bitmm_kv_attention(q, cache, page_table, kv_lens, cu_q, out, workspace, max_q=max_q, max_kv=max_kv,
                               scale=scale, window=window, sinks=sinks, lse=lse, status=status, stream=stream)

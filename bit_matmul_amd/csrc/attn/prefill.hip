@@ -41,6 +41,16 @@ struct TileLoad {
   uint32_t k[W], v[W], kp[PAIRS], vp[PAIRS];
 };
 
+// The next N LDS reads, or matrix products, in the order that the scheduler is asked for.
+template <int N>
+__device__ __forceinline__ void sched_reads() {
+  __builtin_amdgcn_sched_group_barrier(0x100, N, 0);
+}
+template <int N>
+__device__ __forceinline__ void sched_products() {
+  __builtin_amdgcn_sched_group_barrier(0x008, N, 0);
+}
+
 __device__ __forceinline__ void wait_lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
@@ -53,6 +63,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   constexpr int DB = D / 32;                  // blocks of output dims
   __shared__ __attribute__((aligned(16))) char lds[4 * SIDE];
   __shared__ TileNotes notes;
+  constexpr int V_AHEAD = 4;                  // value operands read before the first product
   static_assert(NW * 32 * ROW <= 4 * SIDE, "rows of the epilogue");
 
   int id = xcd_remap(blockIdx.x, gridDim.x);
@@ -290,6 +301,14 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
           const u32x4_t a = *reinterpret_cast<const u32x4_t*>(kb + tb * 32 * ROW + krow + (((2 * s + h) ^ kswz) << 4));
           x[tb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), q[s], x[tb], 0, 0, 0);
         }
+      // Order of the scheduler's making: AHEAD reads, then a read with each product.
+      constexpr int PRODUCTS = 2 * (D / 16), AHEAD = 6;
+      sched_reads<AHEAD>();
+      static_for<0, PRODUCTS - AHEAD>([](auto) {
+        sched_products<1>();
+        sched_reads<1>();
+      });
+      sched_products<AHEAD>();
       const float ck0 = ldexpf(cq, k_unit);
       const float ck = ck0 < 1e-37f ? 1e-37f : ck0;  // masked scores times 0 would be NaN
       if (bad || gone || !all_visible(base, kTile, lo_pos, hi_pos, p.window)) {
@@ -338,16 +357,21 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
           pr[2 * tb + (e >> 3)][e & 7] = (_Float16)y;
         }
 #pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        const char* at = vb + vrow + (((4 * d + vpiece) ^ vswz) << 4) + vhalf;
+      for (int s = 0; s < 4; ++s)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int d = 0; d < DB; ++d) {
+          const char* at = vb + vrow + (((4 * d + vpiece) ^ vswz) << 4) + vhalf;
           const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + 16 * s * ROW)));
           const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + (16 * s + 8) * ROW)));
           const u32x4_t a = {lo[0], lo[1], hi[0], hi[1]};
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), pr[s], o[d], 0, 0, 0);
         }
-      }
+      sched_reads<2 * V_AHEAD>();
+      static_for<0, 4 * DB - V_AHEAD>([](auto) {
+        sched_products<1>();
+        sched_reads<2>();
+      });
+      sched_products<V_AHEAD>();
     }
     if (i + 2 < i1) measure(i + 2, t);
     k_unit = k_next;
