@@ -131,15 +131,15 @@ struct Unit {
   float most = -1.f;
 };
 
-// Takes a larger unit for a largest size, the same in every lane; the unit stays in scalar
-// registers.
-__device__ __forceinline__ void widen(Unit& u, float size) {
+// Takes a larger unit for a largest size, the same in every lane, so that it is near 2^near units,
+// and stays until one passes 2^most. The unit stays in scalar registers.
+__device__ __forceinline__ void widen(Unit& u, float size, int near = 9, int most = 15) {
   const float m = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(size)));
   if (m > 0.f && !(m <= u.most)) {
     // 15 s + |b| of the largest finite s and b is past f32; 2^-120 keeps the factor finite.
-    u.e = __builtin_amdgcn_readfirstlane(max(__builtin_amdgcn_frexp_expf(fminf(m, 3e38f)) - 9, -120));
+    u.e = __builtin_amdgcn_readfirstlane(max(__builtin_amdgcn_frexp_expf(fminf(m, 3e38f)) - near, -120));
     u.down = __uint_as_float((uint32_t)(127 - u.e) << 23);
-    u.most = __uint_as_float((uint32_t)(127 + min(u.e + 15, 127)) << 23);  // 2^15 units
+    u.most = __uint_as_float((uint32_t)(127 + min(u.e + most, 127)) << 23);
   }
 }
 

@@ -20,7 +20,6 @@ namespace bitmm {
 namespace attn {
 namespace {
 
-constexpr int kTile = 64;  // tokens of a tile
 
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
@@ -28,14 +27,14 @@ typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
 // What workgroups tell their waves about the tiles, beside keys and values.
 struct TileNotes {
   uint32_t key_size[2], value_size[2];  // largest sizes (f32 bits) that did not fit, by tile % 2
-  uint64_t bad[4];   // tokens with a scale or bias that is not finite, by tile % 4
-  uint64_t gone[4];  // tokens on pages outside the cache
+  uint64_t bad[4][2];   // tokens with a scale or bias that is not finite, by tile % 4
+  uint64_t gone[4][2];  // tokens on pages outside the cache
 };
 
-template <int D, int GS, int NW>
+template <int D, int GS, int NW, int H>
 struct TileLoad {
   static constexpr int THREADS = 64 * NW;
-  static constexpr int TPT = THREADS / kTile;            // threads of a token
+  static constexpr int TPT = THREADS / (64 * H);         // threads of a token
   static constexpr int W = D / 8 / TPT;                  // words of a thread, of keys and values each
   static constexpr int PAIRS = (W * 8 + GS - 1) / GS;
   uint32_t k[W], v[W], kp[PAIRS], vp[PAIRS];
@@ -57,9 +56,12 @@ __device__ __forceinline__ void wait_lds_barrier() {
 
 template <int D, int GS, int DT, int NW>
 __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kernel(AttentionParams p) {
-  using L = TileLoad<D, GS, NW>;
+  // A tile is one or two halves of 64 tokens, as LDS allows: with two, waves run freely between
+  // barriers for twice as long.
+  constexpr int H = D == 256 ? 1 : 2, TILE = 64 * H;
+  using L = TileLoad<D, GS, NW, H>;
   constexpr int ROW = D * 2;                  // bytes of an LDS row
-  constexpr int SIDE = kTile * ROW;           // bytes of a tile's keys or values
+  constexpr int SIDE = TILE * ROW;           // bytes of a tile's keys or values
   constexpr int DB = D / 32;                  // blocks of output dims
   __shared__ __attribute__((aligned(16))) char lds[4 * SIDE];
   __shared__ TileNotes notes;
@@ -81,14 +83,13 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   const int r0 = rt * 32 * NW;
   if (r0 >= ex.rows) return;
   const int rows = min(32 * NW, ex.rows - r0);
-  const Steps<kTile> steps(ex.first + r0 / p.share, ex.first + (r0 + rows - 1) / p.share, p.window, p.sinks);
+  const Steps<TILE> steps(ex.first + r0 / p.share, ex.first + (r0 + rows - 1) / p.share, p.window, p.sinks);
   const Part part = part_of(steps.count, split, p.splits);
   const int i0 = part.first, i1 = part.last;
   const int32_t* table = p.page_table + (int64_t)b * p.pages_per_seq;
-  if (tid < 10) {
+  if (tid < 8) {
     if (tid < 2) notes.key_size[tid] = notes.value_size[tid] = 0;
-    if (tid >= 2 && tid < 6) notes.bad[tid - 2] = 0;
-    if (tid >= 6) notes.gone[tid - 6] = 0;
+    notes.bad[tid / 2][tid % 2] = notes.gone[tid / 2][tid % 2] = 0;
   }
 
   // This wave's rows, and this lane's.
@@ -102,10 +103,13 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   const int pos = ex.first + qi;
   const uint16_t* qrow = p.q + (int64_t)(ex.q0 + qi) * p.q_stride + (int64_t)q_head * D;
 
-  // The row as binary16, its largest magnitude in [1, 2).
+  // The row as binary16 and times the scores' scale, for keys in units of 2^k_unit, so that the
+  // products are base-2 logarithms as they stand. Where that would pass binary16's range (scores
+  // of 10^5 and more) the row is taken 2^-r fold, and its scores 2^r fold (`wide`).
   f16x8_t q[D / 16];
-  float cq;
-  {
+  float wide = 1.f;
+  bool any_wide = false;
+  auto load_query = [&](int k_unit) {
     u32x4_t raw[D / 16];
     float big = 0.f;
 #pragma unroll
@@ -118,20 +122,22 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
         big = fmaxf(big, fmaxf(fabsf(x), fabsf(y)));
       }
     }
+    const float factor = p.scale * kLog2e;
     big = across32(big, Max());
-    const int e2 = big > 0.f && big < __uint_as_float(0x7F800000u) ? __builtin_amdgcn_frexp_expf(big) - 1 : 0;
-    // The factor stays positive, so that it can wait until after the maximum.
-    cq = p.scale == 0.f ? 1.f : ldexpf(fabsf(p.scale) * kLog2e, e2);
-    const float sign = p.scale < 0.f ? -1.f : p.scale == 0.f ? 0.f : 1.f;
+    const int r = big > 0.f && big < __uint_as_float(0x7F800000u)
+                      ? max(0, __builtin_amdgcn_frexp_expf(big) + __builtin_amdgcn_frexp_expf(factor) + k_unit - 15)
+                      : 0;
+    wide = ldexpf(1.f, r);
+    any_wide = __any(r > 0);
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
       float x[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) unpack_half2<DT>(raw[s][e], x[2 * e], x[2 * e + 1]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)(sign * ldexpf(x[(e & 1) * 4 + e / 2], -e2));
+      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)ldexpf(x[(e & 1) * 4 + e / 2] * factor, k_unit - r);
     }
-  }
+  };
 
   // ---- the tile's words: token tid / TPT, words (tid % TPT) W .. --------------------------
   const int lt = tid / L::TPT, lw = (tid % L::TPT) * L::W;
@@ -141,10 +147,10 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   };
   auto load = [&](int i, int page, L& t) {
     const int at = steps.base(i) + lt;
-    const bool inside = page >= 0 && page < p.cache.num_pages;
+    const bool inside = (uint32_t)page < (uint32_t)p.cache.num_pages;
     const bool live = i < i1 && at < ex.kv && inside;
-    const int64_t row = (((int64_t)(inside ? page : 0) * p.cache.kv_heads + head) << p.cache.page_shift) +
-                        (at & ((1 << p.cache.page_shift) - 1));
+    const int64_t row = (int64_t)((uint64_t)(uint32_t)(inside ? page : 0) * (uint32_t)(p.cache.kv_heads << p.cache.page_shift)) +
+                        ((head << p.cache.page_shift) + (at & ((1 << p.cache.page_shift) - 1)));
     const uint32_t* kc = p.cache.k_codes + row * (D / 8) + lw;
     const uint32_t* vc = p.cache.v_codes + row * (D / 8) + lw;
     if constexpr (L::W == 1) {
@@ -176,7 +182,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
 #pragma unroll
       for (int e = 0; e < L::PAIRS; ++e) t.kp[e] = t.vp[e] = 0;
       if (i < i1 && at < ex.kv) {
-        atomicOr(reinterpret_cast<unsigned long long*>(&notes.gone[i & 3]), 1ull << lt);
+        atomicOr(reinterpret_cast<unsigned long long*>(&notes.gone[i & 3][lt >> 6]), 1ull << (lt & 63));
         if (p.status) *p.status = 1;
       }
     }
@@ -197,7 +203,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
     for (int e = 0; e < L::PAIRS; ++e) odd = odd || !pair_finite(t.kp[e]) || !pair_finite(t.vp[e]);
     if (__any(odd || !(ks <= uk.most) || !(vs <= uv.most))) {
       if (odd) {
-        atomicOr(reinterpret_cast<unsigned long long*>(&notes.bad[i & 3]), 1ull << lt);
+        atomicOr(reinterpret_cast<unsigned long long*>(&notes.bad[i & 3][lt >> 6]), 1ull << (lt & 63));
         ks = vs = 0.f;
 #pragma unroll
         for (int e = 0; e < L::PAIRS; ++e) {
@@ -240,7 +246,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
     expand_side(t.v, t.vp, uv.down, base + SIDE + lt * ROW, value_swz(lt));
   };
   auto read_units = [&](int i) {
-    widen(uk, __uint_as_float(notes.key_size[i & 1]));
+    widen(uk, __uint_as_float(notes.key_size[i & 1]), 3, 8);
     widen(uv, __uint_as_float(notes.value_size[i & 1]));
   };
 
@@ -250,6 +256,9 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
   float m = neg_inf(), l = 0.f;
+  f32x16_t start;  // what a score's sum starts from: -m, over `wide`
+#pragma unroll
+  for (int e = 0; e < 16; ++e) start[e] = 0.f;
   int o_unit = 0;  // exponent of the outputs' unit
 
   // Read offsets. Keys: row c of a block of 32 tokens, pieces 2 s + h. Values: see above.
@@ -259,47 +268,51 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   const int vpiece = 2 * tg + ((tm & 3) >> 1), vswz = value_swz(tm >> 2), vhalf = 8 * (tm & 1);
 
   L t;
-  int page = page_of(i0);
+  int page = 0;
   if (i0 < i1) {
+    const int page0 = page_of(i0), page1 = page_of(i0 + 1);
+    page = page_of(i0 + 2);
     __syncthreads();  // the notes are clear
-    load(i0, page, t);
-    page = page_of(i0 + 1);
+    load(i0, page0, t);
     measure(i0, t);
     __syncthreads();
     read_units(i0);
     expand(i0, t);
-    load(i0 + 1, page, t);
-    page = page_of(i0 + 2);
+    load(i0 + 1, page1, t);
     measure(i0 + 1, t);
   }
   int k_unit = uk.e, v_unit = uv.e;  // of the tile being multiplied
+  int q_unit = k_unit;
+  load_query(q_unit);
   for (int i = i0; i < i1; ++i) {
     wait_lds_barrier();
-    if (tid == 0) notes.bad[(i + 3) & 3] = notes.gone[(i + 3) & 3] = 0;
-    const char* kb = lds + (i & 1) * 2 * SIDE;
-    const char* vb = kb + SIDE;
-    const uint64_t bad = notes.bad[i & 3], gone = notes.gone[i & 3];
+    if (tid < 2) notes.bad[(i + 3) & 3][tid] = notes.gone[(i + 3) & 3][tid] = 0;
     read_units(i + 1);
     const int k_next = uk.e, v_next = uv.e;
-    if (i + 1 < i1) {
-      expand(i + 1, t);
-      load(i + 2, page, t);
-      page = page_of(i + 3);
-    }
+    expand(i + 1, t);
+    load(i + 2, page, t);
+    page = page_of(i + 3);
 
-    const int base = steps.base(i);
-    if (wave_live && base <= hi_pos) {
+#pragma unroll 1
+    for (int half = 0; half < H; ++half) {
+      const int base = steps.base(i) + 64 * half;
+      if (!wave_live || base > hi_pos) break;
+      const char* kb = lds + (i & 1) * 2 * SIDE + half * 64 * ROW;
+      const char* vb = kb + SIDE;
+      const uint64_t bad = notes.bad[i & 3][half], gone = notes.gone[i & 3][half];
+      if (k_unit != q_unit) {
+        q_unit = k_unit;
+        load_query(q_unit);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) start[e] = m == neg_inf() ? 0.f : -m / wide;
+      }
       f32x16_t x[2];
-#pragma unroll
-      for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[tb][e] = 0.f;
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
           const u32x4_t a = *reinterpret_cast<const u32x4_t*>(kb + tb * 32 * ROW + krow + (((2 * s + h) ^ kswz) << 4));
-          x[tb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), q[s], x[tb], 0, 0, 0);
+          x[tb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), q[s], s ? x[tb] : start, 0, 0, 0);
         }
       // Order of the scheduler's making: AHEAD reads, then a read with each product.
       constexpr int PRODUCTS = 2 * (D / 16), AHEAD = 6;
@@ -309,9 +322,13 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
         sched_reads<1>();
       });
       sched_products<AHEAD>();
-      const float ck0 = ldexpf(cq, k_unit);
-      const float ck = ck0 < 1e-37f ? 1e-37f : ck0;  // masked scores times 0 would be NaN
-      if (bad || gone || !all_visible(base, kTile, lo_pos, hi_pos, p.window)) {
+      if (any_wide) {
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[tb][e] *= wide;
+      }
+      if (bad || gone || !all_visible(base, 64, lo_pos, hi_pos, p.window)) {
         const int h4 = 4 * opaque(h);
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb)
@@ -323,12 +340,6 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
             x[tb][e] = see ? y : neg_inf();
           }
       }
-      float top = neg_inf();
-#pragma unroll
-      for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, x[tb][e]);
-      top = across32(top, Max()) * ck;
       if (v_unit != o_unit) {
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -336,26 +347,49 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
           for (int e = 0; e < 16; ++e) o[d][e] = ldexpf(o[d][e], o_unit - v_unit);
         o_unit = v_unit;
       }
-      if (__any(top > m + 8.f)) {
-        const float to = fmaxf(m, top);
-        const float alpha = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - to);
-        if (to > neg_inf()) m = to;
+      u32x4_t pr[4];
+      float sum = 0.f;
+      auto exponentials = [&] {
+        sum = 0.f;
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const uint32_t y = pack_half2<1>(__builtin_amdgcn_exp2f(x[tb][e]), __builtin_amdgcn_exp2f(x[tb][e + 1]));
+            // The sum is of what multiplies the values: rounded, two at a time.
+            sum = __builtin_amdgcn_fdot2(as_f16x2(y), f16x2_t{(_Float16)1.f, (_Float16)1.f}, sum, false);
+            pr[2 * tb + (e >> 3)][(e & 7) / 2] = y;
+          }
+      };
+      exponentials();
+      // The reference m of the exponents is the largest score of the first tokens seen, and need
+      // not follow the largest so far as long as no probability nears binary16's end: a sum up to
+      // 2^13 says so. Only past it is a maximum looked for.
+      if (__any(!(sum <= 8192.f) || m == neg_inf())) {
+        float top = neg_inf();
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) top = fmaxf(top, x[tb][e]);
+        top = across32(top, Max());
+        const bool first = m == neg_inf();
+        const float up = first ? (top > neg_inf() ? top : 0.f) : fmaxf(top, 0.f);
+        const float alpha = first ? 1.f : __builtin_amdgcn_exp2f(-up);
+        m = first ? (top > neg_inf() ? top : m) : m + up;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          start[e] = m == neg_inf() ? 0.f : -m / wide;
+          x[0][e] -= up;
+          x[1][e] -= up;
+        }
         l *= alpha;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[d][e] *= alpha;
+        exponentials();
       }
-      const float off = m == neg_inf() ? 0.f : m;
-      f16x8_t pr[4];
-#pragma unroll
-      for (int tb = 0; tb < 2; ++tb)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float y = __builtin_amdgcn_exp2f(fmaf(x[tb][e], ck, -off));
-          l += y;
-          pr[2 * tb + (e >> 3)][e & 7] = (_Float16)y;
-        }
+      l += sum;
 #pragma unroll
       for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -364,7 +398,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
           const u32x2_t lo = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + 16 * s * ROW)));
           const u32x2_t hi = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + (16 * s + 8) * ROW)));
           const u32x4_t a = {lo[0], lo[1], hi[0], hi[1]};
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), pr[s], o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, pr[s]), o[d], 0, 0, 0);
         }
       sched_reads<2 * V_AHEAD>();
       static_for<0, 4 * DB - V_AHEAD>([](auto) {
@@ -373,7 +407,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
       });
       sched_products<V_AHEAD>();
     }
-    if (i + 2 < i1) measure(i + 2, t);
+    measure(i + 2, t);
     k_unit = k_next;
     v_unit = v_next;
   }
@@ -452,7 +486,7 @@ hipError_t launch_tiles(const AttentionParams& p, int dtype, hipStream_t stream)
     hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 0, NW>), grid, dim3(64 * NW), 0, stream, p);
   else
     hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 1, NW>), grid, dim3(64 * NW), 0, stream, p);
-  launch_log(grid, dim3(64 * NW), (size_t)(4 * kTile * D * 2 + sizeof(TileNotes)),
+  launch_log(grid, dim3(64 * NW), (size_t)((D == 256 ? 4 : 8) * 64 * D * 2 + sizeof(TileNotes)),
              "attention_tiles_kernel<%d, %d, %d, %d>", D, GS, dtype, NW);
   return hipGetLastError();
 }
