@@ -120,13 +120,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   __shared__ float ml_lds[WAVES][2][16];
   float(*o_lds)[J * 4][64] = reinterpret_cast<float(*)[J * 4][64]>(lds);
 
-  int id = blockIdx.x;
-  const int rt = id % p.row_tiles;
-  id /= p.row_tiles;
-  const int split = id % p.splits;
-  id /= p.splits;
-  const int head = id % p.cache.kv_heads;
-  const int b = id / p.cache.kv_heads;
+  const Work work(p, blockIdx.x);
+  const int head = work.head, b = work.b;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   char* ring = lds + wave * WAVE_BYTES;
@@ -134,13 +129,13 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   uint32_t* v_pairs = k_pairs + 32 * NG;
 
   const Extent ex = extent_of(p, b);
-  const int r0 = rt * kRows;
+  const int r0 = work.row_tile * kRows;
   if (r0 >= ex.rows) return;
   const int rows = min(kRows, ex.rows - r0);
   const int lo_pos = ex.first + r0 / p.share;
   const int hi_pos = ex.first + (r0 + rows - 1) / p.share;
   const Steps<kStep> steps(lo_pos, hi_pos, p.window, p.sinks);
-  const Part part = part_of(steps.count, split, p.splits);
+  const Part part = part_of(steps.count, work.split, work.splits);
   const int i0 = part.first, i1 = part.last;
   const int32_t* table = p.page_table + (int64_t)b * p.pages_per_seq;
 
@@ -466,10 +461,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   }
   const int dim0 = (4 * g + i4) * J + j0;
   const bool speaker = g == 0 && wave == 0;
-  const RowOf out_row(p, head, opaque(r0 + n));
-  const int64_t row = (int64_t)(ex.q0 + out_row.i) * p.q_heads + out_row.head;
-  if (p.splits > 1) {
-    const int64_t at = (int64_t)split * p.T * p.q_heads + row;
+  const int row = opaque(r0 + n);
+  if (work.splits > 1) {
+    const int64_t at = part_row(p, work.split, b, head, row);
     if (speaker) {
       p.part_ml[2 * at] = mt;
       p.part_ml[2 * at + 1] = lt;
@@ -479,8 +473,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
       *reinterpret_cast<f32x4_t*>(p.part_o + at * D + dim0 + j) = f32x4_t{y[j], y[j + 1], y[j + 2], y[j + 3]};
     return;
   }
+  const RowOf out_row(p, head, row);
   const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  if (p.lse && speaker) p.lse[row] = kLn2 * (mt + __builtin_amdgcn_logf(lt));
+  if (p.lse && speaker) p.lse[(int64_t)(ex.q0 + out_row.i) * p.q_heads + out_row.head] = kLn2 * (mt + __builtin_amdgcn_logf(lt));
   const int64_t at = (int64_t)(ex.q0 + out_row.i) * p.out_stride + (int64_t)out_row.head * D + dim0;
 #pragma unroll
   for (int j = 0; j < JP; j += 4) store4(p, at + j, y[j] * inv, y[j + 1] * inv, y[j + 2] * inv, y[j + 3] * inv);
@@ -493,22 +488,20 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) 
   constexpr int TPR = D / 4, GROUPS = 256 / TPR;
   __shared__ f32x4_t sums[GROUPS][TPR];
   __shared__ float part_l[GROUPS];
-  const int64_t unit = blockIdx.x;
-  const int q_head = (int)(unit % p.q_heads);
-  const int64_t rest = unit / p.q_heads;
-  const int i = (int)(rest % p.max_q);
-  const Extent ex = extent_of(p, (int)(rest / p.max_q));
-  if (i * p.share >= ex.rows) return;
-  const int64_t row = (int64_t)(ex.q0 + i) * p.q_heads + q_head;
-  const int64_t all = (int64_t)p.T * p.q_heads;
+  const int group = blockIdx.x / p.tail_rows, r = blockIdx.x - group * p.tail_rows;
+  const int b = group / p.cache.kv_heads, head = group - b * p.cache.kv_heads;
+  const Extent ex = extent_of(p, b);
+  if (r >= ex.rows) return;
+  const int64_t row = part_row(p, 0, b, head, r);
+  const int64_t all = (int64_t)p.B * p.cache.kv_heads * p.tail_rows;
   const int lane = threadIdx.x & 63;
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   // At most 128 splits: two a lane.
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  float2 a = make_float2(neg_inf(), 0.f), b = a;
-  if (lane < p.splits) a = ml[lane * all + row];
-  if (lane + 64 < p.splits) b = ml[(lane + 64) * all + row];
-  const float mt = reduce_lanes<64>(fmaxf(a.x, b.x), Max());
+  float near = neg_inf(), far = neg_inf();
+  if (lane < p.splits) near = ml[lane * all + row].x;
+  if (lane + 64 < p.splits) far = ml[(lane + 64) * all + row].x;
+  const float mt = reduce_lanes<64>(fmaxf(near, far), Max());
   f32x4_t y = {0.f, 0.f, 0.f, 0.f};
   float lt = 0.f;
 #pragma unroll 4
@@ -535,14 +528,15 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) 
     for (int e = 0; e < 4; ++e) y[e] += sums[w][t][e];
   }
   const float inv = lt == 0.f ? 0.f : 1.f / lt;
-  if (p.lse && t == 0) p.lse[row] = kLn2 * (mt + __builtin_amdgcn_logf(lt));
-  store4(p, (int64_t)(ex.q0 + i) * p.out_stride + (int64_t)q_head * D + 4 * t, y[0] * inv, y[1] * inv, y[2] * inv,
+  const RowOf out_row(p, head, r);
+  if (p.lse && t == 0) p.lse[(int64_t)(ex.q0 + out_row.i) * p.q_heads + out_row.head] = kLn2 * (mt + __builtin_amdgcn_logf(lt));
+  store4(p, (int64_t)(ex.q0 + out_row.i) * p.out_stride + (int64_t)out_row.head * D + 4 * t, y[0] * inv, y[1] * inv, y[2] * inv,
          y[3] * inv);
 }
 
 template <int D, int GS, int WAVES>
-hipError_t launch_rows(const AttentionParams& p, int dtype, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)p.B * p.cache.kv_heads * p.row_tiles * p.splits)), block(64 * WAVES);
+hipError_t launch_rows(const AttentionParams& p, unsigned workgroups, int dtype, hipStream_t stream) {
+  const dim3 grid(workgroups), block(64 * WAVES);
   if (dtype == 0)
     hipLaunchKernelGGL((attention_rows_kernel<D, GS, 0, WAVES>), grid, block, 0, stream, p);
   else
@@ -552,15 +546,15 @@ hipError_t launch_rows(const AttentionParams& p, int dtype, hipStream_t stream) 
 }
 
 template <int D, int GS>
-hipError_t launch_waves(const AttentionParams& p, int waves, int dtype, hipStream_t stream) {
-  return waves == 4 ? launch_rows<D, GS, 4>(p, dtype, stream) : launch_rows<D, GS, 8>(p, dtype, stream);
+hipError_t launch_waves(const AttentionParams& p, unsigned workgroups, int waves, int dtype, hipStream_t stream) {
+  return waves == 4 ? launch_rows<D, GS, 4>(p, workgroups, dtype, stream) : launch_rows<D, GS, 8>(p, workgroups, dtype, stream);
 }
 
 template <int D>
-hipError_t launch_groups(const AttentionParams& p, int waves, int dtype, hipStream_t stream) {
-  if (p.cache.group == 32) return launch_waves<D, 32>(p, waves, dtype, stream);
-  if (p.cache.group == 64) return launch_waves<D, 64>(p, waves, dtype, stream);
-  if constexpr (D >= 128) return launch_waves<D, 128>(p, waves, dtype, stream);
+hipError_t launch_groups(const AttentionParams& p, unsigned workgroups, int waves, int dtype, hipStream_t stream) {
+  if (p.cache.group == 32) return launch_waves<D, 32>(p, workgroups, waves, dtype, stream);
+  if (p.cache.group == 64) return launch_waves<D, 64>(p, workgroups, waves, dtype, stream);
+  if constexpr (D >= 128) return launch_waves<D, 128>(p, workgroups, waves, dtype, stream);
   return hipErrorInvalidValue;
 }
 
@@ -568,43 +562,57 @@ hipError_t launch_groups(const AttentionParams& p, int waves, int dtype, hipStre
 
 AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q_heads,
                              int64_t kv_heads, int64_t head_dim, int64_t window, int64_t sinks) {
+  constexpr int64_t CUS = 256;
   AttentionPlan plan;
-  const int64_t rows = max_q * (q_heads / kv_heads);
+  const int64_t rows = max_q * (q_heads / kv_heads), groups = B * kv_heads;
   const int64_t span = window > 0 ? std::min(max_kv, window + sinks + max_q) : max_kv;
   plan.tiles = rows > 64;
-  if (plan.tiles) {  // tiles of 32 rows a wave
-    plan.waves = head_dim == 256 || B * kv_heads * ((rows + 255) / 256) < 256 ? 4 : 8;
-    plan.row_tiles = (int)((rows + 32 * plan.waves - 1) / (32 * plan.waves));
-    const int64_t groups = B * kv_heads * plan.row_tiles;
-    const int64_t most = std::max<int64_t>(1, span / 512);
-    plan.splits = (int)std::min<int64_t>(std::min((256 + groups - 1) / groups, most), 128);
-    return plan;
+  int64_t rows_each, fill, most;  // rows of a tile, workgroups at a time, parts of a tile's tokens
+  if (plan.tiles) {
+    plan.waves = head_dim == 256 || groups * ((rows + 255) / 256) < CUS ? 4 : 8;
+    rows_each = 32 * plan.waves;
+    fill = CUS;
+    most = std::max<int64_t>(1, span / 256);
+  } else {
+    // Few short sequences: eight waves each and no joining launch (573 tokens, 8 kv heads: 10.6 us
+    // against 7.8 + 3.5). Otherwise four waves, and splits until the workgroups fill the chip once,
+    // as many as registers and LDS let a CU hold: at twice as many the second half waits (decode
+    // of 64 sequences, head dim 256: 61 us against 50). A wave has at least one step.
+    const int64_t tiles = (rows + kRows - 1) / kRows, steps = (span + kStep - 1) / kStep;
+    plan.waves = groups * tiles <= CUS && steps <= 32 ? 8 : 4;
+    rows_each = kRows;
+    fill = plan.waves == 8 ? 1 : head_dim == 256 ? 2 * CUS : 4 * CUS;
+    most = std::max<int64_t>(1, steps / plan.waves);
   }
-  plan.row_tiles = (int)((rows + kRows - 1) / kRows);
-  const int64_t groups = B * kv_heads * plan.row_tiles;
-  const int64_t steps = (span + kStep - 1) / kStep;
-  // Few short sequences: eight waves each and no joining launch (573 tokens, 8 kv heads: 10.6 us
-  // against 7.8 + 3.5). Otherwise four waves, and splits until the workgroups fill the chip once,
-  // as many as registers and LDS let a CU hold: at twice as many the second half waits (decode of
-  // 64 sequences, head dim 256: 61 us against 50). A wave has at least one step.
-  plan.waves = groups <= 256 && steps <= 32 ? 8 : 4;
-  const int64_t fill = head_dim == 256 ? 512 : 1024;
-  const int64_t want = plan.waves == 8 ? 1 : std::max<int64_t>(1, fill / groups);
-  plan.splits = (int)std::min<int64_t>(std::min(want, std::max<int64_t>(1, steps / plan.waves)), 128);
+  plan.row_tiles = (int)((rows + rows_each - 1) / rows_each);
+  // Whole rounds of workgroups run as they are; the tiles left over for the last, partial round
+  // are split so that they fill it.
+  const int64_t whole = std::min<int64_t>(plan.row_tiles, groups * plan.row_tiles / fill * fill / groups);
+  plan.tail_tiles = (int)(plan.row_tiles - whole);
+  plan.splits = plan.tail_tiles > 0 ? (int)std::min<int64_t>({fill / (groups * plan.tail_tiles), most, 128}) : 1;
+  if (plan.splits <= 1) {
+    plan.splits = 1;
+    plan.tail_tiles = 0;
+  }
+  plan.tail_rows = (int)std::min<int64_t>(rows, plan.tail_tiles * rows_each);
   return plan;
 }
 
 hipError_t launch_kv_attention(AttentionParams p, const AttentionPlan& plan, int dtype,
                                hipStream_t stream) {
   p.row_tiles = plan.row_tiles;
+  p.tail_tiles = plan.tail_tiles;
+  p.tail_rows = plan.tail_rows;
   p.splits = plan.splits;
   const int D = p.cache.head_dim;
-  hipError_t err = plan.tiles  ? launch_attention_tiles(p, plan.waves, dtype, stream)
-                   : D == 64   ? launch_groups<64>(p, plan.waves, dtype, stream)
-                   : D == 128  ? launch_groups<128>(p, plan.waves, dtype, stream)
-                               : launch_groups<256>(p, plan.waves, dtype, stream);
-  if (err != hipSuccess || p.splits == 1) return err;
-  const dim3 grid((unsigned)((int64_t)p.B * p.max_q * p.q_heads)), block(256);
+  const int64_t groups = (int64_t)p.B * p.cache.kv_heads;
+  const unsigned n = (unsigned)plan.workgroups(groups);
+  hipError_t err = plan.tiles  ? launch_attention_tiles(p, plan.waves, n, dtype, stream)
+                   : D == 64   ? launch_groups<64>(p, n, plan.waves, dtype, stream)
+                   : D == 128  ? launch_groups<128>(p, n, plan.waves, dtype, stream)
+                               : launch_groups<256>(p, n, plan.waves, dtype, stream);
+  if (err != hipSuccess || plan.splits == 1) return err;
+  const dim3 grid((unsigned)(groups * plan.tail_rows)), block(256);
   if (D == 64)
     hipLaunchKernelGGL(attention_join_kernel<64>, grid, block, 0, stream, p);
   else if (D == 128)

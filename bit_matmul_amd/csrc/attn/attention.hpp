@@ -103,6 +103,34 @@ __device__ __forceinline__ bool visible(int token, int pos, int window, int sink
   return (token <= pos) & ((window <= 0) | (token > pos - window) | (token < sinks));
 }
 
+// A workgroup's work: a sequence and kv head, one of its row tiles, and which part of how many of
+// the tokens.
+struct Work {
+  int b, head, row_tile, split, splits;
+  __device__ __forceinline__ Work(const AttentionParams& p, int id) {
+    const int whole = p.row_tiles - p.tail_tiles, each = whole + p.tail_tiles * p.splits;
+    const int group = id / each, k = id - group * each;
+    b = group / p.cache.kv_heads;
+    head = group - b * p.cache.kv_heads;
+    if (k < whole) {  // the last rows see most: they come first
+      row_tile = p.row_tiles - 1 - k;
+      split = 0;
+      splits = 1;
+    } else {
+      const int t = (k - whole) / p.splits;
+      row_tile = p.tail_tiles - 1 - t;
+      split = k - whole - t * p.splits;
+      splits = p.splits;
+    }
+  }
+};
+
+// Row r of a sequence and kv head in a split's partial results.
+__device__ __forceinline__ int64_t part_row(const AttentionParams& p, int split, int b, int head, int r) {
+  const int64_t groups = (int64_t)p.B * p.cache.kv_heads;
+  return (split * groups + (int64_t)b * p.cache.kv_heads + head) * p.tail_rows + r;
+}
+
 // The steps [first, last) of part `split` of `splits`: the first ones take one more where the
 // count does not divide.
 struct Part {

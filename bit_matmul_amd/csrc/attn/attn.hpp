@@ -71,26 +71,30 @@ struct AttentionParams {
   const int32_t* cu_q;
   void* out;
   float* lse;
-  float* part_o;    // [splits, T * q_heads, head_dim] f32, not normalised
-  float* part_ml;   // [splits, T * q_heads, 2]: running maximum (base 2) and sum
+  float* part_o;    // [splits, B * kv_heads * tail_rows, head_dim] f32, not normalised
+  float* part_ml;   // [splits, B * kv_heads * tail_rows, 2]: reference exponent (base 2) and sum
   uint32_t* status;
   int64_t q_stride, out_stride, pages_per_seq;
   int T, B, q_heads, share;  // share: query heads of one kv head
   int max_q, max_kv;
   int window, sinks;
-  int splits, row_tiles;
+  int row_tiles, tail_tiles, tail_rows, splits;  // as in AttentionPlan
   int otype;
   float scale;
 };
 
-// How a call is cut up: which kernel, how many row tiles a sequence and kv head has, and
-// over how many workgroups the tokens of each are split. From sizes alone, so that the
-// workspace query and the call agree.
+// How a call is cut up, from sizes alone, so that the workspace query and the call agree: the
+// rows of each sequence and kv head into row tiles, a workgroup each, and the tokens that the first
+// tail_tiles of them see over `splits` workgroups each. (All of them where there are few; where
+// there are many, those that would otherwise run alone at the end.)
 struct AttentionPlan {
-  bool tiles;  // the kernel for many query rows
-  int waves;   // of a workgroup
+  bool tiles;      // the kernel for many query rows
+  int waves;       // of a workgroup
   int row_tiles;
+  int tail_tiles;  // 0 where nothing is split
+  int tail_rows;   // rows that they hold
   int splits;
+  int64_t workgroups(int64_t groups) const { return groups * (row_tiles + (int64_t)tail_tiles * (splits - 1)); }
 };
 AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q_heads,
                              int64_t kv_heads, int64_t head_dim, int64_t window, int64_t sinks);
@@ -98,7 +102,8 @@ hipError_t launch_kv_attention(AttentionParams p, const AttentionPlan& plan, int
                                hipStream_t stream);
 
 // The kernel for many query rows (prefill.hip).
-hipError_t launch_attention_tiles(const AttentionParams& p, int waves, int dtype, hipStream_t stream);
+hipError_t launch_attention_tiles(const AttentionParams& p, int waves, unsigned workgroups, int dtype,
+                                  hipStream_t stream);
 
 // ---- device helpers -------------------------------------------------------------------
 

@@ -218,7 +218,7 @@ size_t bitmm_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t max_q, i
   const AttentionPlan plan =
       bitmm::attn::plan_attention(B, max_q, max_kv, q_heads, kv_heads, head_dim, window, sinks);
   if (plan.splits == 1) return 0;
-  const size_t bytes = (size_t)plan.splits * (size_t)T * (size_t)q_heads * (size_t)(head_dim + 2) * 4;
+  const size_t bytes = (size_t)plan.splits * (size_t)(B * kv_heads) * (size_t)plan.tail_rows * (size_t)(head_dim + 2) * 4;
   return (bytes + 255) / 256 * 256;
 }
 
@@ -251,9 +251,8 @@ bitmm_status bitmm_kv_attention(const void* q, int64_t q_stride, const bitmm_kv_
     const AttentionPlan plan = bitmm::attn::plan_attention(B, max_q, max_kv, q_heads, cache->kv_heads,
                                                            cache->head_dim, window, sinks);
     // Workgroups of a launch are counted in 31 bits.
-    if (B * cache->kv_heads > INT32_MAX / plan.splits / plan.row_tiles ||
-        B * max_q > ((int64_t)INT32_MAX * 4) / q_heads)
-      return BITMM_ERR_UNSUPPORTED;
+    const int64_t groups = B * cache->kv_heads;
+    if (plan.workgroups(groups) > INT32_MAX || groups * plan.tail_rows > INT32_MAX) return BITMM_ERR_UNSUPPORTED;
     const size_t need = bitmm_kv_attention_workspace_bytes(T, B, max_q, max_kv, q_heads, cache->kv_heads,
                                                            cache->head_dim, window, sinks);
     if (need > 0 && (!workspace || workspace_bytes < need)) return BITMM_ERR_WORKSPACE;
@@ -267,7 +266,7 @@ bitmm_status bitmm_kv_attention(const void* q, int64_t q_stride, const bitmm_kv_
     p.out = out;
     p.lse = lse;
     p.part_o = static_cast<float*>(workspace);
-    p.part_ml = p.part_o ? p.part_o + (size_t)plan.splits * T * q_heads * cache->head_dim : nullptr;
+    p.part_ml = p.part_o ? p.part_o + (size_t)plan.splits * groups * plan.tail_rows * cache->head_dim : nullptr;
     p.status = status;
     p.q_stride = q_stride;
     p.out_stride = out_stride;

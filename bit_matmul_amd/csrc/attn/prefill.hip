@@ -58,7 +58,7 @@ template <int D, int GS, int DT, int NW>
 __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kernel(AttentionParams p) {
   // A tile is one or two halves of 64 tokens, as LDS allows: with two, waves run freely between
   // barriers for twice as long.
-  constexpr int H = D == 256 ? 1 : 2, TILE = 64 * H;
+  constexpr int H = D == 256 || NW == 4 ? 1 : 2, TILE = 64 * H;
   using L = TileLoad<D, GS, NW, H>;
   constexpr int ROW = D * 2;                  // bytes of an LDS row
   constexpr int SIDE = TILE * ROW;           // bytes of a tile's keys or values
@@ -68,23 +68,19 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   constexpr int V_AHEAD = 4;                  // value operands read before the first product
   static_assert(NW * 32 * ROW <= 4 * SIDE, "rows of the epilogue");
 
-  int id = xcd_remap(blockIdx.x, gridDim.x);
-  const int rt = p.row_tiles - 1 - id % p.row_tiles;  // the longest first
-  id /= p.row_tiles;
-  const int split = id % p.splits;
-  id /= p.splits;
-  const int head = id % p.cache.kv_heads;
-  const int b = id / p.cache.kv_heads;
+  // The row tiles of a sequence and kv head on one XCD: its codes meet in one L2.
+  const Work work(p, xcd_remap(blockIdx.x, gridDim.x));
+  const int head = work.head, b = work.b;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
 
   const Extent ex = extent_of(p, b);
-  const int r0 = rt * 32 * NW;
+  const int r0 = work.row_tile * 32 * NW;
   if (r0 >= ex.rows) return;
   const int rows = min(32 * NW, ex.rows - r0);
   const Steps<TILE> steps(ex.first + r0 / p.share, ex.first + (r0 + rows - 1) / p.share, p.window, p.sinks);
-  const Part part = part_of(steps.count, split, p.splits);
+  const Part part = part_of(steps.count, work.split, work.splits);
   const int i0 = part.first, i1 = part.last;
   const int32_t* table = p.page_table + (int64_t)b * p.pages_per_seq;
   if (tid < 8) {
@@ -415,12 +411,12 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   l = across32(l, Add());
   const int64_t row = (int64_t)(ex.q0 + qi) * p.q_heads + q_head;
   const bool live = wr + c < ex.rows;
-  const float out_scale = p.splits > 1 ? ldexpf(1.f, o_unit) : (l == 0.f ? 0.f : ldexpf(1.f / l, o_unit));
+  const float out_scale = work.splits > 1 ? ldexpf(1.f, o_unit) : (l == 0.f ? 0.f : ldexpf(1.f / l, o_unit));
   // Dims of a lane's registers: block d, eight dims e / 4, of which (0, 4, 1, 5) for h = 0 and
   // (2, 6, 3, 7) for h = 1, so that registers (0, 2) and (1, 3) are neighbouring dims.
-  if (p.splits > 1) {
+  if (work.splits > 1) {
     if (!live) return;
-    const int64_t at = (int64_t)split * p.T * p.q_heads + row;
+    const int64_t at = part_row(p, work.split, b, head, wr + c);
     if (h == 0) {
       p.part_ml[2 * at] = m;
       p.part_ml[2 * at + 1] = l;
@@ -480,32 +476,32 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
 }
 
 template <int D, int GS, int NW>
-hipError_t launch_tiles(const AttentionParams& p, int dtype, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)p.B * p.cache.kv_heads * p.row_tiles * p.splits));
+hipError_t launch_tiles(const AttentionParams& p, unsigned workgroups, int dtype, hipStream_t stream) {
+  const dim3 grid(workgroups);
   if (dtype == 0)
     hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 0, NW>), grid, dim3(64 * NW), 0, stream, p);
   else
     hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 1, NW>), grid, dim3(64 * NW), 0, stream, p);
-  launch_log(grid, dim3(64 * NW), (size_t)((D == 256 ? 4 : 8) * 64 * D * 2 + sizeof(TileNotes)),
+  launch_log(grid, dim3(64 * NW), (size_t)((D == 256 || NW == 4 ? 4 : 8) * 64 * D * 2 + sizeof(TileNotes)),
              "attention_tiles_kernel<%d, %d, %d, %d>", D, GS, dtype, NW);
   return hipGetLastError();
 }
 
 template <int D, int NW>
-hipError_t launch_groups(const AttentionParams& p, int dtype, hipStream_t stream) {
-  if (p.cache.group == 32) return launch_tiles<D, 32, NW>(p, dtype, stream);
-  if (p.cache.group == 64) return launch_tiles<D, 64, NW>(p, dtype, stream);
-  if constexpr (D >= 128) return launch_tiles<D, 128, NW>(p, dtype, stream);
+hipError_t launch_groups(const AttentionParams& p, unsigned workgroups, int dtype, hipStream_t stream) {
+  if (p.cache.group == 32) return launch_tiles<D, 32, NW>(p, workgroups, dtype, stream);
+  if (p.cache.group == 64) return launch_tiles<D, 64, NW>(p, workgroups, dtype, stream);
+  if constexpr (D >= 128) return launch_tiles<D, 128, NW>(p, workgroups, dtype, stream);
   return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_attention_tiles(const AttentionParams& p, int waves, int dtype, hipStream_t stream) {
-  if (p.cache.head_dim == 256) return launch_groups<256, 4>(p, dtype, stream);
+hipError_t launch_attention_tiles(const AttentionParams& p, int waves, unsigned workgroups, int dtype, hipStream_t stream) {
+  if (p.cache.head_dim == 256) return launch_groups<256, 4>(p, workgroups, dtype, stream);
   if (p.cache.head_dim == 128)
-    return waves == 8 ? launch_groups<128, 8>(p, dtype, stream) : launch_groups<128, 4>(p, dtype, stream);
-  return waves == 8 ? launch_groups<64, 8>(p, dtype, stream) : launch_groups<64, 4>(p, dtype, stream);
+    return waves == 8 ? launch_groups<128, 8>(p, workgroups, dtype, stream) : launch_groups<128, 4>(p, workgroups, dtype, stream);
+  return waves == 8 ? launch_groups<64, 8>(p, workgroups, dtype, stream) : launch_groups<64, 4>(p, workgroups, dtype, stream);
 }
 
 }  // namespace attn
