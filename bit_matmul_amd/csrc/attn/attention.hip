@@ -567,10 +567,12 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
   const int64_t rows = max_q * (q_heads / kv_heads), groups = B * kv_heads;
   const int64_t span = window > 0 ? std::min(max_kv, window + sinks + max_q) : max_kv;
   plan.tiles = rows > 64;
-  int64_t rows_each, fill, most;  // rows of a tile, workgroups at a time, parts of a tile's tokens
+  plan.waves = 0;
+  int64_t rows_each, fill, most;  // fill: workgroups at a time; most: parts of a tile's tokens
   if (plan.tiles) {
-    plan.waves = head_dim == 256 || groups * ((rows + 255) / 256) < CUS ? 4 : 8;
-    rows_each = 32 * plan.waves;
+    // 256 rows a workgroup where that still gives every CU one, else half of them, with two waves
+    // for each 32 rows (a prompt of 600 tokens, 40 heads over 8: PAIRED_US us against WHOLE_US).
+    rows_each = head_dim == 256 || groups * ((rows + 255) / 256) < CUS ? 128 : 256;
     fill = CUS;
     most = std::max<int64_t>(1, span / 256);
   } else {
@@ -584,6 +586,7 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
     fill = plan.waves == 8 ? 1 : head_dim == 256 ? 2 * CUS : 4 * CUS;
     most = std::max<int64_t>(1, steps / plan.waves);
   }
+  plan.rows_each = (int)rows_each;
   plan.row_tiles = (int)((rows + rows_each - 1) / rows_each);
   // Whole rounds of workgroups run as they are; the tiles left over for the last, partial round
   // are split so that they fill it.
@@ -607,7 +610,7 @@ hipError_t launch_kv_attention(AttentionParams p, const AttentionPlan& plan, int
   const int D = p.cache.head_dim;
   const int64_t groups = (int64_t)p.B * p.cache.kv_heads;
   const unsigned n = (unsigned)plan.workgroups(groups);
-  hipError_t err = plan.tiles  ? launch_attention_tiles(p, plan.waves, n, dtype, stream)
+  hipError_t err = plan.tiles  ? launch_attention_tiles(p, plan.rows_each, n, dtype, stream)
                    : D == 64   ? launch_groups<64>(p, n, plan.waves, dtype, stream)
                    : D == 128  ? launch_groups<128>(p, n, plan.waves, dtype, stream)
                                : launch_groups<256>(p, n, plan.waves, dtype, stream);

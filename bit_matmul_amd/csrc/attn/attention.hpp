@@ -94,10 +94,6 @@ struct Steps {
   }
 };
 
-// Whether a step of `n` tokens from base is visible to every row at lo_pos .. hi_pos.
-__device__ __forceinline__ bool all_visible(int base, int n, int lo_pos, int hi_pos, int window) {
-  return base + n - 1 <= lo_pos && (window <= 0 || base > hi_pos - window);
-}
 // Without branches: it is asked for each score of a step at the edge of what is visible.
 __device__ __forceinline__ bool visible(int token, int pos, int window, int sinks) {
   return (token <= pos) & ((window <= 0) | (token > pos - window) | (token < sinks));

@@ -89,7 +89,8 @@ struct AttentionParams {
 // there are many, those that would otherwise run alone at the end.)
 struct AttentionPlan {
   bool tiles;      // the kernel for many query rows
-  int waves;       // of a workgroup
+  int waves;       // of a workgroup, in the kernel for few rows
+  int rows_each;   // rows of a tile
   int row_tiles;
   int tail_tiles;  // 0 where nothing is split
   int tail_rows;   // rows that they hold
@@ -102,7 +103,7 @@ hipError_t launch_kv_attention(AttentionParams p, const AttentionPlan& plan, int
                                hipStream_t stream);
 
 // The kernel for many query rows (prefill.hip).
-hipError_t launch_attention_tiles(const AttentionParams& p, int waves, unsigned workgroups, int dtype,
+hipError_t launch_attention_tiles(const AttentionParams& p, int rows_each, unsigned workgroups, int dtype,
                                   hipStream_t stream);
 
 // ---- device helpers -------------------------------------------------------------------

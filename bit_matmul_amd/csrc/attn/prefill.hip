@@ -54,11 +54,14 @@ __device__ __forceinline__ void wait_lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <int D, int GS, int DT, int NW>
-__global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kernel(AttentionParams p) {
+// RW: waves that take rows of their own. Eight waves are eight row waves, or two for each of four:
+// the one takes the first 64 tokens of each tile, the other the rest, and they join at the end.
+template <int D, int GS, int DT, int NW, int RW>
+__global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(AttentionParams p) {
   // A tile is one or two halves of 64 tokens, as LDS allows: with two, waves run freely between
   // barriers for twice as long.
-  constexpr int H = D == 256 || NW == 4 ? 1 : 2, TILE = 64 * H;
+  constexpr int H = NW / 4, TILE = 64 * H;
+  constexpr bool PAIRED = RW < NW;
   using L = TileLoad<D, GS, NW, H>;
   constexpr int ROW = D * 2;                  // bytes of an LDS row
   constexpr int SIDE = TILE * ROW;           // bytes of a tile's keys or values
@@ -66,7 +69,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   __shared__ __attribute__((aligned(16))) char lds[4 * SIDE];
   __shared__ TileNotes notes;
   constexpr int V_AHEAD = 4;                  // value operands read before the first product
-  static_assert(NW * 32 * ROW <= 4 * SIDE, "rows of the epilogue");
+  static_assert(RW * 32 * ROW <= 4 * SIDE && (!PAIRED || (H == 2 && RW * (D / 2 * 256 + 512) <= 4 * SIDE)), "epilogue");
 
   // The row tiles of a sequence and kv head on one XCD: its codes meet in one L2.
   const Work work(p, xcd_remap(blockIdx.x, gridDim.x));
@@ -76,9 +79,9 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   const int c = lane & 31, h = lane >> 5;
 
   const Extent ex = extent_of(p, b);
-  const int r0 = work.row_tile * 32 * NW;
+  const int r0 = work.row_tile * 32 * RW;
   if (r0 >= ex.rows) return;
-  const int rows = min(32 * NW, ex.rows - r0);
+  const int rows = min(32 * RW, ex.rows - r0);
   const Steps<TILE> steps(ex.first + r0 / p.share, ex.first + (r0 + rows - 1) / p.share, p.window, p.sinks);
   const Part part = part_of(steps.count, work.split, work.splits);
   const int i0 = part.first, i1 = part.last;
@@ -89,15 +92,11 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   }
 
   // This wave's rows, and this lane's.
-  const int wr = r0 + 32 * wave;
+  const int wr = r0 + 32 * (wave % RW);
   const bool wave_live = wr < ex.rows;
   const int lo_pos = ex.first + min(wr, ex.rows - 1) / p.share;
   const int hi_pos = ex.first + min(wr + 31, ex.rows - 1) / p.share;
-  const int r = min(wr + c, ex.rows - 1);
-  const int qi = r / p.share;
-  const int q_head = head * p.share + r % p.share;
-  const int pos = ex.first + qi;
-  const uint16_t* qrow = p.q + (int64_t)(ex.q0 + qi) * p.q_stride + (int64_t)q_head * D;
+  const int pos = ex.first + min(wr + c, ex.rows - 1) / p.share;
 
   // The row as binary16 and times the scores' scale, for keys in units of 2^k_unit, so that the
   // products are base-2 logarithms as they stand. Where that would pass binary16's range (scores
@@ -105,16 +104,21 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   f16x8_t q[D / 16];
   float wide = 1.f;
   bool any_wide = false;
-  auto load_query = [&](int k_unit) {
-    u32x4_t raw[D / 16];
+  auto load_query = [&] {  // as it is
+    const RowOf row(p, head, opaque(min(wr + c, ex.rows - 1)));
+    const uint16_t* qrow = p.q + (int64_t)(ex.q0 + row.i) * p.q_stride + (int64_t)row.head * D;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) q[s] = __builtin_bit_cast(f16x8_t, load_u128(qrow + 16 * s + 8 * h));
+  };
+  auto convert_query = [&](int k_unit) {
     float big = 0.f;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
-      raw[s] = load_u128(qrow + 16 * s + 8 * h);
+      const u32x4_t raw = __builtin_bit_cast(u32x4_t, q[s]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float x, y;
-        unpack_half2<DT>(raw[s][e], x, y);
+        unpack_half2<DT>(raw[e], x, y);
         big = fmaxf(big, fmaxf(fabsf(x), fabsf(y)));
       }
     }
@@ -127,13 +131,15 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
     any_wide = __any(r > 0);
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
+      const u32x4_t raw = __builtin_bit_cast(u32x4_t, q[s]);
       float x[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) unpack_half2<DT>(raw[s][e], x[2 * e], x[2 * e + 1]);
+      for (int e = 0; e < 4; ++e) unpack_half2<DT>(raw[e], x[2 * e], x[2 * e + 1]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)ldexpf(x[(e & 1) * 4 + e / 2] * factor, k_unit - r);
     }
   };
+  load_query();
 
   // ---- the tile's words: token tid / TPT, words (tid % TPT) W .. --------------------------
   const int lt = tid / L::TPT, lw = (tid % L::TPT) * L::W;
@@ -279,7 +285,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   }
   int k_unit = uk.e, v_unit = uv.e;  // of the tile being multiplied
   int q_unit = k_unit;
-  load_query(q_unit);
+  convert_query(q_unit);
   for (int i = i0; i < i1; ++i) {
     wait_lds_barrier();
     if (tid < 2) notes.bad[(i + 3) & 3][tid] = notes.gone[(i + 3) & 3][tid] = 0;
@@ -290,7 +296,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
     page = page_of(i + 3);
 
 #pragma unroll 1
-    for (int half = 0; half < H; ++half) {
+    for (int half = PAIRED ? wave / RW : 0; half < (PAIRED ? wave / RW + 1 : H); ++half) {
       const int base = steps.base(i) + 64 * half;
       if (!wave_live || base > hi_pos) break;
       const char* kb = lds + (i & 1) * 2 * SIDE + half * 64 * ROW;
@@ -298,7 +304,8 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
       const uint64_t bad = notes.bad[i & 3][half], gone = notes.gone[i & 3][half];
       if (k_unit != q_unit) {
         q_unit = k_unit;
-        load_query(q_unit);
+        load_query();
+        convert_query(q_unit);
 #pragma unroll
         for (int e = 0; e < 16; ++e) start[e] = m == neg_inf() ? 0.f : -m / wide;
       }
@@ -324,16 +331,33 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
 #pragma unroll
           for (int e = 0; e < 16; ++e) x[tb][e] *= wide;
       }
-      if (bad || gone || !all_visible(base, 64, lo_pos, hi_pos, p.window)) {
+      // Score e of block tb is token 32 tb + 8 (e / 4) + 4 h + e % 4 of the half.
+      auto mask = [&](auto keep) {
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[tb][e] = keep(32 * tb + 8 * (e >> 2) + (e & 3)) ? x[tb][e] : neg_inf();
+      };
+      if (base + 63 > lo_pos) {
+        const int last = opaque(pos) - base - 4 * h;
+        mask([&](int at) { return at <= last; });
+      }
+      if (p.window > 0 && base <= hi_pos - p.window) {
+        const int before = opaque(pos) - p.window - base - 4 * h, sinks = p.sinks - base - 4 * h;
+        if (base < p.sinks)
+          mask([&](int at) { return (at > before) | (at < sinks); });
+        else
+          mask([&](int at) { return at > before; });
+      }
+      if (bad || gone) {
         const int h4 = 4 * opaque(h);
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int at = 32 * tb + 8 * (e >> 2) + h4 + (e & 3);
-            const bool see = visible(base + at, pos, p.window, p.sinks) & !(gone >> at & 1);
-            const float y = bad >> at & 1 ? quiet_nan() : x[tb][e];
-            x[tb][e] = see ? y : neg_inf();
+            const bool see = x[tb][e] != neg_inf() && !(gone >> at & 1);
+            x[tb][e] = !see ? neg_inf() : bad >> at & 1 ? quiet_nan() : x[tb][e];
           }
       }
       if (v_unit != o_unit) {
@@ -409,8 +433,34 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   }
 
   l = across32(l, Add());
-  const int64_t row = (int64_t)(ex.q0 + qi) * p.q_heads + q_head;
-  const bool live = wr + c < ex.rows;
+  if constexpr (PAIRED) {
+    // [wave of the pair's rows][register][lane], then references and sums.
+    float* part = reinterpret_cast<float*>(lds) + (wave % RW) * (D / 2 * 64 + 128) + lane;
+    __syncthreads();
+    if (wave >= RW) {
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) part[(16 * d + e) * 64] = ldexpf(o[d][e], o_unit);
+      part[D / 2 * 64] = m;
+      part[D / 2 * 64 + 64] = l;
+    }
+    __syncthreads();
+    if (wave < RW) {
+      const float m2 = part[D / 2 * 64], l2 = part[D / 2 * 64 + 64], mt = fmaxf(m, m2);
+      const float f = m == mt ? 1.f : __builtin_amdgcn_exp2f(m - mt), f2 = m2 == mt ? 1.f : __builtin_amdgcn_exp2f(m2 - mt);
+      const float own = ldexpf(f, o_unit);
+      m = mt;
+      l = l * f + l2 * f2;
+      o_unit = 0;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[d][e] = o[d][e] * own + part[(16 * d + e) * 64] * f2;
+    }
+  }
+  const RowOf mine_row(p, head, opaque(min(wr + c, ex.rows - 1)));
+  const bool live = wr + c < ex.rows && wave < RW;
   const float out_scale = work.splits > 1 ? ldexpf(1.f, o_unit) : (l == 0.f ? 0.f : ldexpf(1.f / l, o_unit));
   // Dims of a lane's registers: block d, eight dims e / 4, of which (0, 4, 1, 5) for h = 0 and
   // (2, 6, 3, 7) for h = 1, so that registers (0, 2) and (1, 3) are neighbouring dims.
@@ -431,10 +481,10 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
       }
     return;
   }
-  if (p.lse && live && h == 0) p.lse[row] = kLn2 * (m + __builtin_amdgcn_logf(l));
+  if (p.lse && live && h == 0) p.lse[(int64_t)(ex.q0 + mine_row.i) * p.q_heads + mine_row.head] = kLn2 * (m + __builtin_amdgcn_logf(l));
   if (p.otype == kOutF32) {
     if (!live) return;
-    float* to0 = static_cast<float*>(p.out) + (int64_t)(ex.q0 + qi) * p.out_stride + (int64_t)q_head * D;
+    float* to0 = static_cast<float*>(p.out) + (int64_t)(ex.q0 + mine_row.i) * p.out_stride + (int64_t)mine_row.head * D;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -448,6 +498,7 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   // 16-bit outputs go through LDS, so that a row is stored in 16-byte pieces. The wave's own
   // region: no barrier but the one that ends the tiles.
   __syncthreads();
+  if (wave >= RW) return;
   char* mine = lds + wave * 32 * ROW;
 #pragma unroll
   for (int d = 0; d < DB; ++d)
@@ -475,33 +526,36 @@ __global__ __launch_bounds__(64 * NW, NW >= 8 ? 2 : 1) void attention_tiles_kern
   }
 }
 
-template <int D, int GS, int NW>
+template <int D, int GS, int NW, int RW>
 hipError_t launch_tiles(const AttentionParams& p, unsigned workgroups, int dtype, hipStream_t stream) {
   const dim3 grid(workgroups);
   if (dtype == 0)
-    hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 0, NW>), grid, dim3(64 * NW), 0, stream, p);
+    hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 0, NW, RW>), grid, dim3(64 * NW), 0, stream, p);
   else
-    hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 1, NW>), grid, dim3(64 * NW), 0, stream, p);
-  launch_log(grid, dim3(64 * NW), (size_t)((D == 256 || NW == 4 ? 4 : 8) * 64 * D * 2 + sizeof(TileNotes)),
-             "attention_tiles_kernel<%d, %d, %d, %d>", D, GS, dtype, NW);
+    hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 1, NW, RW>), grid, dim3(64 * NW), 0, stream, p);
+  launch_log(grid, dim3(64 * NW), (size_t)(NW * 64 * D * 2 + sizeof(TileNotes)),
+             "attention_tiles_kernel<%d, %d, %d, %d, %d>", D, GS, dtype, NW, RW);
   return hipGetLastError();
 }
 
-template <int D, int NW>
+template <int D, int NW, int RW>
 hipError_t launch_groups(const AttentionParams& p, unsigned workgroups, int dtype, hipStream_t stream) {
-  if (p.cache.group == 32) return launch_tiles<D, 32, NW>(p, workgroups, dtype, stream);
-  if (p.cache.group == 64) return launch_tiles<D, 64, NW>(p, workgroups, dtype, stream);
-  if constexpr (D >= 128) return launch_tiles<D, 128, NW>(p, workgroups, dtype, stream);
+  if (p.cache.group == 32) return launch_tiles<D, 32, NW, RW>(p, workgroups, dtype, stream);
+  if (p.cache.group == 64) return launch_tiles<D, 64, NW, RW>(p, workgroups, dtype, stream);
+  if constexpr (D >= 128) return launch_tiles<D, 128, NW, RW>(p, workgroups, dtype, stream);
   return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_attention_tiles(const AttentionParams& p, int waves, unsigned workgroups, int dtype, hipStream_t stream) {
-  if (p.cache.head_dim == 256) return launch_groups<256, 4>(p, workgroups, dtype, stream);
+hipError_t launch_attention_tiles(const AttentionParams& p, int rows_each, unsigned workgroups, int dtype,
+                                  hipStream_t stream) {
+  if (p.cache.head_dim == 256) return launch_groups<256, 4, 4>(p, workgroups, dtype, stream);
   if (p.cache.head_dim == 128)
-    return waves == 8 ? launch_groups<128, 8>(p, workgroups, dtype, stream) : launch_groups<128, 4>(p, workgroups, dtype, stream);
-  return waves == 8 ? launch_groups<64, 8>(p, workgroups, dtype, stream) : launch_groups<64, 4>(p, workgroups, dtype, stream);
+    return rows_each == 256 ? launch_groups<128, 8, 8>(p, workgroups, dtype, stream)
+                            : launch_groups<128, 8, 4>(p, workgroups, dtype, stream);
+  return rows_each == 256 ? launch_groups<64, 8, 8>(p, workgroups, dtype, stream)
+                          : launch_groups<64, 8, 4>(p, workgroups, dtype, stream);
 }
 
 }  // namespace attn
