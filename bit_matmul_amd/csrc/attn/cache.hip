@@ -1,7 +1,7 @@
-// Writing and reading the 4-bit paged cache. A lane holds eight consecutive dims of a key or
-// value head: 16 bytes of activations, one word of codes. A group of dims sits on 4, 8 or 16
-// neighbouring lanes, so its minimum and maximum are DPP reductions within a row of lanes,
-// and the first lane of the group writes the (scale, bias) pair.
+// Writing and reading the 4-bit paged cache. A lane holds eight consecutive dims of a key head and
+// the same of the value head: 16 bytes of activations and one word of codes each. A group of dims
+// sits on 4, 8 or 16 neighbouring lanes, so its minimum and maximum are DPP reductions within a row
+// of lanes, and the first lane of the group writes the (scale, bias) pair.
 #include "attn.hpp"
 
 namespace bitmm {
@@ -22,30 +22,21 @@ __device__ __forceinline__ bool find_slot(const Cache& c, int64_t slot, uint32_t
   return true;
 }
 
-// Each thread's place: dims 8 l .. 8 l + 7 of head `head` of the keys (side 0) or values of
-// token `token`.
+// Each thread's place: dims 8 l .. 8 l + 7 of head `head` of token `token`.
 template <int D>
-__device__ __forceinline__ bool place(int T, int kv_heads, int& token, int& side, int& head, int& l) {
+__device__ __forceinline__ bool place(int T, int kv_heads, int& token, int& head, int& l) {
   constexpr int L = D / 8;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   l = (int)(id % L);
   const uint32_t unit = (uint32_t)(id / L);
-  token = (int)(unit / (uint32_t)(2 * kv_heads));
-  const int h = (int)(unit - (uint32_t)token * (uint32_t)(2 * kv_heads));
-  side = h >= kv_heads;
-  head = h - side * kv_heads;
+  token = (int)(unit / (uint32_t)kv_heads);
+  head = (int)(unit - (uint32_t)token * (uint32_t)kv_heads);
   return token < T;
 }
 
-template <int D, int GS, int DT>
-__global__ __launch_bounds__(256) void kv_append_kernel(AppendParams p) {
-  int token, side, head, l;
-  if (!place<D>(p.T, p.cache.kv_heads, token, side, head, l)) return;
-  int64_t row = 0;
-  if (!find_slot(p.cache, p.slots[token], p.status, row, head)) return;  // a head's lanes go together
-  const uint16_t* src = (side ? p.v + (int64_t)token * p.v_stride : p.k + (int64_t)token * p.k_stride) +
-                        (int64_t)head * D + 8 * l;
-  const u32x4_t raw = load_u128(src);
+// Codes and the pair of a lane's eight values, in a group of GS / 8 lanes.
+template <int GS, int DT>
+__device__ __forceinline__ uint32_t quantise(u32x4_t raw, uint32_t& pair) {
   float x[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) unpack_half2<DT>(raw[i], x[2 * i], x[2 * i + 1]);
@@ -59,48 +50,85 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendParams p) {
   lo = reduce_lanes<GS / 8>(lo, Min());
   hi = reduce_lanes<GS / 8>(hi, Max());
   odd = reduce_lanes<GS / 8>(odd, Add());
-  uint32_t pair = pack_bf16x2((hi - lo) / 15.f, lo);
+  pair = pack_bf16x2((hi - lo) / 15.f, lo);
   if (!(odd == 0.f)) pair = 0x7FC07FC0u;
   const float s = bf16_lo(pair), b = bf16_hi(pair);
+  if (!(s > 0.f)) return 0;
+  // A product with the reciprocal is off by less than 2^-17 of a code; where that could decide
+  // between two codes, the quotient itself does.
+  const float r = __builtin_amdgcn_rcpf(s);
   uint32_t word = 0;
-  if (s > 0.f) {
+  float edge = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // A true quotient: a product with the reciprocal would put values next to a border
-      // on the wrong side of it.
-      const float t = fminf(fmaxf(rintf((x[i] - b) / s), 0.f), 15.f);
-      word |= (uint32_t)t << (4 * i);
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float t = (x[i] - b) * r, c = rintf(t);
+    edge = fmaxf(edge, fabsf(t - c));
+    word |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * i);
   }
-  uint32_t* codes = side ? p.cache.v_codes : p.cache.k_codes;
-  uint32_t* scales = side ? p.cache.v_scales : p.cache.k_scales;
-  codes[row * (D / 8) + l] = word;
-  if (l % (GS / 8) == 0) scales[row * (D / GS) + l / (GS / 8)] = pair;
+  if (!(edge < 0.4999f)) {  // also where the reciprocal was infinite
+    word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) word |= (uint32_t)fminf(fmaxf(rintf((x[i] - b) / s), 0.f), 15.f) << (4 * i);
+  }
+  return word;
+}
+
+template <int D, int GS, int DT>
+__global__ __launch_bounds__(256) void kv_append_kernel(AppendParams p) {
+  int token, head, l;
+  if (!place<D>(p.T, p.cache.kv_heads, token, head, l)) return;
+  int64_t row = 0;
+  if (!find_slot(p.cache, p.slots[token], p.status, row, head)) return;  // a head's lanes go together
+  const u32x4_t k = load_u128(p.k + (int64_t)token * p.k_stride + (int64_t)head * D + 8 * l);
+  const u32x4_t v = load_u128(p.v + (int64_t)token * p.v_stride + (int64_t)head * D + 8 * l);
+  uint32_t k_pair, v_pair;
+  const uint32_t k_word = quantise<GS, DT>(k, k_pair), v_word = quantise<GS, DT>(v, v_pair);
+  p.cache.k_codes[row * (D / 8) + l] = k_word;
+  p.cache.v_codes[row * (D / 8) + l] = v_word;
+  if (l % (GS / 8) == 0) {
+    p.cache.k_scales[row * (D / GS) + l / (GS / 8)] = k_pair;
+    p.cache.v_scales[row * (D / GS) + l / (GS / 8)] = v_pair;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ u32x4_t expand_word(uint32_t word, uint32_t pair) {
+  const float s = bf16_lo(pair), b = bf16_hi(pair);
+  u32x4_t y;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    y[i] = pack_half2<DT>(fmaf(s, (float)((word >> (8 * i)) & 15u), b),
+                          fmaf(s, (float)((word >> (8 * i + 4)) & 15u), b));
+  return y;
 }
 
 template <int D, int GS, int DT>
 __global__ __launch_bounds__(256) void kv_read_kernel(ReadParams p) {
-  int token, side, head, l;
-  if (!place<D>(p.T, p.cache.kv_heads, token, side, head, l)) return;
-  uint16_t* out = side ? p.v_out : p.k_out;
-  if (!out) return;
+  int token, head, l;
+  if (!place<D>(p.T, p.cache.kv_heads, token, head, l)) return;
   int64_t row = 0;
-  u32x4_t y = {0, 0, 0, 0};
+  u32x4_t k = {0, 0, 0, 0}, v = k;
   if (find_slot(p.cache, p.slots[token], p.status, row, head)) {
-    const uint32_t word = (side ? p.cache.v_codes : p.cache.k_codes)[row * (D / 8) + l];
-    const uint32_t pair = (side ? p.cache.v_scales : p.cache.k_scales)[row * (D / GS) + l / (GS / 8)];
-    const float s = bf16_lo(pair), b = bf16_hi(pair);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      y[i] = pack_half2<DT>(fmaf(s, (float)((word >> (8 * i)) & 15u), b),
-                            fmaf(s, (float)((word >> (8 * i + 4)) & 15u), b));
+    const int64_t word = row * (D / 8) + l, pair = row * (D / GS) + l / (GS / 8);
+    uint32_t kw = 0, kp = 0, vw = 0, vp = 0;
+    if (p.k_out) {
+      kw = p.cache.k_codes[word];
+      kp = p.cache.k_scales[pair];
+    }
+    if (p.v_out) {
+      vw = p.cache.v_codes[word];
+      vp = p.cache.v_scales[pair];
+    }
+    k = expand_word<DT>(kw, kp);
+    v = expand_word<DT>(vw, vp);
   }
-  *reinterpret_cast<u32x4_t*>(out + (int64_t)token * (side ? p.v_stride : p.k_stride) +
-                              (int64_t)head * D + 8 * l) = y;
+  const int64_t at = (int64_t)head * D + 8 * l;
+  if (p.k_out) *reinterpret_cast<u32x4_t*>(p.k_out + (int64_t)token * p.k_stride + at) = k;
+  if (p.v_out) *reinterpret_cast<u32x4_t*>(p.v_out + (int64_t)token * p.v_stride + at) = v;
 }
 
 unsigned blocks(int T, const Cache& c) {
-  return (unsigned)(((int64_t)T * 2 * c.kv_heads * (c.head_dim / 8) + 255) / 256);
+  return (unsigned)(((int64_t)T * c.kv_heads * (c.head_dim / 8) + 255) / 256);
 }
 
 template <int D, int GS, int DT>

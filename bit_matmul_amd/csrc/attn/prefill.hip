@@ -309,6 +309,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
 #pragma unroll
         for (int e = 0; e < 16; ++e) start[e] = m == neg_inf() ? 0.f : -m / wide;
       }
+      // Between the products a wave goes first: its SIMD's other wave then has products to fill the
+      // time with (1.31 -> 1.27 ms at 4096 queries over 16384 tokens).
+      __builtin_amdgcn_s_setprio(0);
       f32x16_t x[2];
 #pragma unroll
       for (int s = 0; s < D / 16; ++s)
@@ -325,6 +328,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
         sched_reads<1>();
       });
       sched_products<AHEAD>();
+      __builtin_amdgcn_s_setprio(1);
       if (any_wide) {
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb)
@@ -410,6 +414,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
         exponentials();
       }
       l += sum;
+      __builtin_amdgcn_s_setprio(0);
 #pragma unroll
       for (int s = 0; s < 4; ++s)
 #pragma unroll

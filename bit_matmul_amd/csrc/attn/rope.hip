@@ -73,17 +73,21 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(RopeParams p) {
   load_weight(p.k_weight, wk);
 
   const int heads = p.q_heads + p.kv_heads;
+  u32x2_t next_a = {0, 0}, next_b = {0, 0};
+  auto load = [&](int h) {
+    if (h >= heads) return;
+    const uint16_t* src = h < p.q_heads ? p.q + token64 * p.q_stride + (int64_t)h * D
+                                        : p.k + token64 * p.k_stride + (int64_t)(h - p.q_heads) * D;
+    next_a = *reinterpret_cast<const u32x2_t*>(src + a);
+    next_b = *reinterpret_cast<const u32x2_t*>(src + b);
+  };
+  load(part * HPW + sub);
   for (int h0 = part * HPW; h0 < heads; h0 += p.waves_per_token * HPW) {
     const int h = h0 + sub;
     const bool live = h < heads;
     const bool is_q = h < p.q_heads;
-    const uint16_t* src = is_q ? p.q + token64 * p.q_stride + (int64_t)h * D
-                               : p.k + token64 * p.k_stride + (int64_t)(h - p.q_heads) * D;
-    u32x2_t xa = {0, 0}, xb = {0, 0};
-    if (live) {
-      xa = *reinterpret_cast<const u32x2_t*>(src + a);
-      xb = *reinterpret_cast<const u32x2_t*>(src + b);
-    }
+    const u32x2_t xa = next_a, xb = next_b;
+    load(h + p.waves_per_token * HPW);  // the next heads while these are worked on
     float x[8];
     unpack_half2<DT>(xa[0], x[0], x[1]);
     unpack_half2<DT>(xa[1], x[2], x[3]);
