@@ -79,21 +79,36 @@ __device__ __forceinline__ void load_pairs(const uint32_t* scales, const StepPla
   }
 }
 
-// Copies the codes of a side of a step to LDS, rows of D / 2 bytes one after the other.
+// Codes in LDS: rows of D / 2 bytes one after the other, and within a row the 16-byte piece w at
+// w ^ swizzle(row), so that the pieces which the rows of a product's operand are read at lie on
+// distinct banks. For heads of 256 dims, where straight rows meet on two places (decode of 64
+// sequences over windows of 1024 tokens: 50 us against 47); narrower rows meet little, and the extra arithmetic costs 1.5 %.
+template <int D>
+__device__ __forceinline__ constexpr int swizzle(int row) {
+  return D == 256 ? (row >> 1) & 7 : 0;
+}
+
+// Copies the codes of a side of a step to LDS.
 template <int D>
 __device__ __forceinline__ void copy_codes(const uint32_t* codes, const StepPlace& s, int lane, char* to) {
-  constexpr int HALF = 8 * D;  // bytes of 16 rows
-  if constexpr (D == 64) {     // one instruction's lanes hold both halves
+  constexpr int HALF = 8 * D, PIECES = D / 32;  // bytes of 16 rows, pieces of a row
+  // Source of the 16 bytes that land at place `at` of a half.
+  auto source = [](int at) {
+    const int row = at / PIECES;
+    return 16 * (row * PIECES + ((at % PIECES) ^ swizzle<D>(row)));
+  };
+  if constexpr (D == 64) {  // one instruction's lanes hold both halves
+    const int from = source(lane & 31);
     if (lane < 32)
-      dma<16>(make_rsrc(codes + s.row[0] * (D / 8), HALF), 16 * lane, to);
+      dma<16>(make_rsrc(codes + s.row[0] * (D / 8), HALF), from, to);
     else
-      dma<16>(make_rsrc(codes + s.row[1] * (D / 8), HALF), 16 * lane - HALF, to);
+      dma<16>(make_rsrc(codes + s.row[1] * (D / 8), HALF), from, to);
   } else {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const __amdgpu_buffer_rsrc_t from = make_rsrc(codes + s.row[u] * (D / 8), HALF);
 #pragma unroll
-      for (int e = 0; e < HALF; e += 1024) dma<16>(from, 16 * lane + e, to + u * HALF + e);
+      for (int e = 0; e < HALF / 1024; ++e) dma<16>(from, source(64 * e + lane), to + u * HALF + 1024 * e);
     }
   }
 }
@@ -120,24 +135,39 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   __shared__ float ml_lds[WAVES][2][16];
   float(*o_lds)[J * 4][64] = reinterpret_cast<float(*)[J * 4][64]>(lds);
 
-  const Work work(p, blockIdx.x);
-  const int head = work.head, b = work.b;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Work work(p, blockIdx.x);
+  Extent ex;
+  int part = work.split * p.B + work.b;  // of the partial results
+  if (p.balanced) {
+    const int slot = blockIdx.x / p.cache.kv_heads;
+    work.head = blockIdx.x - slot * p.cache.kv_heads;
+    const Shares shares(p, lane);
+    const Share mine = shares.of_slot(slot);
+    if (mine.b < 0) return;
+    work.b = mine.b;
+    work.split = slot - mine.first;
+    work.splits = mine.count;
+    part = slot;
+    ex = shares.extent(work.b);
+  } else {
+    ex = extent_of(p, work.b);
+  }
+  const int head = work.head;
   const int n = lane & 15, g = lane >> 4;
   char* ring = lds + wave * WAVE_BYTES;
   uint32_t* k_pairs = reinterpret_cast<uint32_t*>(ring + 4 * SIDE);
   uint32_t* v_pairs = k_pairs + 32 * NG;
 
-  const Extent ex = extent_of(p, b);
   const int r0 = work.row_tile * kRows;
   if (r0 >= ex.rows) return;
   const int rows = min(kRows, ex.rows - r0);
   const int lo_pos = ex.first + r0 / p.share;
   const int hi_pos = ex.first + (r0 + rows - 1) / p.share;
   const Steps<kStep> steps(lo_pos, hi_pos, p.window, p.sinks);
-  const Part part = part_of(steps.count, work.split, work.splits);
-  const int i0 = part.first, i1 = part.last;
-  const int32_t* table = p.page_table + (int64_t)b * p.pages_per_seq;
+  const Part range = part_of(steps.count, work.split, work.splits);
+  const int i0 = range.first, i1 = range.last;
+  const int32_t* table = p.page_table + (int64_t)work.b * p.pages_per_seq;
 
   uint32_t kp[PL], vp[PL];  // pairs of the step being copied
   StepPages pages = {};
@@ -301,18 +331,19 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
       x[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       // Row n of the product is token 4 (n % 4) + n / 4 of the half, so that a lane's four scores
       // are tokens g, 4 + g, 8 + g, 12 + g, whose values the lanes then read in one piece.
-      const char* krow = kc + u * (8 * D) + (4 * (n & 3) + (n >> 2)) * (D / 2) + g * (GS / 8);
+      const int k_row = 4 * (n & 3) + (n >> 2), k_swizzle = 16 * swizzle<D>(k_row);
+      const char* krow = kc + u * (8 * D) + k_row * (D / 2);
 #pragma unroll
       for (int y = 0; y < NG; ++y) {
         uint32_t k[WG];
         if constexpr (WG == 1) {
-          k[0] = *reinterpret_cast<const uint32_t*>(krow + y * (GS / 2));
+          k[0] = *reinterpret_cast<const uint32_t*>(krow + ((y * (GS / 2) + g * (GS / 8)) ^ k_swizzle));
         } else if constexpr (WG == 2) {
-          const u32x2_t w = *reinterpret_cast<const u32x2_t*>(krow + y * (GS / 2));
+          const u32x2_t w = *reinterpret_cast<const u32x2_t*>(krow + ((y * (GS / 2) + g * (GS / 8)) ^ k_swizzle));
           k[0] = w[0];
           k[1] = w[1];
         } else {
-          const u32x4_t w = *reinterpret_cast<const u32x4_t*>(krow + y * (GS / 2));
+          const u32x4_t w = *reinterpret_cast<const u32x4_t*>(krow + ((y * (GS / 2) + g * (GS / 8)) ^ k_swizzle));
 #pragma unroll
           for (int e = 0; e < 4; ++e) k[e] = w[e];
         }
@@ -386,7 +417,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
     uint32_t v[8][VW];
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
-      const char* at = vc + t / 4 * (8 * D) + (4 * (t % 4) + g) * (D / 2) + n * (D / 32);
+      const int row = 4 * (t % 4) + g;
+      const char* at = vc + t / 4 * (8 * D) + row * (D / 2) + ((n * (D / 32)) ^ (16 * swizzle<D>(row)));
       if constexpr (D == 64) {
         v[t][0] = *reinterpret_cast<const uint16_t*>(at);
       } else if constexpr (D == 128) {
@@ -462,8 +494,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   const int dim0 = (4 * g + i4) * J + j0;
   const bool speaker = g == 0 && wave == 0;
   const int row = opaque(r0 + n);
-  if (work.splits > 1) {
-    const int64_t at = part_row(p, work.split, b, head, row);
+  if (p.splits > 1 && (p.balanced || work.splits > 1)) {
+    const int64_t at = part_row(p, part, head, row);
     if (speaker) {
       p.part_ml[2 * at] = mt;
       p.part_ml[2 * at + 1] = lt;
@@ -490,22 +522,31 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) 
   __shared__ float part_l[GROUPS];
   const int group = blockIdx.x / p.tail_rows, r = blockIdx.x - group * p.tail_rows;
   const int b = group / p.cache.kv_heads, head = group - b * p.cache.kv_heads;
-  const Extent ex = extent_of(p, b);
-  if (r >= ex.rows) return;
-  const int64_t row = part_row(p, 0, b, head, r);
-  const int64_t all = (int64_t)p.B * p.cache.kv_heads * p.tail_rows;
   const int lane = threadIdx.x & 63;
   const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
-  // At most 128 splits: two a lane.
+  // The row's parts: every `step`-th from `first` on.
+  Extent ex;
+  int first = b, step = p.B, parts = p.splits;
+  if (p.balanced) {
+    const Shares shares(p, lane);
+    const Share mine = shares.of_sequence(b);
+    ex = shares.extent(b);
+    first = mine.first;
+    step = 1;
+    parts = mine.count;
+  } else {
+    ex = extent_of(p, b);
+  }
+  if (r >= ex.rows) return;
+  const int64_t row = part_row(p, first, head, r), all = part_row(p, step, 0, 0);
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  float near = neg_inf(), far = neg_inf();
-  if (lane < p.splits) near = ml[lane * all + row].x;
-  if (lane + 64 < p.splits) far = ml[(lane + 64) * all + row].x;
-  const float mt = reduce_lanes<64>(fmaxf(near, far), Max());
+  float mt = neg_inf();
+  for (int s = lane; s < parts; s += 64) mt = fmaxf(mt, ml[s * all + row].x);
+  mt = reduce_lanes<64>(mt, Max());
   f32x4_t y = {0.f, 0.f, 0.f, 0.f};
   float lt = 0.f;
 #pragma unroll 4
-  for (int s = grp; s < p.splits; s += GROUPS) {
+  for (int s = grp; s < parts; s += GROUPS) {
     const int64_t at = s * all + row;
     const float2 part = ml[at];
     const f32x4_t o = *reinterpret_cast<const f32x4_t*>(p.part_o + at * D + 4 * t);
@@ -541,7 +582,7 @@ hipError_t launch_rows(const AttentionParams& p, unsigned workgroups, int dtype,
     hipLaunchKernelGGL((attention_rows_kernel<D, GS, 0, WAVES>), grid, block, 0, stream, p);
   else
     hipLaunchKernelGGL((attention_rows_kernel<D, GS, 1, WAVES>), grid, block, 0, stream, p);
-  launch_log(grid, block, (size_t)WAVES * (D * 64 + 128), "attention_rows_kernel<%d, %d, %d, %d>", D, GS, dtype, WAVES);
+  launch_log(grid, block, (size_t)WAVES * (D * 64 + 256 * (D / GS) + 128), "attention_rows_kernel<%d, %d, %d, %d>", D, GS, dtype, WAVES);
   return hipGetLastError();
 }
 
@@ -597,6 +638,12 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
     plan.splits = 1;
     plan.tail_tiles = 0;
   }
+  // One row tile of each of several sequences: the workgroups are shared out by what each has to
+  // do, which the kernels find from the lengths, join included, for 2 us. 32 sequences of 512
+  // tokens but one of 32768: 120 us as equal splits, 32 so; of 1024 to 4096: 38 against 35; all of
+  // 4096: 42 against 44. A wave looks at 64 sequences, with step counts that add up in 31 bits.
+  plan.balanced = !plan.tiles && plan.row_tiles == 1 && plan.splits > 1 && B > 1 && B <= 64 &&
+                  B * (max_kv / kStep + 2) <= INT32_MAX;
   plan.tail_rows = (int)std::min<int64_t>(rows, plan.tail_tiles * rows_each);
   return plan;
 }
@@ -607,6 +654,7 @@ hipError_t launch_kv_attention(AttentionParams p, const AttentionPlan& plan, int
   p.tail_tiles = plan.tail_tiles;
   p.tail_rows = plan.tail_rows;
   p.splits = plan.splits;
+  p.balanced = plan.balanced;
   const int D = p.cache.head_dim;
   const int64_t groups = (int64_t)p.B * p.cache.kv_heads;
   const unsigned n = (unsigned)plan.workgroups(groups);

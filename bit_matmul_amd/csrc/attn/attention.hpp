@@ -45,7 +45,7 @@ struct Extent {
   int kv;     // tokens
 };
 
-__device__ __forceinline__ Extent extent_of(const AttentionParams& p, int b) {
+__device__ __forceinline__ Extent extent_of(const AttentionParams& p, int b, bool report = threadIdx.x == 0) {
   Extent e;
   const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], len = p.kv_lens[b];
   const int64_t room = p.pages_per_seq << p.cache.page_shift;
@@ -57,7 +57,7 @@ __device__ __forceinline__ Extent extent_of(const AttentionParams& p, int b) {
   e.kv = min(max(len, 0), most);
   e.rows = min(n, p.max_q) * p.share;
   e.first = e.kv - n;
-  if (p.status && (q0 != c0 || q1 != c1 || n > p.max_q || e.kv != len) && threadIdx.x == 0) *p.status = 1;
+  if (report && p.status && (q0 != c0 || q1 != c1 || n > p.max_q || e.kv != len)) *p.status = 1;
   return e;
 }
 
@@ -94,6 +94,62 @@ struct Steps {
   }
 };
 
+// A lane's value moved across; zero where none arrives.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int moved(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+
+// The balanced form: B * splits slots of workgroups shared out among up to 64 sequences so that all
+// have about as many steps. Lane b holds sequence b.
+struct Share {
+  int b, first, count;  // sequence (-1: none), its first slot and how many it has
+};
+struct Shares {
+  Extent mine;
+  int count, end;  // slots of lane b's sequence, and up to its end
+
+  __device__ __forceinline__ Shares(const AttentionParams& p, int lane) {
+    mine = lane < p.B ? extent_of(p, lane, blockIdx.x == 0) : Extent{0, 0, 0, 0};
+    int steps = 0;
+    if (mine.rows > 0) {
+      steps = Steps<32>(mine.first, mine.first + (mine.rows - 1) / p.share, p.window, p.sinks).count;
+    }
+    const int slots = p.B * p.splits;
+    auto sum = [](int v) {
+      return (int)__float_as_uint(reduce_lanes<64>(__uint_as_float((uint32_t)v), AddInt()));
+    };
+    // A last share is half full on the average; all fit for certain if each may be nearly empty.
+    // A sequence without steps still has its rows to write.
+    const int total = __builtin_amdgcn_readfirstlane(sum(steps));
+    auto shared_out = [&](int of) {
+      const int share = max(1, (total + of - 1) / of);
+      count = mine.rows > 0 ? max(1, (steps + share - 1) / share) : 0;
+      return __builtin_amdgcn_readfirstlane(sum(count)) <= slots;
+    };
+    if (!shared_out(slots - p.B / 2)) shared_out(slots - p.B);
+    end = count;
+    end += moved<0x111, 0xF>(end);  // within 16 lanes, from 1, 2, 4 and 8 before
+    end += moved<0x112, 0xF>(end);
+    end += moved<0x114, 0xF>(end);
+    end += moved<0x118, 0xF>(end);
+    end += moved<0x142, 0xA>(end);  // the 16 lanes before, then the 32
+    end += moved<0x143, 0xC>(end);
+  }
+  __device__ __forceinline__ Share of_sequence(int b) const {
+    const int n = __builtin_amdgcn_readlane(count, b);
+    return {b, __builtin_amdgcn_readlane(end, b) - n, n};
+  }
+  __device__ __forceinline__ Share of_slot(int slot) const {
+    const int b = __builtin_popcountll(__ballot(end <= slot));
+    return b < 64 ? of_sequence(b) : Share{-1, 0, 0};
+  }
+  __device__ __forceinline__ Extent extent(int b) const {
+    return {__builtin_amdgcn_readlane(mine.q0, b), __builtin_amdgcn_readlane(mine.rows, b),
+            __builtin_amdgcn_readlane(mine.first, b), __builtin_amdgcn_readlane(mine.kv, b)};
+  }
+};
+
 // Without branches: it is asked for each score of a step at the edge of what is visible.
 __device__ __forceinline__ bool visible(int token, int pos, int window, int sinks) {
   return (token <= pos) & ((window <= 0) | (token > pos - window) | (token < sinks));
@@ -121,10 +177,10 @@ struct Work {
   }
 };
 
-// Row r of a sequence and kv head in a split's partial results.
-__device__ __forceinline__ int64_t part_row(const AttentionParams& p, int split, int b, int head, int r) {
-  const int64_t groups = (int64_t)p.B * p.cache.kv_heads;
-  return (split * groups + (int64_t)b * p.cache.kv_heads + head) * p.tail_rows + r;
+// Row r of a kv head in part `part` of the partial results: parts are a split of a sequence, split
+// by split, or in the balanced form the slots of the sequences one after the other.
+__device__ __forceinline__ int64_t part_row(const AttentionParams& p, int part, int head, int r) {
+  return ((int64_t)part * p.cache.kv_heads + head) * p.tail_rows + r;
 }
 
 // The steps [first, last) of part `split` of `splits`: the first ones take one more where the

@@ -71,14 +71,15 @@ struct AttentionParams {
   const int32_t* cu_q;
   void* out;
   float* lse;
-  float* part_o;    // [splits, B * kv_heads * tail_rows, head_dim] f32, not normalised
-  float* part_ml;   // [splits, B * kv_heads * tail_rows, 2]: reference exponent (base 2) and sum
+  float* part_o;    // [splits * B, kv_heads, tail_rows, head_dim] f32, not normalised
+  float* part_ml;   // [splits * B, kv_heads, tail_rows, 2]: reference exponent (base 2) and sum
   uint32_t* status;
   int64_t q_stride, out_stride, pages_per_seq;
   int T, B, q_heads, share;  // share: query heads of one kv head
   int max_q, max_kv;
   int window, sinks;
   int row_tiles, tail_tiles, tail_rows, splits;  // as in AttentionPlan
+  bool balanced;
   int otype;
   float scale;
 };
@@ -95,6 +96,7 @@ struct AttentionPlan {
   int tail_tiles;  // 0 where nothing is split
   int tail_rows;   // rows that they hold
   int splits;
+  bool balanced;   // splits are an average: longer sequences get more, shorter ones fewer
   int64_t workgroups(int64_t groups) const { return groups * (row_tiles + (int64_t)tail_tiles * (splits - 1)); }
 };
 AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q_heads,
@@ -188,6 +190,11 @@ struct Min {
   __device__ float operator()(float a, float b) const { return fminf(a, b); }
 };
 
+struct AddInt {  // of integers
+  __device__ float operator()(float a, float b) const {
+    return __uint_as_float(__float_as_uint(a) + __float_as_uint(b));
+  }
+};
 struct Or {  // of bit patterns
   __device__ float operator()(float a, float b) const {
     return __uint_as_float(__float_as_uint(a) | __float_as_uint(b));

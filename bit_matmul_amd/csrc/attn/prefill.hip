@@ -20,7 +20,6 @@ namespace bitmm {
 namespace attn {
 namespace {
 
-
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
 
@@ -374,16 +373,18 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
       u32x4_t pr[4];
       float sum = 0.f;
       auto exponentials = [&] {
+        float odd = 0.f;
         sum = 0.f;
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            const uint32_t y = pack_half2<1>(__builtin_amdgcn_exp2f(x[tb][e]), __builtin_amdgcn_exp2f(x[tb][e + 1]));
-            // The sum is of what multiplies the values: rounded, two at a time.
-            sum = __builtin_amdgcn_fdot2(as_f16x2(y), f16x2_t{(_Float16)1.f, (_Float16)1.f}, sum, false);
-            pr[2 * tb + (e >> 3)][(e & 7) / 2] = y;
+            const float p0 = __builtin_amdgcn_exp2f(x[tb][e]), p1 = __builtin_amdgcn_exp2f(x[tb][e + 1]);
+            sum += p0;
+            odd += p1;
+            pr[2 * tb + (e >> 3)][(e & 7) / 2] = pack_half2<1>(p0, p1);
           }
+        sum += odd;
       };
       exponentials();
       // The reference m of the exponents is the largest score of the first tokens seen, and need
@@ -471,7 +472,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
   // (2, 6, 3, 7) for h = 1, so that registers (0, 2) and (1, 3) are neighbouring dims.
   if (work.splits > 1) {
     if (!live) return;
-    const int64_t at = part_row(p, work.split, b, head, wr + c);
+    const int64_t at = part_row(p, work.split * p.B + b, head, wr + c);
     if (h == 0) {
       p.part_ml[2 * at] = m;
       p.part_ml[2 * at + 1] = l;

@@ -215,7 +215,8 @@ def check(seq, out_dtype=None, scale=None, window=0, sinks=0, **kw):
     none = lse == -math.inf
     rows = rows.double().cpu()
     assert torch.equal(rows == -math.inf, none)
-    near(rows[~none], lse[~none], tol_lse[~none], "lse")
+    if not none.all():
+        near(rows[~none], lse[~none], tol_lse[~none], "lse")
     return got
 
 
@@ -258,6 +259,74 @@ def test_long(lens, hq, hk, D):
     seq = U.Sequences(lens, q_heads=hq, kv_heads=hk, head_dim=D, group=64, page=64, dtype=BF16, seed=len(lens))
     check(seq)
     check(seq, F32, window=1000, sinks=4)
+
+
+UNEVEN = {
+    "one long": [(1, 40), (1, 9000), (0, 500), (1, 0), (1, 1), (1, 700)],
+    "none": [(0, 90), (1, 0)],
+    "guesses": [(2, 5000), (1, 33), (0, 0), (2, 2), (2, 1)],
+    "64 of them": [(1, 17 * i) for i in range(63)] + [(1, 20000)],
+}
+
+
+@pytest.mark.parametrize("hq, hk, D", [(8, 1, 128), (6, 2, 256), (3, 3, 64)])
+@pytest.mark.parametrize("lens", list(UNEVEN), ids=str)
+def test_uneven_lengths(lens, hq, hk, D):
+    """Workgroups shared out by length, also to sequences without tokens or without queries."""
+    seq = U.Sequences(UNEVEN[lens], q_heads=hq, kv_heads=hk, head_dim=D, group=64, page=64, dtype=BF16, seed=3)
+    check(seq)
+    check(seq, F32, window=600, sinks=70)
+
+
+@pytest.mark.parametrize("lens, hq, hk, D, name, groups", [
+    ([(1, 300)], 2, 2, 64, "rows_kernel<64, 64, 0, 8>", 2),
+    ([(1, 300)] * 80, 4, 4, 64, "rows_kernel<64, 64, 0, 4>", 320 * 2),
+    ([(1, 300)] * 65, 2, 1, 128, "rows_kernel<128, 64, 0, 8>", 65),
+    ([(65, 100)], 1, 1, 128, "tiles_kernel<128, 64, 0, 8, 4>", 1),
+    ([(1024, 1024)], 64, 64, 64, "tiles_kernel<64, 64, 0, 8, 8>", 256),
+    ([(300, 300)] * 16, 32, 16, 64, "tiles_kernel<64, 64, 0, 8, 8>", 3 * 256),
+    ([(1, 40), (300, 301), (33, 600), (0, 5), (290, 290)] * 13, 8, 4, 128, "tiles_kernel<128, 64, 0, 8, 8>", 3 * 260),
+    ([(100, 700)] * 3, 33, 1, 256, "tiles_kernel<256, 64, 0, 4, 4>", 3 * 26 * 2),
+    ([(70, 2300), (700, 700)], 48, 6, 128, "tiles_kernel<128, 64, 0, 8, 8>", 12 * (21 + 8)),
+])
+def test_variants(lens, hq, hk, D, name, groups):
+    """Each kernel and way to split, and that the rule takes the one meant here."""
+    seq = U.Sequences(lens, q_heads=hq, kv_heads=hk, head_dim=D, group=64, page=64, dtype=BF16, seed=5)
+    attend(seq, seq.cache("cuda:0"), BF16)
+    assert bm.bitmm_last_launches()[0].startswith(f"attention_{name} grid={groups}x1 ")
+    check(seq)
+
+
+@pytest.mark.parametrize("lens", [[(1, 700), (2, 90)], [(90, 700)], [(90, 100), (70, 3000)]], ids=str)
+@pytest.mark.parametrize("D, power", [(64, 8), (128, 8), (256, 12), (128, -10)])
+def test_scores_of_millions(lens, D, power):
+    """Integer keys and queries, and scale = 2^power ln 2: a step of a score is a factor of
+    2^(2^power), so that a row is the mean of the values at its largest score, or for a negative
+    power a softmax whose exponents are exact. Both products are exact in any order: only the
+    values, the probabilities and the sums are rounded."""
+    seq = U.Sequences(lens, q_heads=4, kv_heads=2, head_dim=D, group=64, page=16, dtype=F16, seed=power)
+    codes, scale, bias = seq.sides[0]
+    seq.sides[0] = (codes, torch.ones_like(scale), torch.zeros_like(bias))
+    seq.q = torch.randint(-3, 4, seq.q.shape, generator=torch.Generator().manual_seed(D)).to(F16)
+    factor = 2.0 ** power * math.log(2.0)
+    got, lse = attend(seq, seq.cache("cuda:0"), F32, scale=factor)
+    h16, f32 = 2.0 ** -11, 2.0 ** -24
+    for b, (nq, kv) in enumerate(seq.lens):
+        r = slice(int(seq.cu[b]), int(seq.cu[b + 1]))
+        (k, _), (v, vc) = seq.tokens(0, b, kv), seq.tokens(1, b, kv)
+        see = torch.arange(kv)[None] <= torch.arange(kv - nq, kv)[:, None]
+        for h in range(4):
+            x = (seq.q[r, h].double() @ k[:, h // 2].T).masked_fill(~see, -math.inf) * factor
+            p, n = torch.softmax(x, -1), see.sum(-1, keepdim=True)
+            off = 4 * f32 * x.masked_fill(~see, 0).abs().amax(-1, keepdim=True)  # factor and exponents in f32
+            if power > 0:  # the same for scores that are the same, and nothing beside them
+                off = off * 0
+            e = torch.expm1(2 * off) + h16 + f32 * (n + 64)
+            va = v[:, h // 2].abs()
+            tol = (p @ va) * e + h16 * (p @ (va + vc[:, h // 2])) + 2.0 ** -25 * (see.double() @ va)
+            near(got[r, h], p @ v[:, h // 2], 1.01 * tol + f32 * (p @ va), f"head {h} of sequence {b}")
+            want = torch.logsumexp(x, -1)
+            near(lse[r, h], want, off[:, 0] + f32 * (n[:, 0] + 64) + 8 * f32 * want.abs(), "lse")
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
