@@ -12,6 +12,10 @@
 // Angles. position * inv_freq is formed in f64 and reduced to a fraction of a turn there: at
 // position 2^20 an f32 product is off by up to 2^-5 radians. The fraction goes to sincospi
 // in f32.
+//
+// What bounds it: HBM. 8191 tokens of 16 + 2 heads of 256 dims: 151 MB in 30.5 us, 4.95 TB/s, the
+// rate of a large copy (4.86); the heads of the next turn are loaded before the present ones are
+// finished. 8 tokens of 40 + 8 heads: 4 us, a launch and the latency of a load and a store.
 #include "attn.hpp"
 
 namespace bitmm {
