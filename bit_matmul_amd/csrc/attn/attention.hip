@@ -625,7 +625,14 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
   AttentionPlan plan;
   const int64_t rows = max_q * (q_heads / kv_heads), groups = B * kv_heads;
   const int64_t span = window > 0 ? std::min(max_kv, window + sinks + max_q) : max_kv;
-  plan.tiles = rows > 64;
+  const int64_t tiles16 = (rows + kRows - 1) / kRows, steps = (span + kStep - 1) / kStep;
+  // The kernel for few rows starts and ends sooner, and spreads over more CUs; tiles of many rows
+  // read and expand the cache once for all of them. Up to 64 rows, or 64 steps for each CU, the
+  // first (40 heads over 8 of 128 dims, by queries of a sequence: 64 after 600 tokens 11 us against
+  // 27, 300 after 600 20 against 41, 64 after 4096 33 against 35; 32 sequences of 12 after 2048 59
+  // against 56), above that the second (32 sequences of 16 after 2048: 57 us against 112; 600 of
+  // 600: 25 against 42; 160 after 4096: 47 against 65).
+  plan.tiles = rows > 64 && (double)groups * tiles16 * steps > 64 * CUS;
   plan.waves = 0;
   int64_t rows_each, fill, most;  // fill: workgroups at a time; most: parts of a tile's tokens
   if (plan.tiles) {
@@ -633,14 +640,15 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
     // for each 32 rows (a prompt of 600 tokens, 40 heads over 8: 26 us against 30).
     rows_each = head_dim == 256 || groups * ((rows + 255) / 256) < CUS ? 128 : 256;
     fill = CUS;
-    most = std::max<int64_t>(1, span / 256);
+    // Over short spans the join costs more than the split saves (300 after 600: 41 us against 25).
+    most = span < 2048 ? 1 : span / 512;
   } else {
-    // Few short sequences: eight waves each and no joining launch (573 tokens, 8 kv heads: 10.6 us
-    // against 7.8 + 3.5). Otherwise four waves, and splits until the workgroups fill the chip once,
+    // Few short sequences, as many workgroups as the chip holds at a time: eight waves each and no
+    // joining launch (573 tokens, 8 kv heads: 10.6 us against 7.8 + 3.5; 160 queries after 600
+    // tokens: 17 against 27). Otherwise four waves, and splits until the workgroups fill the chip once,
     // as many as registers and LDS let a CU hold: at twice as many the second half waits (decode
     // of 64 sequences, head dim 256: 61 us against 50). A wave has at least one step.
-    const int64_t tiles = (rows + kRows - 1) / kRows, steps = (span + kStep - 1) / kStep;
-    plan.waves = groups * tiles <= CUS && steps <= 32 ? 8 : 4;
+    plan.waves = groups * tiles16 <= (head_dim == 256 ? CUS : 2 * CUS) && steps <= 32 ? 8 : 4;
     rows_each = kRows;
     fill = plan.waves == 8 ? 1 : head_dim == 256 ? 2 * CUS : 4 * CUS;
     most = std::max<int64_t>(1, steps / plan.waves);

@@ -138,9 +138,9 @@ size_t bitmm_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t max_q, i
  * the page table is cut to them and sets *status. A token on a page outside the cache is
  * seen by nobody and sets *status. Rows of q that belong to no sequence are not written.
  * Scores, softmax and sums are f32; keys, values and probabilities enter the matrix cores
- * as binary16, in units chosen from the stored scales, and so do queries times `scale`
- * where max_q * q_heads / kv_heads > 64. How the tokens are split, and
- * with it the order of sums, follows from the arguments and all the lengths of the call.
+ * as binary16, in units chosen from the stored scales, and so do queries times `scale` in
+ * the form for many query rows. Which form runs, how the tokens are split, and with it the
+ * order of sums, follows from the arguments and all the lengths of the call.
  * `workspace`: caller-owned device memory of bitmm_kv_attention_workspace_bytes(...) bytes,
  * 16-byte aligned, no initialisation needed (NULL if that is 0); two calls that share it
  * must be ordered on one stream.

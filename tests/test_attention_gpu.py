@@ -280,14 +280,17 @@ def test_uneven_lengths(lens, hq, hk, D):
 
 @pytest.mark.parametrize("lens, hq, hk, D, name, groups", [
     ([(1, 300)], 2, 2, 64, "rows_kernel<64, 64, 0, 8>", 2),
-    ([(1, 300)] * 80, 4, 4, 64, "rows_kernel<64, 64, 0, 4>", 320 * 2),
+    ([(1, 300)] * 80, 4, 4, 64, "rows_kernel<64, 64, 0, 8>", 320),
+    ([(1, 1500)] * 65, 4, 4, 64, "rows_kernel<64, 64, 0, 4>", 260 * 3),
     ([(1, 300)] * 65, 2, 1, 128, "rows_kernel<128, 64, 0, 8>", 65),
-    ([(65, 100)], 1, 1, 128, "tiles_kernel<128, 64, 0, 8, 4>", 1),
+    ([(65, 100)], 1, 1, 128, "rows_kernel<128, 64, 0, 8>", 5),
+    ([(300, 600)] * 2, 40, 8, 128, "tiles_kernel<128, 64, 0, 8, 4>", 16 * 12),
     ([(1024, 1024)], 64, 64, 64, "tiles_kernel<64, 64, 0, 8, 8>", 256),
     ([(300, 300)] * 16, 32, 16, 64, "tiles_kernel<64, 64, 0, 8, 8>", 3 * 256),
     ([(1, 40), (300, 301), (33, 600), (0, 5), (290, 290)] * 13, 8, 4, 128, "tiles_kernel<128, 64, 0, 8, 8>", 3 * 260),
-    ([(100, 700)] * 3, 33, 1, 256, "tiles_kernel<256, 64, 0, 4, 4>", 3 * 26 * 2),
-    ([(70, 2300), (700, 700)], 48, 6, 128, "tiles_kernel<128, 64, 0, 8, 8>", 12 * (21 + 8)),
+    ([(100, 700)] * 3, 33, 1, 256, "rows_kernel<256, 64, 0, 4>", 3 * (170 + 37 * 4)),
+    ([(70, 2300)], 64, 1, 256, "tiles_kernel<256, 64, 0, 4, 4>", 35 * 4),
+    ([(70, 2300), (700, 700)], 48, 6, 128, "tiles_kernel<128, 64, 0, 8, 8>", 12 * (21 + 4)),
 ])
 def test_variants(lens, hq, hk, D, name, groups):
     """Each kernel and way to split, and that the rule takes the one meant here."""
