@@ -63,7 +63,8 @@ __device__ __forceinline__ uint32_t quantise(u32x4_t raw, uint32_t& pair) {
   const float s = bf16_lo(pair), b = bf16_hi(pair);
   if (!(s > 0.f)) return 0;
   // A product with the reciprocal is off by less than 2^-17 of a code; where that could decide
-  // between two codes, the quotient itself does.
+  // between two codes, the quotient itself does. So it does for scales below f32's normal numbers,
+  // whose reciprocal the instruction does not give.
   const float r = __builtin_amdgcn_rcpf(s);
   uint32_t word = 0;
   float edge = 0.f;
@@ -73,7 +74,7 @@ __device__ __forceinline__ uint32_t quantise(u32x4_t raw, uint32_t& pair) {
     edge = fmaxf(edge, fabsf(t - c));
     word |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * i);
   }
-  if (!(edge < 0.4999f)) {  // also where the reciprocal was infinite
+  if (edge >= 0.4999f || s < __FLT_MIN__) {
     word = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) word |= (uint32_t)fminf(fmaxf(rintf((x[i] - b) / s), 0.f), 15.f) << (4 * i);
