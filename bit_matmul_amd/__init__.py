@@ -23,6 +23,7 @@ import ctypes
 import os
 
 from . import attention as _attention
+from ._alloc import new as _new
 from .attention import *  # noqa: F401,F403
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -343,13 +344,13 @@ def bitmm_gather_qmv(x, w, scales, biases, token_idx, expert_idx, y, bits: int,
 
 def qmv(x, w, scales, biases, bits: int, out_dtype=None, stream=None):
     torch = _torch()
-    y = torch.empty((x.shape[0], w.shape[0]), dtype=out_dtype or torch.bfloat16, device=x.device)
+    y = _new(x, (x.shape[0], w.shape[0]), out_dtype or torch.bfloat16, stream)
     return bitmm_qmv(x, w, scales, biases, y, bits, stream=stream)
 
 
 def qmm(x, w, scales, biases, bits: int, out_dtype=None, stream=None):
     torch = _torch()
-    y = torch.empty((x.shape[0], w.shape[0]), dtype=out_dtype or torch.bfloat16, device=x.device)
+    y = _new(x, (x.shape[0], w.shape[0]), out_dtype or torch.bfloat16, stream)
     return bitmm_qmm(x, w, scales, biases, y, bits, stream=stream)
 
 
@@ -358,10 +359,9 @@ def gather_qmm(x, w, scales, biases, expert_idx, bits: int, out_dtype=None, work
     """Returns (y, workspace); workspace word 0 is the precondition status."""
     torch = _torch()
     B, N, E = x.shape[0], w.shape[1], w.shape[0]
-    y = torch.empty((B, N), dtype=out_dtype or torch.bfloat16, device=x.device)
+    y = _new(x, (B, N), out_dtype or torch.bfloat16, stream)
     if workspace is None:
-        workspace = torch.empty(max(bitmm_gather_qmm_workspace_bytes(B, N, E), 256),
-                                dtype=torch.uint8, device=x.device)
+        workspace = _new(x, max(bitmm_gather_qmm_workspace_bytes(B, N, E), 256), torch.uint8, stream)
     bitmm_gather_qmm(x, w, scales, biases, expert_idx, y, workspace, bits, stream=stream)
     return y, workspace
 
@@ -369,8 +369,7 @@ def gather_qmm(x, w, scales, biases, expert_idx, bits: int, out_dtype=None, work
 def gather_qmv(x, w, scales, biases, token_idx, expert_idx, bits: int, out_dtype=None,
                stream=None):
     torch = _torch()
-    y = torch.empty((expert_idx.shape[0], w.shape[1]), dtype=out_dtype or torch.bfloat16,
-                    device=x.device)
+    y = _new(x, (expert_idx.shape[0], w.shape[1]), out_dtype or torch.bfloat16, stream)
     return bitmm_gather_qmv(x, w, scales, biases, token_idx, expert_idx, y, bits, stream=stream)
 
 
@@ -379,10 +378,9 @@ def gather_qmm_indexed(x, w, scales, biases, token_idx, expert_idx, bits: int, o
     """Returns (y, workspace); workspace word 0 flags the first row with an out-of-range id."""
     torch = _torch()
     B, N, E = expert_idx.shape[0], w.shape[1], w.shape[0]
-    y = torch.empty((B, N), dtype=out_dtype or torch.bfloat16, device=x.device)
+    y = _new(x, (B, N), out_dtype or torch.bfloat16, stream)
     if workspace is None:
-        workspace = torch.empty(max(bitmm_gather_qmm_indexed_workspace_bytes(B, N, E), 256),
-                                dtype=torch.uint8, device=x.device)
+        workspace = _new(x, max(bitmm_gather_qmm_indexed_workspace_bytes(B, N, E), 256), torch.uint8, stream)
     bitmm_gather_qmm_indexed(x, w, scales, biases, token_idx, expert_idx, y, workspace, bits,
                              stream=stream)
     return y, workspace
@@ -422,12 +420,10 @@ def bitmm_gather_mm(x, w, token_idx, expert_idx, y, workspace, layout: str = "nk
 def gather_mm(x, w, token_idx, expert_idx, layout: str = "nk", out_dtype=None, workspace=None,
               stream=None):
     """Returns (y, workspace); y has x's dtype unless out_dtype is given."""
-    torch = _torch()
     B, E = expert_idx.shape[0], w.shape[0]
     N = w.shape[1] if layout == "nk" else w.shape[2]
-    y = torch.empty((B, N), dtype=out_dtype or x.dtype, device=x.device)
+    y = _new(x, (B, N), out_dtype or x.dtype, stream)
     if workspace is None:
-        workspace = torch.empty(max(bitmm_gather_mm_workspace_bytes(B, N, E), 256),
-                                dtype=torch.uint8, device=x.device)
+        workspace = _new(x, max(bitmm_gather_mm_workspace_bytes(B, N, E), 256), torch.uint8, stream)
     bitmm_gather_mm(x, w, token_idx, expert_idx, y, workspace, layout, stream=stream)
     return y, workspace

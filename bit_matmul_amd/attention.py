@@ -20,6 +20,8 @@ import ctypes
 import math
 import sys
 
+from ._alloc import new as _new
+
 __all__ = [
     "KVCache", "rope_frequencies", "bitmm_qk_norm_rope", "qk_norm_rope", "bitmm_kv_append",
     "bitmm_kv_read", "kv_read", "bitmm_kv_attention_workspace_bytes", "bitmm_kv_attention",
@@ -246,10 +248,10 @@ def bitmm_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out, k_o
     return q_out, k_out
 
 
-def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, **options):
+def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, *, stream=None, **options):
     """Returns (q_out, k_out), new tensors."""
-    return bitmm_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, None if q is None else q.new_empty(q.shape),
-                              None if k is None else k.new_empty(k.shape), **options)
+    q_out, k_out = (None if x is None else _new(x, x.shape, x.dtype, stream) for x in (q, k))
+    return bitmm_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, stream=stream, **options)
 
 
 def bitmm_kv_append(k, v, slots, cache: KVCache, status=None, stream=None):
@@ -291,7 +293,7 @@ def kv_read(cache: KVCache, slots, dtype=None, status=None, stream=None):
     """Returns (k, v), new tensors of `dtype` (bfloat16 by default)."""
     torch = _torch()
     shape = (slots.shape[0], cache.kv_heads, cache.head_dim)
-    k, v = (cache.k_scales.new_empty(shape, dtype=dtype or torch.bfloat16) for _ in range(2))
+    k, v = (_new(cache.k_scales, shape, dtype or torch.bfloat16, stream) for _ in range(2))
     return bitmm_kv_read(cache, slots, k, v, status=status, stream=stream)
 
 
@@ -342,11 +344,11 @@ def kv_attention(q, cache: KVCache, page_table, kv_lens, cu_q, *, max_q: int, ma
                  window: int = 0, sinks: int = 0, out_dtype=None, workspace=None, lse=None, status=None, stream=None):
     """Returns the output, a new tensor of q's type unless out_dtype is given. Rows of q that
     belong to no sequence are left uninitialised."""
-    out = q.new_empty(q.shape, dtype=out_dtype) if out_dtype is not None else q.new_empty(q.shape)
+    out = _new(q, q.shape, q.dtype if out_dtype is None else out_dtype, stream)
     if workspace is None:
         need = bitmm_kv_attention_workspace_bytes(q.shape[0], kv_lens.shape[0], max_q, max_kv, q.shape[1],
                                                   cache.kv_heads, cache.head_dim, window, sinks)
         if need:
-            workspace = q.new_empty(need, dtype=_torch().uint8)
+            workspace = _new(q, need, _torch().uint8, stream, returned=False)
     return bitmm_kv_attention(q, cache, page_table, kv_lens, cu_q, out, workspace, max_q=max_q, max_kv=max_kv,
                               scale=scale, window=window, sinks=sinks, lse=lse, status=status, stream=stream)

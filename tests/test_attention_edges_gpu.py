@@ -43,3 +43,70 @@ def test_append_of_tiny_groups(spread, group):
         pairs = scales.cpu()[0, :, :9].transpose(0, 1).double()
         assert torch.equal(pairs[..., 0], s) and torch.equal(pairs[..., 1], b)
         assert torch.equal(codes.cpu()[0, :, :9].transpose(0, 1), U.pack(c))
+
+
+# ---------------------------------------------------------------------------
+# streams
+# ---------------------------------------------------------------------------
+
+def test_memory_of_a_call_on_another_stream(monkeypatch):
+    """What a form allocates for a call on `stream` is not handed to the current stream when it is dropped
+    (the call may still be at work on it), nor taken from what the current stream has dropped."""
+    seq = U.Sequences([(1, 9000), (1, 4001)], q_heads=8, kv_heads=2, head_dim=128, group=64, page=64, dtype=BF16)
+    cache = seq.cache("cuda:0")
+    t = [dev(x) for x in (seq.q, seq.table, seq.kv_lens, seq.cu)]
+    at = []
+    inner = bm.attention.bitmm_kv_attention
+
+    def noting(*args, **kw):
+        at.append(args[6].data_ptr())
+        return inner(*args, **kw)
+
+    monkeypatch.setattr(bm.attention, "bitmm_kv_attention", noting)
+    need = bm.bitmm_kv_attention_workspace_bytes(2, 2, 1, 9000, 8, 2, 128)
+    assert need > 0
+    good = bm.kv_attention(t[0], cache, t[1], t[2], t[3], max_q=1, max_kv=9000)
+    slots = torch.arange(70, device="cuda:0")
+    freq = dev(bm.rope_frequencies(128)[0])
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        at.clear()
+        dropped = [torch.empty(need, dtype=torch.uint8, device="cuda:0") for _ in range(4)]
+        before = [x.data_ptr() for x in dropped]
+        del dropped
+        side.wait_stream(torch.cuda.current_stream())
+        y = bm.kv_attention(t[0], cache, t[1], t[2], t[3], max_q=1, max_kv=9000, stream=stream)
+        after = [torch.empty(need, dtype=torch.uint8, device="cuda:0") for _ in range(4)]
+        assert len(at) == 1 and at[0] not in before and at[0] not in [x.data_ptr() for x in after]
+        for make in (lambda: bm.kv_attention(t[0], cache, t[1], t[2], t[3], max_q=1, max_kv=9000, stream=stream),
+                     lambda: bm.kv_read(cache, slots, stream=stream)[0],
+                     lambda: bm.qk_norm_rope(t[0], None, None, None, t[2], freq, stream=stream)[0]):
+            x = make()
+            shape, dtype, p = x.shape, x.dtype, x.data_ptr()
+            del x
+            assert p not in [torch.empty(shape, dtype=dtype, device="cuda:0").data_ptr() for _ in range(4)]
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(y, good)
+        side.synchronize()
+
+
+def test_memory_of_a_product_on_another_stream():
+    x = torch.randn(600, 512, device="cuda:0").to(BF16)
+    w = torch.randint(-2 ** 31, 2 ** 31, (256, 64), device="cuda:0").to(torch.int32)
+    s, b = (torch.rand(256, 8, device="cuda:0").to(BF16) for _ in range(2))
+    side = torch.cuda.Stream()
+    good = bm.qmm(x, w, s, b, 4)
+    side.wait_stream(torch.cuda.current_stream())
+    y = bm.qmm(x, w, s, b, 4, stream=side)
+    z = bm.qmm(x, w, s, b, 4, stream=side)
+    p = z.data_ptr()
+    del z
+    assert p not in [torch.empty_like(good).data_ptr() for _ in range(4)]
+    ids = torch.zeros(600, dtype=torch.int32, device="cuda:0")
+    side.wait_stream(torch.cuda.current_stream())
+    z, ws = bm.gather_qmm(x, w[None], s[None], b[None], ids, 4, stream=side)
+    p, size = ws.data_ptr(), ws.numel()
+    del ws
+    assert p not in [torch.empty(size, dtype=torch.uint8, device="cuda:0").data_ptr() for _ in range(4)]
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, good) and (z.float() - good.float()).norm() <= 2.0 ** -7 * good.float().norm()
