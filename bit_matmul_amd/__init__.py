@@ -420,6 +420,7 @@ def bitmm_gather_mm(x, w, token_idx, expert_idx, y, workspace, layout: str = "nk
 def gather_mm(x, w, token_idx, expert_idx, layout: str = "nk", out_dtype=None, workspace=None,
               stream=None):
     """Returns (y, workspace); y has x's dtype unless out_dtype is given."""
+    torch = _torch()
     B, E = expert_idx.shape[0], w.shape[0]
     N = w.shape[1] if layout == "nk" else w.shape[2]
     y = _new(x, (B, N), out_dtype or x.dtype, stream)
