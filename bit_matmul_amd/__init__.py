@@ -156,6 +156,8 @@ def _torch():
 
 def _stream_ptr(stream, device):
     torch = _torch()
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on the GPU, got {device}")
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))

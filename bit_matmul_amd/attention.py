@@ -81,9 +81,9 @@ def _raise(status: int, where: str):
 
 
 def _stream(stream, index):
+    if index < 0:
+        raise ValueError("tensors must be on the GPU")
     if stream is None:
-        if index < 0:
-            raise ValueError("tensors must be on the GPU")
         return _current_stream(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
