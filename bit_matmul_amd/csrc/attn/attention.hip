@@ -180,8 +180,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   const int r0 = work.row_tile * kRows;
   if (r0 >= ex.rows) return;
   const int rows = min(kRows, ex.rows - r0);
-  const int lo_pos = ex.first + r0 / p.share;
-  const int hi_pos = ex.first + (r0 + rows - 1) / p.share;
+  const int lo_pos = position(ex, r0 / p.share);
+  const int hi_pos = position(ex, (r0 + rows - 1) / p.share);
   const Steps<kStep> steps(lo_pos, hi_pos, p.window, p.sinks);
   const Part range = part_of(steps.count, work.split, work.splits);
   const int i0 = range.first, i1 = range.last;
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   // every bit that way. A word's codes come out in the order 0 4 1 5 2 6 3 7, the odd ones
   // times 16, which the query takes back.
   const RowOf row_of(p, head, min(r0 + n, ex.rows - 1));
-  const int pos = ex.first + row_of.i;
+  const int pos = position(ex, row_of.i);
   const uint16_t* qrow = p.q + (int64_t)(ex.q0 + row_of.i) * p.q_stride + (int64_t)row_of.head * D + g * (GS / 4);
   f16x8_t q[KW];
   float c;            // scores to base-2 logarithms, but for the keys' unit

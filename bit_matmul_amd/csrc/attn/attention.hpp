@@ -61,6 +61,10 @@ __device__ __forceinline__ Extent extent_of(const AttentionParams& p, int b, boo
   return e;
 }
 
+// Position of the sequence's query i. Those before the first token see nothing, wherever they are: all at
+// -1, so that a window's width can be taken off any position in 32 bits.
+__device__ __forceinline__ int position(const Extent& e, int i) { return max(e.first + i, -1); }
+
 // Row r of a sequence and kv head: query i of the sequence, one of the heads that share.
 struct RowOf {
   int i, head;
@@ -113,7 +117,7 @@ struct Shares {
     mine = lane < p.B ? extent_of(p, lane, blockIdx.x == 0) : Extent{0, 0, 0, 0};
     int steps = 0;
     if (mine.rows > 0) {
-      steps = Steps<32>(mine.first, mine.first + (mine.rows - 1) / p.share, p.window, p.sinks).count;
+      steps = Steps<32>(position(mine, 0), position(mine, (mine.rows - 1) / p.share), p.window, p.sinks).count;
     }
     const int slots = p.B * p.splits;
     auto sum = [](int v) {

@@ -98,7 +98,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
   const int r0 = work.row_tile * 32 * RW;
   if (r0 >= ex.rows) return;
   const int rows = min(32 * RW, ex.rows - r0);
-  const Steps<TILE> steps(ex.first + r0 / p.share, ex.first + (r0 + rows - 1) / p.share, p.window, p.sinks);
+  const Steps<TILE> steps(position(ex, r0 / p.share), position(ex, (r0 + rows - 1) / p.share), p.window, p.sinks);
   const Part part = part_of(steps.count, work.split, work.splits);
   const int i0 = part.first, i1 = part.last;
   const int32_t* table = p.page_table + (int64_t)b * p.pages_per_seq;
@@ -110,9 +110,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
   // This wave's rows, and this lane's.
   const int wr = r0 + 32 * (wave % RW);
   const bool wave_live = wr < ex.rows;
-  const int lo_pos = ex.first + min(wr, ex.rows - 1) / p.share;
-  const int hi_pos = ex.first + min(wr + 31, ex.rows - 1) / p.share;
-  const int pos = ex.first + min(wr + c, ex.rows - 1) / p.share;
+  const int lo_pos = position(ex, min(wr, ex.rows - 1) / p.share);
+  const int hi_pos = position(ex, min(wr + 31, ex.rows - 1) / p.share);
+  const int pos = position(ex, min(wr + c, ex.rows - 1) / p.share);
 
   // The row as binary16 and times the scores' scale, for keys in units of 2^k_unit, so that the
   // products are base-2 logarithms as they stand. Where that would pass binary16's range (scores

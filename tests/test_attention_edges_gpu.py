@@ -110,3 +110,33 @@ def test_memory_of_a_product_on_another_stream():
     assert p not in [torch.empty(size, dtype=torch.uint8, device="cuda:0").data_ptr() for _ in range(4)]
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(y, good) and (z.float() - good.float()).norm() <= 2.0 ** -7 * good.float().norm()
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+
+# The host's bounds of the lengths choose the kernel: these send small sizes through the one for many rows,
+# with a row tile's tokens in one piece or split over workgroups.
+KERNELS = {"rows": {}, "tiles": dict(max_q=8192, max_kv=2047), "tiles, split": dict(max_q=130, max_kv=65536)}
+
+
+def bounds(kernel, seq):
+    b = KERNELS[kernel]
+    return {} if not b else dict(max_q=max(b["max_q"], max(q for q, _ in seq.lens)),
+                                 max_kv=max(b["max_kv"], max(kv for _, kv in seq.lens)))
+
+
+def ran(kernel):
+    assert bm.bitmm_last_launches()[0].startswith(f"attention_{kernel.split(',')[0]}_kernel<")
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30])
+@pytest.mark.parametrize("sinks", [0, 2 ** 31 - 1])
+def test_widest_windows(kernel, window, sinks):
+    """More queries than tokens under windows at the end of their range: the queries that see tokens see them all."""
+    seq = U.Sequences([(9, 4), (1, 50), (40, 3)], q_heads=4, kv_heads=2, head_dim=64, group=32, page=16, dtype=BF16)
+    got = T.check(seq, window=window, sinks=sinks, **bounds(kernel, seq))
+    ran(kernel)
+    assert (got[:5] == 0).all() and (got[5:9] != 0).any(-1).all()
