@@ -58,16 +58,17 @@ __device__ __forceinline__ StepPages step_pages(const AttentionParams& p, const 
   for (int u = 0; u < 2; ++u) s.page[u] = base + 16 * u < kv ? table[(base + 16 * u) >> p.cache.page_shift] : 0;
   return s;
 }
-// `outside` collects whether a page was outside the cache.
+// `outside` collects whether a page was outside the cache that holds tokens which a row sees.
+template <typename F>
 __device__ __forceinline__ StepPlace step_place(const Cache& c, int head_row, int kv, int base,
-                                                const StepPages& pages, bool& outside) {
+                                                const StepPages& pages, F seen, bool& outside) {
   StepPlace s;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int tb = base + 16 * u;
     const int page = __builtin_amdgcn_readfirstlane(pages.page[u]);
     const bool inside = (uint32_t)page < (uint32_t)c.num_pages;
-    outside = outside || !inside;
+    outside = outside || (!inside && seen(tb, tb + 15));
     s.ok[u] = tb < kv && inside;
     s.row[u] = (int64_t)(inside ? page : 0) * (c.kv_heads << c.page_shift) + (head_row + (tb & ((1 << c.page_shift) - 1)));
   }
@@ -191,6 +192,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   StepPages pages = {};
   StepPlace place = {};
   bool outside = false;
+  auto seen = [&](int from, int to) { return any_sees(from, to, lo_pos, hi_pos, p.window, p.sinks); };
   const int head_row = head << p.cache.page_shift;
   const int first = i0 + wave;
   auto copy = [&](int stage) {
@@ -202,7 +204,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   };
   if (first < i1) {
     pages = step_pages(p, table, ex.kv, steps.base(first));
-    place = step_place(p.cache, head_row, ex.kv, steps.base(first), pages, outside);
+    place = step_place(p.cache, head_row, ex.kv, steps.base(first), pages, seen, outside);
     if (first + WAVES < i1) pages = step_pages(p, table, ex.kv, steps.base(first + WAVES));
     copy(0);
   }
@@ -337,7 +339,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
     }
     __builtin_amdgcn_wave_barrier();
     if (i + WAVES < i1) {
-      place = step_place(p.cache, head_row, ex.kv, steps.base(i + WAVES), pages, outside);
+      place = step_place(p.cache, head_row, ex.kv, steps.base(i + WAVES), pages, seen, outside);
       if (i + 2 * WAVES < i1) pages = step_pages(p, table, ex.kv, steps.base(i + 2 * WAVES));
       copy(stage);
     }

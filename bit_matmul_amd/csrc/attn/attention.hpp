@@ -159,6 +159,11 @@ __device__ __forceinline__ bool visible(int token, int pos, int window, int sink
   return (token <= pos) & ((window <= 0) | (token > pos - window) | (token < sinks));
 }
 
+// Whether a row at one of the positions lo_pos .. hi_pos sees one of the tokens from .. to.
+__device__ __forceinline__ bool any_sees(int from, int to, int lo_pos, int hi_pos, int window, int sinks) {
+  return from <= hi_pos && (window <= 0 || to > lo_pos - window || from < sinks);
+}
+
 // A workgroup's work: a sequence and kv head, one of its row tiles, and which part of how many of
 // the tokens.
 struct Work {

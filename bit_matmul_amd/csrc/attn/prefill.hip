@@ -201,7 +201,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
       for (int e = 0; e < L::PAIRS; ++e) t.kp[e] = t.vp[e] = 0;
       if (i < i1 && at < ex.kv) {
         atomicOr(reinterpret_cast<unsigned long long*>(&notes.gone[i & 3][lt >> 6]), 1ull << (lt & 63));
-        if (p.status) *p.status = 1;
+        if (p.status && any_sees(at, at, position(ex, r0 / p.share), position(ex, (r0 + rows - 1) / p.share), p.window, p.sinks))
+          *p.status = 1;
       }
     }
   };

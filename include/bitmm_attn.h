@@ -136,7 +136,8 @@ size_t bitmm_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t max_q, i
  * in slots they do not see. max_q and max_kv bound the sequences' queries and tokens; a
  * length or offset on the device that is negative, decreasing or passes these bounds, T or
  * the page table is cut to them and sets *status. A token on a page outside the cache is
- * seen by nobody and sets *status. Rows of q that belong to no sequence are not written.
+ * seen by nobody, and sets *status if a query would see it: pages that a window has left behind
+ * need no entry in the table. Rows of q that belong to no sequence are not written.
  * Scores, softmax and sums are f32; keys, values and probabilities enter the matrix cores
  * as binary16, in units chosen from the stored scales, and so do queries times `scale` in
  * the form for many query rows. Which form runs, how the tokens are split, and with it the

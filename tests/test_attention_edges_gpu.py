@@ -140,3 +140,39 @@ def test_widest_windows(kernel, window, sinks):
     got = T.check(seq, window=window, sinks=sinks, **bounds(kernel, seq))
     ran(kernel)
     assert (got[:5] == 0).all() and (got[5:9] != 0).any(-1).all()
+
+
+@pytest.mark.parametrize("kernel", ["rows", "tiles"])
+@pytest.mark.parametrize("nq", [1, 3, 70])
+@pytest.mark.parametrize("page", [16, 32])
+def test_evicted_pages(kernel, nq, page):
+    """Pages that no query sees any token of may be gone from the table, wherever the window begins in a step
+    or tile of the kernels; one that a query sees a token of is reported, and its tokens are seen by nobody."""
+    window, sinks = 100, 5
+    word = torch.zeros(1, dtype=torch.int32, device="cuda:0")
+    evicted = 0
+    for kv in (nq + 150, nq + 187, nq + 222, nq + 255, nq + 300, nq + 333):
+        seq = U.Sequences([(nq, kv), (1, 90)], q_heads=2, kv_heads=1, head_dim=64, group=32, page=page, dtype=BF16)
+        low = max(0, kv - nq - window + 1)                       # the first token that a query's window holds
+        want, _, tol, _ = seq.reference(BF16, 0.125, window, sinks)
+        cache, keep = seq.cache("cuda:0"), seq.table.clone()
+        for j in range(-(-kv // page)):
+            if (j + 1) * page <= low and j * page >= sinks:
+                keep[0, j] = (-1, cache.num_pages, 2 ** 31 - 1)[j % 3]
+                evicted += 1
+        whole, seq.table = seq.table, keep
+        word.zero_()
+        got, _ = T.attend(seq, cache, BF16, scale=0.125, window=window, sinks=sinks, status=word, **bounds(kernel, seq))
+        ran(kernel)
+        near(got, want, tol)
+        assert word.item() == 0, kv
+        for j in {0, low // page, (kv - 1) // page}:             # the pages at each end of what is seen
+            seq.table = whole
+            want2, _, tol2, _ = seq.reference(BF16, 0.125, window, sinks, hide=lambda b, t: (t // page == j) & (b == 0))
+            seq.table = keep.clone()
+            seq.table[0, j] = -1
+            word.zero_()
+            got, _ = T.attend(seq, cache, BF16, scale=0.125, window=window, sinks=sinks, status=word, **bounds(kernel, seq))
+            near(got, want2, tol2)
+            assert word.item() == 1, (kv, j)
+    assert evicted > 10
