@@ -5,8 +5,8 @@
 //   q . k_j = sum_g s_g (sum q c - 8 sum q) + (b_g + 8 s_g) sum q
 // over each group's dims, so bare codes (as 1024 + c: mask and OR) go through the matrix cores, a
 // product a group whose sum starts from what takes 1024 + 8 off again, and two f32 operations a
-// group give the score. Softmax in one pass: a running maximum m and sum l of exp2(x - m), outputs
-// scaled when m grows. Values are expanded to binary16, s (c - 8) + (b + 8 s), two at a time.
+// group give the score. Softmax in one pass: a running reference m and sum l of exp2(x - m), outputs
+// scaled when m moves. Values are expanded to binary16, s (c - 8) + (b + 8 s), two at a time.
 //
 // Rounded to binary16 (11 bits, against the cache's 4): s and b + 8 s of each pair, values,
 // probabilities. Queries are not, but for parts of a binary16 row 2^-14 and less of its largest.
@@ -401,17 +401,19 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
         }
     }
 
-    // Running maximum, kept until a score passes it by 2^8: probabilities up to 256 are as
-    // good as those up to 1.
+    // The reference m, kept while the step's largest probability is 2^-4 to 2^12; 2^4 where it is set.
     float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
                       fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
     const float ck0 = ldexpf(c, uk.e);
     const float ck = ck0 < 1e-37f ? 1e-37f : ck0;  // masked scores times 0 would be NaN
     top = across32(across16(top, Max()), Max()) * ck;
-    if (__any(top > m + 8.f)) {
-      const float to = fmaxf(m, top);
+    const float above = top - m;  // NaN where no score is seen yet
+    const bool low = above < -4.f && top > neg_inf();
+    if (__any(above > 12.f || low)) {
+      const float room = room_below(across32(across16(l, Add()), Add()), uv.e);
+      const float to = above > 12.f ? top - 4.f : low ? fmaxf(top - 4.f, m - room) : m;
       const float alpha = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - to);
-      if (to > neg_inf()) m = to;
+      m = to;
       l *= alpha;
 #pragma unroll
       for (int j = 0; j < J; ++j)

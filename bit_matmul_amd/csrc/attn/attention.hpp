@@ -7,6 +7,13 @@
 // E so that their largest magnitude is near 2^9 of 2^15, and E grows when later ones need it
 // (a wave-uniform branch that ordinary data takes once). Scores are scaled back by a factor
 // that multiplies them anyway, outputs when they are stored.
+//
+// Probabilities. What the second product takes is exp2(x - m) as binary16, which reaches from 2^16 down to
+// 2^-14, or 2^-24 with fewer and fewer bits. m is a reference near the largest score of late, not the largest of
+// all: where a token of long ago has most of the weight (the first one often has, with little to give) the rest
+// would otherwise be rounded to nothing, each by itself, in an output that they alone make up. m rises when a
+// probability nears 2^16, and falls when those of a step or half tile are all small, as long as the sum of what
+// came before stays below 2^40 beside them: what they add to it is then past f32's 24 bits.
 #pragma once
 
 #include "attn.hpp"
@@ -230,6 +237,12 @@ __device__ __forceinline__ void widen(Unit& u, float size, int near = 9, int mos
     u.down = __uint_as_float((uint32_t)(127 - u.e) << 23);
     u.most = __uint_as_float((uint32_t)(127 + min(u.e + most, 127)) << 23);
   }
+}
+
+// How many bits the reference of a row's exponents may still fall, by its sum l so far in all its lanes: until l
+// is near 2^40. Outputs are held in units of 2^unit beside it, so large values leave less room.
+__device__ __forceinline__ float room_below(float l, int unit) {
+  return (float)max(0, 40 - max(0, unit - 40) - __builtin_amdgcn_frexp_expf(l));
 }
 
 // Four neighbouring outputs at index `at` of p.out.

@@ -3,9 +3,8 @@
 // Mathematics. Queries times scale * log2(e), keys and values are binary16 in LDS and registers,
 // s (c - 8) + (b + 8 s) two codes at a time; the products' sums are f32 and start from -m, so that
 // scores leave the matrix cores as the exponents of p = exp2(x - m). The sum of p is f32, taken
-// before the rounding; p is rounded to binary16 for the product with the values. m is the largest
-// score of the first tokens that a row sees, and is looked for again only when a sum passes 2^13:
-// no probability has then passed binary16's range. Each of these roundings is 2^-12 of a value on
+// before the rounding; p is rounded to binary16 for the product with the values. m follows the
+// largest score only where a sum says that probabilities near the ends of binary16's range. Each of these roundings is 2^-12 of a value on
 // the average where the cache keeps 4 bits: with bf16 results the error is that of the result's
 // own rounding; binary16 results are off by 4.5e-4 of their size against 2.1e-4 for that alone.
 //
@@ -422,32 +421,42 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
         sum += odd;
       };
       exponentials();
-      // The reference m of the exponents is the largest score of the first tokens seen, and need
-      // not follow the largest so far as long as no probability nears binary16's end: a sum up to
-      // 2^13 says so. Only past it is a maximum looked for.
-      if (__any(!(sum <= 8192.f) || m == neg_inf())) {
+      // The reference m of the exponents is set so that the largest probability is 2^4, and need not follow
+      // scores as long as a half's probabilities neither near binary16's upper end nor become all small: a
+      // sum from 2^-9 to 2^15.9 says so (32 of them round to 2^-25 at worst, 2^-11 of that together; none at
+      // all are masked ones). Only past it is a maximum looked for.
+      if (__any(!(sum <= 61440.f) || (sum < 0x1p-9f && sum > 0.f) || m == neg_inf())) {
         float top = neg_inf();
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
           for (int e = 0; e < 16; ++e) top = fmaxf(top, x[tb][e]);
         top = across32(top, Max());
-        const bool first = m == neg_inf();
-        const float up = first ? (top > neg_inf() ? top : 0.f) : fmaxf(top, 0.f);
-        const float alpha = first ? 1.f : __builtin_amdgcn_exp2f(-up);
-        m = first ? (top > neg_inf() ? top : m) : m + up;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          start[e] = m == neg_inf() ? 0.f : -m / wide;
-          x[0][e] -= up;
-          x[1][e] -= up;
+        const bool seen = top > neg_inf();
+        float up = 0.f, alpha = 1.f;
+        if (m == neg_inf()) {
+          up = seen ? top - 4.f : 0.f;
+          m = seen ? up : m;
+        } else {
+          const float room = room_below(across32(l, Add()), o_unit);
+          up = top > 4.f ? top - 4.f : seen && top < -4.f ? fmaxf(top - 4.f, -room) : 0.f;
+          alpha = __builtin_amdgcn_exp2f(-up);
+          m += up;
         }
-        l *= alpha;
+        if (__any(up != 0.f)) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+          for (int e = 0; e < 16; ++e) {
+            start[e] = m == neg_inf() ? 0.f : -m / wide;
+            x[0][e] -= up;
+            x[1][e] -= up;
+          }
+          l *= alpha;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[d][e] *= alpha;
-        exponentials();
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[d][e] *= alpha;
+          exponentials();
+        }
       }
       l += sum;
       __builtin_amdgcn_s_setprio(0);

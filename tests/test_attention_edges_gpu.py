@@ -176,3 +176,63 @@ def test_evicted_pages(kernel, nq, page):
             near(got, want2, tol2)
             assert word.item() == 1, (kv, j)
     assert evicted > 10
+
+
+def one_heavy_token(lens, D, at, bits, seed=1):
+    """Keys that are codes and queries of one dim, so that scores are whole numbers of bits: token `at` of each
+    sequence scores `bits` more than the others do on the average, and its value is zero; the others' are 1 to 2."""
+    seq = U.Sequences(lens, q_heads=4, kv_heads=2, head_dim=D, group=64, page=32, dtype=BF16, seed=seed)
+    g = torch.Generator().manual_seed(seed)
+    for side, (codes, scale, bias) in enumerate(seq.sides):
+        codes = torch.randint(1, 4, codes.shape, generator=g) if side == 0 else codes
+        scale, bias = torch.ones_like(scale), torch.zeros_like(bias)
+        if side == 1:
+            scale, bias = scale / 16, bias + 1
+        for b in range(len(lens)):
+            page, off = seq.table[b, at // 32].long(), at % 32
+            if side == 0:
+                codes[page, :, off, 0] = 15
+            else:
+                scale[page, :, off], bias[page, :, off] = 0, 0
+        seq.sides[side] = (codes, scale, bias)
+    seq.q = torch.zeros_like(seq.q)
+    seq.q[..., 0] = bits / 13          # 15 against 1, 2 or 3
+    return seq
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("at", [0, 40])
+@pytest.mark.parametrize("bits", [13, 26, 39])
+@pytest.mark.parametrize("sinks", [0, 50])
+def test_weight_on_one_token(kernel, D, at, bits, sinks):
+    """A token that takes all but 2^-3 to 2^-29 of the weight and has nothing to give: the output is what the rest
+    add up to, and its probabilities keep their bits.
+
+    Scores are exact. A probability is rounded to 2^-11 of itself, or, where it is small beside the others of
+    its step or half tile, to no more than 2^-25 of 2^-9 at least: 2^-11 of the part's weight for 32 of them. Where
+    the heavy token is in the part itself, that is 64 * 2^-29 of its weight."""
+    window = 200 if sinks else 0
+    if window and kernel == "tiles, split":
+        pytest.skip("a window is not split")
+    seq = one_heavy_token([(3, 573), (40, 900)], D, at, bits)
+    got, lse = T.attend(seq, seq.cache("cuda:0"), F32, scale=math.log(2), window=window, sinks=sinks, **bounds(kernel, seq))
+    ran(kernel)
+    h16, f32 = 2.0 ** -11, 2.0 ** -24
+    for b, (nq, kv) in enumerate(seq.lens):
+        r = slice(int(seq.cu[b]), int(seq.cu[b + 1]))
+        (k, _), (v, vc) = seq.tokens(0, b, kv), seq.tokens(1, b, kv)
+        pos, j = torch.arange(kv - nq, kv)[:, None], torch.arange(kv)[None]
+        see = (j <= pos) & ((j > pos - window) | (j < sinks)) if window else j <= pos
+        for h in range(4):
+            x = (seq.q[r, h].double() @ k[:, h // 2].T).masked_fill(~see, -math.inf) * math.log(2)
+            p, n = torch.softmax(x, -1), see.sum(-1, keepdim=True)
+            off = 4 * f32 * x.masked_fill(~see, 0).abs().amax(-1, keepdim=True)
+            rest = p.clone()
+            rest[:, at] = 0
+            want = p @ v[:, h // 2]
+            tol = want * (torch.expm1(2 * off) + h16 + f32 * (n + 64)) + h16 * (p @ (v + vc)[:, h // 2])
+            tol += 2 * (h16 * rest.sum(-1, keepdim=True) + 64 * 2.0 ** -29 * p[:, at:at + 1])
+            near(got[r, h], want, 1.01 * tol, f"head {h} of sequence {b}")
+            total = torch.logsumexp(x, -1)
+            near(lse[r, h], total, off[:, 0] + f32 * (n[:, 0] + 64) + 8 * f32 * total.abs(), "lse")
