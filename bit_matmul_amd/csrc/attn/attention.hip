@@ -138,49 +138,103 @@ __device__ __forceinline__ uint32_t pair_f16(uint32_t pair, float down) {
   return pack_half2<1>(s, fmaf(8.f, s, bf16_hi(pair) * down));
 }
 
-template <int D, int GS, int DT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_kernel(AttentionParams p) {
+// The largest of a token's NG pairs, which lie side by side, in all their lanes.
+template <int NG>
+__device__ __forceinline__ float token_size(float v) {
+  if constexpr (NG == 2) return fmaxf(v, dpp<0xB1>(v));
+  if constexpr (NG >= 4) return reduce_lanes<NG>(v, Max());
+  return v;
+}
+template <int PL>
+__device__ __forceinline__ float largest(const float (&size)[PL]) {
+  float m = size[0];
+#pragma unroll
+  for (int e = 1; e < PL; ++e) m = fmaxf(m, size[e]);
+  return reduce_lanes<64>(m, Max());
+}
+// Whether most of the tokens that have a size do not fit.
+template <typename U, int PL>
+__device__ __forceinline__ bool mostly_apart(const U& u, const float (&size)[PL]) {
+  int out = 0, all = 0;
+#pragma unroll
+  for (int e = 0; e < PL; ++e) {
+    out += __builtin_popcountll(__ballot(!u.fits(size[e])));
+    all += __builtin_popcountll(__ballot(size[e] > 0.f));
+  }
+  return 2 * out > all;
+}
+
+// LDS of a workgroup. Each wave's own: codes of two steps (keys, then values), and the pairs of one as binary16,
+// [group][place] of the keys and of the values, where token t of a half is at 4 (t % 4) + t / 4, and the
+// exponents of its tokens' keys and values over the units, where some have units of their own.
+// The joined outputs afterwards.
+template <int D, int GS, int WAVES>
+struct RowsLds {
+  static constexpr int SIDE = 16 * D;  // bytes of a step's keys or values
+  static constexpr int WAVE_BYTES = 4 * SIDE + 2 * 32 * (D / GS) * 4 + 2 * 32 * 4, JOIN_BYTES = D / 16 * 4 * 64 * 4;
+  __attribute__((aligned(16))) char bytes[WAVES * (WAVE_BYTES > JOIN_BYTES ? WAVE_BYTES : JOIN_BYTES)];
+  float ml[WAVES][2][16];
+};
+
+// A workgroup's rows: those of a row tile, and which part of how many of the tokens; `part` is its place in the
+// partial results.
+struct Rows {
+  Work work;
+  Extent ex;
+  int part, r0, rows;  // no rows: nothing to do
+};
+__device__ __forceinline__ Rows rows_of(const AttentionParams& p, int tid, int workgroup) {
+  Work work(p, workgroup);
+  Extent ex;
+  int part = work.split * p.B + work.b;
+  if (p.balanced) {
+    part = workgroup / p.cache.kv_heads;
+    work.head = workgroup - part * p.cache.kv_heads;
+    const Shares shares(p, tid & 63, workgroup == 0);
+    const Share mine = shares.of_slot(part);
+    work.b = max(mine.b, 0);
+    work.split = part - mine.first;
+    work.splits = mine.count;
+    ex = shares.extent(work.b);
+    if (mine.b < 0) ex.rows = 0;
+  } else {
+    ex = extent_of(p, work.b, tid == 0);
+  }
+  const int r0 = work.row_tile * kRows;
+  return {work, ex, part, r0, min(kRows, ex.rows - r0)};
+}
+
+// What a wave gathers: outputs in units of 2^unit, the exponents' reference and the sum.
+template <int D>
+struct Gathered {
+  f32x4_t o[D / 16];
+  float m, l;
+  int unit;
+};
+
+// A wave's share of the tokens. CAREFUL: with units that change and tokens that have their own. Without, those of
+// the wave's first step have to do for all its tokens, and it returns false where they do not.
+template <int D, int GS, int DT, int WAVES, bool CAREFUL>
+__device__ __forceinline__ bool gather_rows(const AttentionParams& p, const Rows& mine, int tid, RowsLds<D, GS, WAVES>& mem,
+                                            Gathered<D>& out) {
   constexpr int NG = D / GS;                         // groups of a head
   constexpr int J = D / 16;                          // output tiles
   constexpr int KW = D / 32, WG = GS / 32;           // a lane's key words, and those of a group
   constexpr int VW = D >= 128 ? D / 128 : 1;         // words of a value piece (64: half a word)
   constexpr int PL = NG > 2 ? NG / 2 : 1;            // pairs of a lane
-  // Each wave's own: codes of two steps (keys, then values), and the pairs of one as binary16,
-  // [group][place] of the keys and of the values, where token t of a half is at 4 (t % 4) + t / 4.
-  // The joined outputs afterwards.
-  constexpr int SIDE = 16 * D;  // bytes of a step's keys or values
-  constexpr int WAVE_BYTES = 4 * SIDE + 2 * 32 * NG * 4, JOIN_BYTES = J * 4 * 64 * 4;
-  __shared__ __attribute__((aligned(16))) char lds[WAVES * (WAVE_BYTES > JOIN_BYTES ? WAVE_BYTES : JOIN_BYTES)];
-  __shared__ float ml_lds[WAVES][2][16];
-  float(*o_lds)[J * 4][64] = reinterpret_cast<float(*)[J * 4][64]>(lds);
+  constexpr int SIDE = RowsLds<D, GS, WAVES>::SIDE, WAVE_BYTES = RowsLds<D, GS, WAVES>::WAVE_BYTES;
+  char* lds = mem.bytes;
 
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  Work work(p, blockIdx.x);
-  Extent ex;
-  int part = work.split * p.B + work.b;  // of the partial results
-  if (p.balanced) {
-    const int slot = blockIdx.x / p.cache.kv_heads;
-    work.head = blockIdx.x - slot * p.cache.kv_heads;
-    const Shares shares(p, lane);
-    const Share mine = shares.of_slot(slot);
-    if (mine.b < 0) return;
-    work.b = mine.b;
-    work.split = slot - mine.first;
-    work.splits = mine.count;
-    part = slot;
-    ex = shares.extent(work.b);
-  } else {
-    ex = extent_of(p, work.b);
-  }
-  const int head = work.head;
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 15, g = lane >> 4;
   char* ring = lds + wave * WAVE_BYTES;
   uint32_t* k_pairs = reinterpret_cast<uint32_t*>(ring + 4 * SIDE);
   uint32_t* v_pairs = k_pairs + 32 * NG;
+  int(*apart)[32] = reinterpret_cast<int(*)[32]>(v_pairs + 32 * NG);
 
-  const int r0 = work.row_tile * kRows;
-  if (r0 >= ex.rows) return;
-  const int rows = min(kRows, ex.rows - r0);
+  const Work work = mine.work;
+  const Extent ex = mine.ex;
+  const int head = work.head, r0 = mine.r0, rows = mine.rows;
   const int lo_pos = position(ex, r0 / p.share);
   const int hi_pos = position(ex, (r0 + rows - 1) / p.share);
   const Steps<kStep> steps(lo_pos, hi_pos, p.window, p.sinks);
@@ -259,11 +313,15 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
     }
   }
 
-  f32x4_t o[J];
+  f32x4_t(&o)[J] = out.o;
 #pragma unroll
   for (int j = 0; j < J; ++j) o[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  float m = neg_inf(), l = 0.f;
-  Unit uk, uv;
+  float &m = out.m, &l = out.l;
+  m = neg_inf();
+  l = 0.f;
+  RowsKeys uk;
+  Values uv;
+  Sizes k_sizes, v_sizes;
   // 1024 twice in binary16, in a register, so that mask and OR are one instruction. (No inline
   // assembly next to the matrix cores: the compiler keeps the distance that their operands and
   // results need only for instructions that it knows.)
@@ -296,35 +354,55 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
         vp[e] = ok ? vp[e] : 0;
       }
     }
-    float ksize = 0.f, vsize = 0.f;
-    auto sizes = [&] {
-      ksize = vsize = 0.f;
+    bool spread = false;  // some of the step's tokens have units of their own
+    if constexpr (!CAREFUL) {
 #pragma unroll
       for (int e = 0; e < PL; ++e) {
-        ksize += pair_size(kp[e]);
-        vsize += pair_size(vp[e]);
+        k_sizes.add(pair_size(kp[e]));
+        v_sizes.add(pair_size(vp[e]));
       }
-    };
-    sizes();
-    if (__any(!(ksize <= uk.most) || !(vsize <= uv.most))) {
+      if (i == first) {
+        uk.take(reduce_lanes<64>(k_sizes.most(), Max()));
+        uv.take(reduce_lanes<64>(v_sizes.most(), Max()));
+      }
+    } else {
       const int at = opaque(lane);
+      float ks[PL], vs[PL];
 #pragma unroll
       for (int e = 0; e < PL; ++e) {
         const bool odd_k = !pair_finite(kp[e]), odd_v = !pair_finite(vp[e]);
         if (odd_k) kp[e] = 0;
         if (odd_v) vp[e] = 0;
         if (odd_k || odd_v) bad |= 1u << ((64 * e + at) / NG % 32);
+        ks[e] = token_size<NG>(pair_size(kp[e]));
+        vs[e] = token_size<NG>(pair_size(vp[e]));
       }
       bad = __float_as_uint(reduce_lanes<64>(__uint_as_float(bad), Or()));
-      sizes();
-      widen(uk, reduce_lanes<64>(ksize, Max()));
-      const int before = uv.e;
-      widen(uv, reduce_lanes<64>(vsize, Max()));
-      if (uv.e != before) {
+      if (mostly_apart(uk, ks)) uk.take(largest(ks));
+      if (mostly_apart(uv, vs)) {
+        const int before = uv.e;
+        uv.take(largest(vs));
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[j][e] = ldexpf(o[j][e], before - uv.e);
+      }
+      bool rest = false;
+#pragma unroll
+      for (int e = 0; e < PL; ++e) rest = rest || !uk.fits(ks[e]) || !uv.fits(vs[e]);
+      spread = __any(rest);
+      if (spread) {
+#pragma unroll
+        for (int e = 0; e < PL; ++e) {
+          const int kd = uk.apart(ks[e]), vd = uv.apart(vs[e]);
+          kp[e] = pair_down(kp[e], kd);
+          vp[e] = pair_down(vp[e], vd);
+          const int f = 64 * e + at;
+          if (f < 32 * NG) {
+            apart[0][f / NG] = kd;
+            apart[1][f / NG] = vd;
+          }
+        }
       }
     }
     // The wave's own part of LDS: its operations are in order.
@@ -333,8 +411,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
       const int f = 64 * e + lane, t = f / NG;
       if (NG >= 2 || lane < 32) {
         const int to = f % NG * 32 + (t & 16) + 4 * (t & 3) + (t >> 2 & 3);
-        k_pairs[to] = pair_f16(kp[e], uk.down);
-        v_pairs[to] = pair_f16(vp[e], uv.down);
+        k_pairs[to] = pair_f16(kp[e], uk.down());
+        v_pairs[to] = pair_f16(vp[e], uv.down());
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -401,16 +479,34 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
         }
     }
 
+    const float ck0 = ldexpf(c, uk.e);
+    float ck = ck0 < 1e-37f ? 1e-37f : ck0;  // masked scores times 0 would be NaN
+    if (CAREFUL && spread) {  // to the exponents of what the values are multiplied by
+      const int g0 = opaque(g);
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int at = 16 * u + 4 * t + g0;
+          x[u][t] = ldexpf(x[u][t] * ck, apart[0][at]) + (float)apart[1][at];
+        }
+      ck = 1.f;
+    }
+
     // The reference m, kept while the step's largest probability is 2^-4 to 2^12; 2^4 where it is set.
     float top = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
                       fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3])));
-    const float ck0 = ldexpf(c, uk.e);
-    const float ck = ck0 < 1e-37f ? 1e-37f : ck0;  // masked scores times 0 would be NaN
     top = across32(across16(top, Max()), Max()) * ck;
     const float above = top - m;  // NaN where no score is seen yet
     const bool low = above < -4.f && top > neg_inf();
     if (__any(above > 12.f || low)) {
-      const float room = room_below(across32(across16(l, Add()), Add()), uv.e);
+      float sofar = opaque(0.f);
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sofar = fmaxf(sofar, fabsf(o[j][e]));
+      sofar = fmaxf(sofar * 0x1p-15f, l);
+      const float room = room_below(across32(across16(sofar, Max()), Max()));
       const float to = above > 12.f ? top - 4.f : low ? fmaxf(top - 4.f, m - room) : m;
       const float alpha = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - to);
       m = to;
@@ -422,15 +518,25 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
     }
     const float off = m == neg_inf() ? 0.f : m;
     u32x4_t pr;
+    float sum = 0.f;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int t = 0; t < 4; t += 2) {
         const float e0 = __builtin_amdgcn_exp2f(fmaf(x[u][t], ck, -off)),
                     e1 = __builtin_amdgcn_exp2f(fmaf(x[u][t + 1], ck, -off));
-        l += e0 + e1;
+        sum += e0 + e1;
         pr[2 * u + t / 2] = pack_half2<1>(e0, e1);
       }
+    if (CAREFUL && spread) {  // the sum is of the probabilities alone
+      const int g0 = opaque(g);
+      sum = 0.f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) sum += __builtin_amdgcn_exp2f(x[u][t] - off - (float)apart[1][16 * u + 4 * t + g0]);
+    }
+    l += sum;
     const f16x8_t prob = __builtin_bit_cast(f16x8_t, pr);
 
     // Outputs.
@@ -478,24 +584,49 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
 
   if (outside && p.status && lane == 0) *p.status = 1;
 
+  out.unit = uv.e;
+  return CAREFUL || !__any(!k_sizes.fit(uk) || !v_sizes.fit(uv));
+}
+
+template <int D, int GS, int DT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_kernel(AttentionParams p) {
+  constexpr int J = D / 16;
+  __shared__ RowsLds<D, GS, WAVES> mem;
+  const Rows own = rows_of(p, threadIdx.x, blockIdx.x);
+  if (own.rows <= 0) return;
+  Gathered<D> got;
+  if (!gather_rows<D, GS, DT, WAVES, false>(p, own, threadIdx.x, mem, got)) {
+    const AttentionParams& again = params_again();
+    const int same = opaque((int)threadIdx.x);
+    gather_rows<D, GS, DT, WAVES, true>(again, rows_of(again, same, scalar_again(blockIdx.x)), same, mem, got);
+  }
+  f32x4_t(&o)[J] = got.o;
+  float m = got.m, l = got.l;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const Work work = own.work;
+  const Extent ex = own.ex;
+  const int head = work.head, r0 = own.r0;
+
   // The waves' results joined: each brings its own to the common maximum, and wave w stores
   // every WAVES / 4-th part of dims (4 g + w % 4) D/16 .. of its lanes' rows.
   l = across32(across16(l, Add()), Add());
   if (g == 0) {
-    ml_lds[wave][0][n] = m;
-    ml_lds[wave][1][n] = l;
+    mem.ml[wave][0][n] = m;
+    mem.ml[wave][1][n] = l;
   }
   __syncthreads();
+  float(*o_lds)[J * 4][64] = reinterpret_cast<float(*)[J * 4][64]>(mem.bytes);
   float mt = neg_inf(), lt = 0.f;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) mt = fmaxf(mt, ml_lds[w][0][n]);
+  for (int w = 0; w < WAVES; ++w) mt = fmaxf(mt, mem.ml[w][0][n]);
 #pragma unroll
   for (int w = 0; w < WAVES; ++w) {
-    const float mw = ml_lds[w][0][n];
+    const float mw = mem.ml[w][0][n];
     // A sum that is NaN has a maximum of -infinity if it met nothing else.
-    lt += ml_lds[w][1][n] * (mw == mt ? 1.f : __builtin_amdgcn_exp2f(mw - mt));
+    lt += mem.ml[w][1][n] * (mw == mt ? 1.f : __builtin_amdgcn_exp2f(mw - mt));
   }
-  const float mine = ldexpf(m == mt ? 1.f : __builtin_amdgcn_exp2f(m - mt), uv.e);
+  const float mine = ldexpf(m == mt ? 1.f : __builtin_amdgcn_exp2f(m - mt), got.unit);
 #pragma unroll
   for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -517,7 +648,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   const bool speaker = g == 0 && wave == 0;
   const int row = opaque(r0 + n);
   if (p.splits > 1 && (p.balanced || work.splits > 1)) {
-    const int64_t at = part_row(p, part, head, row);
+    const int64_t at = part_row(p, own.part, head, row);
     if (speaker) {
       p.part_ml[2 * at] = mt;
       p.part_ml[2 * at + 1] = lt;
@@ -550,14 +681,14 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) 
   Extent ex;
   int first = b, step = p.B, parts = p.splits;
   if (p.balanced) {
-    const Shares shares(p, lane);
+    const Shares shares(p, lane, blockIdx.x == 0);
     const Share mine = shares.of_sequence(b);
     ex = shares.extent(b);
     first = mine.first;
     step = 1;
     parts = mine.count;
   } else {
-    ex = extent_of(p, b);
+    ex = extent_of(p, b, threadIdx.x == 0);
   }
   if (r >= ex.rows) return;
   const int64_t row = part_row(p, first, head, r), all = part_row(p, step, 0, 0);
@@ -604,7 +735,7 @@ hipError_t launch_rows(const AttentionParams& p, unsigned workgroups, int dtype,
     hipLaunchKernelGGL((attention_rows_kernel<D, GS, 0, WAVES>), grid, block, 0, stream, p);
   else
     hipLaunchKernelGGL((attention_rows_kernel<D, GS, 1, WAVES>), grid, block, 0, stream, p);
-  launch_log(grid, block, (size_t)WAVES * (D * 64 + 256 * (D / GS) + 128), "attention_rows_kernel<%d, %d, %d, %d>", D, GS, dtype, WAVES);
+  launch_log(grid, block, sizeof(RowsLds<D, GS, WAVES>), "attention_rows_kernel<%d, %d, %d, %d>", D, GS, dtype, WAVES);
   return hipGetLastError();
 }
 

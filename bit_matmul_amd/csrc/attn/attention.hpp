@@ -3,10 +3,15 @@
 //
 // Units. Keys and values enter the matrix cores as binary16, whose eleven bits hold
 // scale * code + bias with an eighth of the rounding of bf16, but whose range is narrow
-// against a bf16 scale's. So each is taken in units of a power of two 2^E: the first tokens set
-// E so that their largest magnitude is near 2^9 of 2^15, and E grows when later ones need it
-// (a wave-uniform branch that ordinary data takes once). Scores are scaled back by a factor
-// that multiplies them anyway, outputs when they are stored.
+// against a bf16 scale's. So each is taken in units of a power of two 2^E, chosen so that the first tokens'
+// largest magnitude is near 2^9 of 2^15 (keys over many rows: 2^3 of 2^8). Scores are scaled back by a factor
+// that multiplies them anyway, outputs when they are stored. The largest of a token has all its bits down to
+// 2^-6 units. The sizes met are kept, a maximum and a minimum a lane, and looked at when all is done.
+// Where a token was not within, all is done again, in a careful form that ordinary data does not meet and
+// that has registers of its own: units move to where most tokens of a step or tile are, and any other token has
+// a unit 2^d times theirs: its score is multiplied by 2^d, and the exponent of its probability takes d in,
+// for the product with the values alone. So no row depends on the size of a token that it does not see.
+// (As one form for both, a prompt's chunk took 5 to 15 % longer, for scalar registers alone.)
 //
 // Probabilities. What the second product takes is exp2(x - m) as binary16, which reaches from 2^16 down to
 // 2^-14, or 2^-24 with fewer and fewer bits. m is a reference near the largest score of late, not the largest of
@@ -52,7 +57,7 @@ struct Extent {
   int kv;     // tokens
 };
 
-__device__ __forceinline__ Extent extent_of(const AttentionParams& p, int b, bool report = threadIdx.x == 0) {
+__device__ __forceinline__ Extent extent_of(const AttentionParams& p, int b, bool report) {
   Extent e;
   const int c0 = p.cu_q[b], c1 = p.cu_q[b + 1], len = p.kv_lens[b];
   const int64_t room = p.pages_per_seq << p.cache.page_shift;
@@ -120,8 +125,8 @@ struct Shares {
   Extent mine;
   int count, end;  // slots of lane b's sequence, and up to its end
 
-  __device__ __forceinline__ Shares(const AttentionParams& p, int lane) {
-    mine = lane < p.B ? extent_of(p, lane, blockIdx.x == 0) : Extent{0, 0, 0, 0};
+  __device__ __forceinline__ Shares(const AttentionParams& p, int lane, bool report) {
+    mine = lane < p.B ? extent_of(p, lane, report) : Extent{0, 0, 0, 0};
     int steps = 0;
     if (mine.rows > 0) {
       steps = Steps<32>(position(mine, 0), position(mine, (mine.rows - 1) / p.share), p.window, p.sinks).count;
@@ -171,6 +176,16 @@ __device__ __forceinline__ bool any_sees(int from, int to, int lo_pos, int hi_po
   return from <= hi_pos && (window <= 0 || to > lo_pos - window || from < sinks);
 }
 
+// A kernel's parameters, and a scalar, to be read and worked with anew: what a rare second attempt shares with the
+// first one would take up scalar registers throughout.
+__device__ __forceinline__ const AttentionParams& params_again() {
+  typedef __attribute__((address_space(4))) AttentionParams Params;
+  const Params* p = (const Params*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const AttentionParams*)p;
+}
+__device__ __forceinline__ int scalar_again(unsigned v) { return __builtin_amdgcn_readfirstlane(opaque((int)v)); }
+
 // A workgroup's work: a sequence and kv head, one of its row tiles, and which part of how many of
 // the tokens.
 struct Work {
@@ -219,30 +234,60 @@ __device__ __forceinline__ float pair_size(uint32_t pair) {
   return fmaf(15.f, fabsf(bf16_lo(pair)), fabsf(bf16_hi(pair)));
 }
 
-// The unit of keys or values: 2^e, its reciprocal as a factor, and the largest size that fits
-// it. Unset (nothing fits) until tokens with a nonzero magnitude have come.
+// 15 s + |b| of the largest finite s and b is past f32.
+__device__ __forceinline__ int size_exponent(float size) { return __builtin_amdgcn_frexp_expf(fminf(size, 3e38f)); }
+
+// The unit 2^e of keys or values. NEAR: the exponent, in units, that a token's size is brought to; MOST: the one
+// that it may reach; LOW, HIGH: the units' range. Keys' units may be any that keep their reciprocal finite. Outputs
+// are held in the values' units as these change, so those stay where that leaves f32's range alone.
+template <int NEAR, int MOST, int LOW, int HIGH>
 struct Unit {
-  int e = 0;
-  float down = 1.f;
-  float most = -1.f;
+  int e = 0;  // in a scalar register, and all else made from it
+  bool set = false;  // before tokens with a nonzero magnitude have come, those of zero alone fit
+  __device__ __forceinline__ float down() const { return __uint_as_float((uint32_t)(127 - e) << 23); }
+  // The sizes of tokens that it is good for, as bits.
+  __device__ __forceinline__ uint32_t most() const { return set ? (uint32_t)(127 + min(e + MOST, 127)) << 23 : 0; }
+  __device__ __forceinline__ uint32_t least() const { return set ? (uint32_t)(127 + max(e - 6, -126)) << 23 : 0; }
+  __device__ __forceinline__ bool fits(float size) const {
+    return size <= __uint_as_float(most()) && (size >= __uint_as_float(least()) || size == 0.f);
+  }
+  // Takes a unit for a size, the same in every lane.
+  __device__ __forceinline__ void take(float size) {
+    const float m = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(size)));
+    e = __builtin_amdgcn_readfirstlane(min(max(size_exponent(m) - NEAR, LOW), HIGH));
+    set = true;
+  }
+  // The exponent d of a token that does not fit, over the unit.
+  __device__ __forceinline__ int apart(float size) const { return fits(size) ? 0 : size_exponent(size) - NEAR - e; }
 };
 
-// Takes a larger unit for a largest size, the same in every lane, so that it is near 2^near units,
-// and stays until one passes 2^most. The unit stays in scalar registers.
-__device__ __forceinline__ void widen(Unit& u, float size, int near = 9, int most = 15) {
-  const float m = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(size)));
-  if (m > 0.f && !(m <= u.most)) {
-    // 15 s + |b| of the largest finite s and b is past f32; 2^-120 keeps the factor finite.
-    u.e = __builtin_amdgcn_readfirstlane(max(__builtin_amdgcn_frexp_expf(fminf(m, 3e38f)) - near, -120));
-    u.down = __uint_as_float((uint32_t)(127 - u.e) << 23);
-    u.most = __uint_as_float((uint32_t)(127 + min(u.e + most, 127)) << 23);
+// The largest and smallest of some sizes, that of zero apart, and whether a unit is good for all between.
+// As bits: those of what is not finite are larger than all others, and zero, less one, is large.
+struct Sizes {
+  uint32_t high = 0, low = ~0u;
+  __device__ __forceinline__ void add(float size) {
+    high = max(high, __float_as_uint(size));
+    low = min(low, __float_as_uint(size) - 1);
   }
+  __device__ __forceinline__ float most() const { return __uint_as_float(high); }
+  template <typename U>
+  __device__ __forceinline__ bool fit(const U& u) const {
+    return high <= u.most() && low >= u.least() - 1;
+  }
+};
+using RowsKeys = Unit<9, 15, -120, 118>;
+using TileKeys = Unit<3, 8, -120, 118>;
+using Values = Unit<9, 15, -30, 30>;
+
+// A pair in units 2^d times larger: exact, where it does not become too small to matter.
+__device__ __forceinline__ uint32_t pair_down(uint32_t pair, int d) {
+  return pack_bf16x2(ldexpf(bf16_lo(pair), -d), ldexpf(bf16_hi(pair), -d));
 }
 
-// How many bits the reference of a row's exponents may still fall, by its sum l so far in all its lanes: until l
-// is near 2^40. Outputs are held in units of 2^unit beside it, so large values leave less room.
-__device__ __forceinline__ float room_below(float l, int unit) {
-  return (float)max(0, 40 - max(0, unit - 40) - __builtin_amdgcn_frexp_expf(l));
+// How many bits the reference of a row's exponents may still fall, by the largest of its sum l so far and
+// 2^-15 of its outputs, in all its lanes: until that is near 2^40.
+__device__ __forceinline__ float room_below(float largest) {
+  return (float)max(0, 40 - __builtin_amdgcn_frexp_expf(largest));
 }
 
 // Four neighbouring outputs at index `at` of p.out.

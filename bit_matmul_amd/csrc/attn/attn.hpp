@@ -208,5 +208,10 @@ __device__ __forceinline__ int opaque(int v) {
   return v;
 }
 
+__device__ __forceinline__ float opaque(float v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 }  // namespace attn
 }  // namespace bitmm

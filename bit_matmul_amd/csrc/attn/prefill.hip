@@ -41,9 +41,17 @@ typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
 
 // What workgroups tell their waves about the tiles, beside keys and values.
 struct TileNotes {
-  uint32_t key_size[2], value_size[2];  // largest sizes (f32 bits) that did not fit, by tile % 2
-  uint64_t bad[4][2];   // tokens with a scale or bias that is not finite, by tile % 4
-  uint64_t gone[4][2];  // tokens on pages outside the cache
+  struct Tile {
+    uint64_t bad[2];   // tokens with a scale or bias that is not finite
+    uint64_t gone[2];  // tokens on pages outside the cache
+    // How many keys and values (in the upper half) do not fit the units, and the largest size (f32 bits) in
+    // their waves and the smallest that is not zero (its bits inverted).
+    uint32_t apart, most[2], least[2];
+  } tile[4];           // by tile % 4
+  static constexpr int WORDS = sizeof(Tile) / 4;
+  uint32_t undone;     // the first tile's units do not fit all tokens
+  float2 first[8];     // the largest sizes of the first tile's keys and values, by wave
+  int2 apart[2][128];  // exponents of a token's keys and values over the units, by tile % 2, where some have any
 };
 
 template <int D, int GS, int NW, int H>
@@ -69,10 +77,39 @@ __device__ __forceinline__ void wait_lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// RW: waves that take rows of their own. Eight waves are eight row waves, or two for each of four:
-// the one takes the first 64 tokens of each tile, the other the rest, and they join at the end.
-template <int D, int GS, int DT, int NW, int RW>
-__global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(AttentionParams p) {
+// LDS of a workgroup: two tiles of keys and values.
+template <int D, int NW>
+constexpr int kTileBytes = NW * 64 * D * 2;
+
+// A workgroup's rows.
+template <int RW>
+struct Rows {
+  Work work;
+  Extent ex;
+  int r0, rows;
+  __device__ __forceinline__ Rows(const AttentionParams& p, int tid, int workgroup)
+      : work(p, workgroup), ex(extent_of(p, work.b, tid == 0)), r0(work.row_tile * 32 * RW), rows(min(32 * RW, ex.rows - r0)) {}
+};
+
+__device__ __forceinline__ float larger(float a, float b) {
+  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
+
+// What a wave gathers: outputs in units of 2^unit, the exponents' reference and the sum.
+template <int D>
+struct Gathered {
+  f32x16_t o[D / 32];
+  float m, l;
+  int unit;
+};
+
+// RW: waves that take rows of their own. Eight waves are eight row waves, or two for each of four: the one takes
+// the first 64 tokens of each tile, the other the rest, and they join at the end.
+// CAREFUL: with units that change and tokens that have their own. Without, the first tile's units have to do for
+// all, and it returns false where they do not.
+template <int D, int GS, int DT, int NW, int RW, bool CAREFUL>
+__device__ __forceinline__ bool gather_tiles(const AttentionParams& p, const Rows<RW>& mine, int tid, char* lds, TileNotes& notes,
+                                             Gathered<D>& out) {
   // A tile is one or two halves of 64 tokens, as LDS allows: with two, waves run freely between
   // barriers for twice as long.
   constexpr int H = NW / 4, TILE = 64 * H;
@@ -81,30 +118,22 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
   constexpr int ROW = D * 2;                  // bytes of an LDS row
   constexpr int SIDE = TILE * ROW;           // bytes of a tile's keys or values
   constexpr int DB = D / 32;                  // blocks of output dims
-  __shared__ __attribute__((aligned(16))) char lds[4 * SIDE];
-  __shared__ TileNotes notes;
   constexpr int V_AHEAD = 4;                  // value operands read before the first product
-  static_assert(RW * 32 * ROW <= 4 * SIDE && (!PAIRED || (H == 2 && RW * (D / 2 * 256 + 512) <= 4 * SIDE)), "epilogue");
+  static_assert(4 * SIDE == kTileBytes<D, NW>, "tiles");
+  static_assert(!PAIRED || H == 2, "halves");
 
-  // The row tiles of a sequence and kv head on one XCD: its codes meet in one L2.
-  const Work work(p, xcd_remap(blockIdx.x, gridDim.x));
-  const int head = work.head, b = work.b;
-  const int tid = threadIdx.x, lane = tid & 63;
+  const Work work = mine.work;
+  const Extent ex = mine.ex;
+  const int head = work.head, b = work.b, r0 = mine.r0, rows = mine.rows;
+  const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, h = lane >> 5;
-
-  const Extent ex = extent_of(p, b);
-  const int r0 = work.row_tile * 32 * RW;
-  if (r0 >= ex.rows) return;
-  const int rows = min(32 * RW, ex.rows - r0);
   const Steps<TILE> steps(position(ex, r0 / p.share), position(ex, (r0 + rows - 1) / p.share), p.window, p.sinks);
   const Part part = part_of(steps.count, work.split, work.splits);
   const int i0 = part.first, i1 = part.last;
   const int32_t* table = p.page_table + (int64_t)b * p.pages_per_seq;
-  if (tid < 8) {
-    if (tid < 2) notes.key_size[tid] = notes.value_size[tid] = 0;
-    notes.bad[tid / 2][tid % 2] = notes.gone[tid / 2][tid % 2] = 0;
-  }
+  if (tid < 4 * TileNotes::WORDS) reinterpret_cast<uint32_t*>(notes.tile)[tid] = 0;
+  if (tid == 0) notes.undone = 0;
 
   // This wave's rows, and this lane's.
   const int wr = r0 + 32 * (wave % RW);
@@ -115,7 +144,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
 
   // The row as binary16 and times the scores' scale, for keys in units of 2^k_unit, so that the
   // products are base-2 logarithms as they stand. Where that would pass binary16's range (scores
-  // of 10^5 and more) the row is taken 2^-r fold, and its scores 2^r fold (`wide`).
+  // of 10^5 and more) the row is taken 2^-r fold, and its scores 2^r fold (`wide`). So it is where it
+  // would near the other end (scores below 2^-4, but for tokens of a larger unit of their own).
   f16x8_t q[D / 16];
   float wide = 1.f;
   bool any_wide = false;
@@ -139,11 +169,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
     }
     const float factor = p.scale * kLog2e;
     big = across32(big, Max());
-    const int r = big > 0.f && big < __uint_as_float(0x7F800000u)
-                      ? max(0, __builtin_amdgcn_frexp_expf(big) + __builtin_amdgcn_frexp_expf(factor) + k_unit - 15)
-                      : 0;
+    int r = 0;
+    if (big > 0.f && big < __uint_as_float(0x7F800000u) && factor != 0.f) {
+      const int end = __builtin_amdgcn_frexp_expf(big) + __builtin_amdgcn_frexp_expf(factor) + k_unit;
+      r = end > 15 ? end - 15 : end < -7 ? max(end, -80) : 0;
+    }
     wide = ldexpf(1.f, r);
-    any_wide = __any(r > 0);
+    any_wide = __any(r != 0);
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
       const u32x4_t raw = __builtin_bit_cast(u32x4_t, q[s]);
@@ -199,45 +231,57 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
 #pragma unroll
       for (int e = 0; e < L::PAIRS; ++e) t.kp[e] = t.vp[e] = 0;
       if (i < i1 && at < ex.kv) {
-        atomicOr(reinterpret_cast<unsigned long long*>(&notes.gone[i & 3][lt >> 6]), 1ull << (lt & 63));
+        atomicOr(reinterpret_cast<unsigned long long*>(&notes.tile[i & 3].gone[lt >> 6]), 1ull << (lt & 63));
         if (p.status && any_sees(at, at, position(ex, r0 / p.share), position(ex, (r0 + rows - 1) / p.share), p.window, p.sinks))
           *p.status = 1;
       }
     }
   };
 
-  Unit uk, uv;  // of the tile being written
-  // Whether the tile's sizes fit the units, told to the workgroup if not; tokens that are not
-  // finite are marked and emptied first.
-  auto measure = [&](int i, L& t) {
-    float ks = 0.f, vs = 0.f;
+  TileKeys uk;  // of the tile being written
+  Values uv;
+  // The size of a thread's token. As bits, where what is not finite is larger than all else.
+  static_assert(L::TPT == 4, "token_size");
+  auto token_size = [](const uint32_t* pairs) {
+    float m = pair_size(pairs[0]);
 #pragma unroll
-    for (int e = 0; e < L::PAIRS; ++e) {
-      ks = fmaxf(ks, pair_size(t.kp[e]));
-      vs = fmaxf(vs, pair_size(t.vp[e]));
-    }
+    for (int e = 1; e < L::PAIRS; ++e) m = larger(m, pair_size(pairs[e]));
+    return reduce_lanes<4>(m, larger);
+  };
+  // Tokens that are not finite are marked and emptied.
+  auto empty_odd = [&](int i, L& t) {
     bool odd = false;
 #pragma unroll
-    for (int e = 0; e < L::PAIRS; ++e) odd = odd || !pair_finite(t.kp[e]) || !pair_finite(t.vp[e]);
-    if (__any(odd || !(ks <= uk.most) || !(vs <= uv.most))) {
-      if (odd) {
-        atomicOr(reinterpret_cast<unsigned long long*>(&notes.bad[i & 3][lt >> 6]), 1ull << (lt & 63));
-        ks = vs = 0.f;
-#pragma unroll
-        for (int e = 0; e < L::PAIRS; ++e) {
-          if (!pair_finite(t.kp[e])) t.kp[e] = 0;
-          if (!pair_finite(t.vp[e])) t.vp[e] = 0;
-          ks = fmaxf(ks, pair_size(t.kp[e]));
-          vs = fmaxf(vs, pair_size(t.vp[e]));
-        }
-      }
-      ks = reduce_lanes<64>(ks, Max());
-      vs = reduce_lanes<64>(vs, Max());
-      if (lane == 0) {  // not negative: their bits are in order
-        atomicMax(&notes.key_size[i & 1], __float_as_uint(ks));
-        atomicMax(&notes.value_size[i & 1], __float_as_uint(vs));
-      }
+    for (int e = 0; e < L::PAIRS; ++e) {
+      odd = odd || !pair_finite(t.kp[e]) || !pair_finite(t.vp[e]);
+      if (!pair_finite(t.kp[e])) t.kp[e] = 0;
+      if (!pair_finite(t.vp[e])) t.vp[e] = 0;
     }
+    if (odd) atomicOr(reinterpret_cast<unsigned long long*>(&notes.tile[i & 3].bad[lt >> 6]), 1ull << (lt & 63));
+  };
+  // What the workgroup is told of a tile's keys (side 0) or values: not negative, so their bits are in order.
+  auto tell = [&](int i, int side, const auto& u, float size) {
+    TileNotes::Tile& note = notes.tile[i & 3];
+    const uint32_t apart = __builtin_popcountll(__ballot(!u.fits(size))) / 4;
+    const float most = reduce_lanes<64>(size, Max()), least = reduce_lanes<64>(size > 0.f ? size : 3e38f, Min());
+    if (lane == 0) {
+      atomicAdd(&note.apart, apart << (16 * side));
+      atomicMax(&note.most[side], __float_as_uint(most));
+      atomicMax(&note.least[side], ~__float_as_uint(least));
+    }
+  };
+  // Whether the tile's tokens fit the units, told to the workgroup if not.
+  auto measure = [&](int i, L& t) {
+    if (__any(!uk.fits(token_size(t.kp)) || !uv.fits(token_size(t.vp)))) {
+      empty_odd(i, t);
+      tell(i, 0, uk, token_size(t.kp));
+      tell(i, 1, uv, token_size(t.vp));
+    }
+  };
+  Sizes k_sizes, v_sizes;  // not CAREFUL: of all tokens, looked at in the end
+  auto collect = [&](const L& t) {
+    k_sizes.add(token_size(t.kp));
+    v_sizes.add(token_size(t.vp));
   };
   auto expand_side = [&](const uint32_t* words, const uint32_t* pairs, float down, char* row, int swz) {
 #pragma unroll
@@ -260,24 +304,46 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
   auto value_swz = [](int row) { return D == 64 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); };
   auto expand = [&](int i, const L& t) {
     char* base = lds + (i & 1) * 2 * SIDE;
-    expand_side(t.k, t.kp, uk.down, base + lt * ROW, key_swz(lt));
-    expand_side(t.v, t.vp, uv.down, base + SIDE + lt * ROW, value_swz(lt));
+    expand_side(t.k, t.kp, uk.down(), base + lt * ROW, key_swz(lt));
+    expand_side(t.v, t.vp, uv.down(), base + SIDE + lt * ROW, value_swz(lt));
   };
-  auto read_units = [&](int i) {
-    widen(uk, __uint_as_float(notes.key_size[i & 1]), 3, 8);
-    widen(uv, __uint_as_float(notes.value_size[i & 1]));
+  // CAREFUL: where tokens of a tile were found not to fit the units: others for most of them, and units of
+  // their own for the rest. Returns whether there may be such a rest.
+  auto settle = [&](int i, uint32_t apart, L& t) {
+    const int tokens = max(min(TILE, ex.kv - steps.base(i)), 0);
+    auto rest = [&](int side, int count, auto& u) {
+      if (2 * count <= tokens) return count > 0;
+      const TileNotes::Tile& note = notes.tile[i & 3];
+      const bool first = !u.set;  // then all that have a size have told it
+      u.take(__uint_as_float(note.most[side]));
+      return !first || !u.fits(__uint_as_float(note.most[side])) || !u.fits(__uint_as_float(~note.least[side]));
+    };
+    const bool keys = rest(0, apart & 0xFFFF, uk), values = rest(1, apart >> 16, uv);
+    if (!__builtin_amdgcn_readfirstlane(keys || values)) return false;
+    const int kd = uk.apart(token_size(t.kp)), vd = uv.apart(token_size(t.vp));
+#pragma unroll
+    for (int e = 0; e < L::PAIRS; ++e) {
+      t.kp[e] = pair_down(t.kp[e], kd);
+      t.vp[e] = pair_down(t.vp[e], vd);
+    }
+    if (tid % 4 == 0) notes.apart[i & 1][lt] = make_int2(kd, vd);
+    return true;
   };
+  auto tokens_apart = [&](int i) { return (uint32_t)__builtin_amdgcn_readfirstlane(notes.tile[i & 3].apart); };
 
-  f32x16_t o[DB];
+  f32x16_t(&o)[DB] = out.o;
 #pragma unroll
   for (int d = 0; d < DB; ++d)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
-  float m = neg_inf(), l = 0.f;
+  float &m = out.m, &l = out.l;
+  m = neg_inf();
+  l = 0.f;
   f32x16_t start;  // what a score's sum starts from: -m, over `wide`
 #pragma unroll
   for (int e = 0; e < 16; ++e) start[e] = 0.f;
-  int o_unit = 0;  // exponent of the outputs' unit
+  int& o_unit = out.unit;  // exponent of the outputs' unit
+  o_unit = 0;
 
   // Read offsets. Keys: row c of a block of 32 tokens, pieces 2 s + h. Values: see above.
   const int krow = c * ROW, kswz = key_swz(c);
@@ -286,27 +352,51 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
   const int vpiece = 2 * tg + ((tm & 3) >> 1), vswz = value_swz(tm >> 2), vhalf = 8 * (tm & 1);
 
   L t;
+  bool spread = false;  // some tokens of the tile being multiplied may have units of their own
   int page = 0;
   if (i0 < i1) {
     const int page0 = page_of(i0), page1 = page_of(i0 + 1);
     page = page_of(i0 + 2);
     __syncthreads();  // the notes are clear
     load(i0, page0, t);
-    measure(i0, t);
-    __syncthreads();
-    read_units(i0);
+    if constexpr (CAREFUL) {
+      empty_odd(i0, t);
+      tell(i0, 0, uk, token_size(t.kp));
+      tell(i0, 1, uv, token_size(t.vp));
+      __syncthreads();
+      if (const uint32_t apart = tokens_apart(i0)) spread = settle(i0, apart, t);
+    } else {
+      collect(t);
+      const float key = reduce_lanes<64>(k_sizes.most(), Max()), value = reduce_lanes<64>(v_sizes.most(), Max());
+      if (lane == 0) notes.first[wave] = make_float2(key, value);
+      __syncthreads();
+      float2 all = notes.first[0];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) {
+        all.x = fmaxf(all.x, notes.first[w].x);
+        all.y = fmaxf(all.y, notes.first[w].y);
+      }
+      uk.take(all.x);
+      uv.take(all.y);
+    }
     expand(i0, t);
     load(i0 + 1, page1, t);
-    measure(i0 + 1, t);
+    if constexpr (CAREFUL)
+      measure(i0 + 1, t);
+    else
+      collect(t);
   }
   int k_unit = uk.e, v_unit = uv.e;  // of the tile being multiplied
   int q_unit = k_unit;
+  if constexpr (!CAREFUL) o_unit = v_unit;
   convert_query(q_unit);
   for (int i = i0; i < i1; ++i) {
     wait_lds_barrier();
-    if (tid < 2) notes.bad[(i + 3) & 3][tid] = notes.gone[(i + 3) & 3][tid] = 0;
-    read_units(i + 1);
-    const int k_next = uk.e, v_next = uv.e;
+    if (tid < TileNotes::WORDS) reinterpret_cast<uint32_t*>(&notes.tile[(i + 3) & 3])[tid] = 0;
+    [[maybe_unused]] bool spread_next = false;
+    if constexpr (CAREFUL)
+      if (const uint32_t apart = tokens_apart(i + 1)) spread_next = settle(i + 1, apart, t);
+    [[maybe_unused]] const int k_next = uk.e, v_next = uv.e;
     expand(i + 1, t);
     load(i + 2, page, t);
     page = page_of(i + 3);
@@ -320,8 +410,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
       if (p.window > 0 && base + 63 <= lo_pos - p.window && base >= p.sinks) continue;
       const char* kb = lds + (i & 1) * 2 * SIDE + half * 64 * ROW;
       const char* vb = kb + SIDE;
-      const uint64_t bad = notes.bad[i & 3][half], gone = notes.gone[i & 3][half];
-      if (k_unit != q_unit) {
+      const uint64_t bad = CAREFUL ? notes.tile[i & 3].bad[half] : 0, gone = notes.tile[i & 3].gone[half];
+      if (CAREFUL && k_unit != q_unit) {
         q_unit = k_unit;
         load_query();
         convert_query(q_unit);
@@ -338,7 +428,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
                                                                            (((2 * s + h) ^ kswz) << 4)));
       };
       auto score = [&](int s, int tb, f16x8_t k) {
-        x[tb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[s], s ? x[tb] : start, 0, 0, 0);
+        x[tb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(k, q[s], s ? x[tb] : CAREFUL ? f32x16_t{} : start, 0, 0, 0);
       };
       if constexpr (D == 64) {
         // All keys of the half before the first product: the order below leaves each read to be
@@ -362,7 +452,19 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
         sched_products<AHEAD>();
       }
       __builtin_amdgcn_s_setprio(1);
-      if (any_wide) {
+      if constexpr (CAREFUL) {
+        // The scores stand alone: beside -m the small ones of small keys would be rounded. They become the
+        // exponents of what the values are multiplied by.
+        const int2* apart = notes.apart[i & 1] + 64 * half + 4 * opaque(h);
+        const float was = m == neg_inf() ? 0.f : m;
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int2 d = spread ? apart[32 * tb + 8 * (e >> 2) + (e & 3)] : make_int2(0, 0);
+            x[tb][e] = ldexpf(x[tb][e] * wide, d.x) - was + (float)d.y;
+          }
+      } else if (any_wide) {
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
@@ -397,7 +499,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
             x[tb][e] = !see ? neg_inf() : bad >> at & 1 ? quiet_nan() : x[tb][e];
           }
       }
-      if (v_unit != o_unit) {
+      if (CAREFUL && v_unit != o_unit) {
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -425,7 +527,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
       // scores as long as a half's probabilities neither near binary16's upper end nor become all small: a
       // sum from 2^-9 to 2^15.9 says so (32 of them round to 2^-25 at worst, 2^-11 of that together; none at
       // all are masked ones). Only past it is a maximum looked for.
-      if (__any(!(sum <= 61440.f) || (sum < 0x1p-9f && sum > 0.f) || m == neg_inf())) {
+      if (spread | __any(!(sum <= 61440.f) || (sum < 0x1p-9f && sum > 0.f) || m == neg_inf())) {
         float top = neg_inf();
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb)
@@ -438,7 +540,16 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
           up = seen ? top - 4.f : 0.f;
           m = seen ? up : m;
         } else {
-          const float room = room_below(across32(l, Add()), o_unit);
+          float sofar = l;
+          if constexpr (CAREFUL) {  // else none of the values is beyond 2^15 units
+            float most = opaque(0.f);
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) most = fmaxf(most, fabsf(o[d][e]));
+            sofar = fmaxf(sofar, most * 0x1p-15f);
+          }
+          const float room = room_below(across32(sofar, Max()));
           up = top > 4.f ? top - 4.f : seen && top < -4.f ? fmaxf(top - 4.f, -room) : 0.f;
           alpha = __builtin_amdgcn_exp2f(-up);
           m += up;
@@ -446,7 +557,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
         if (__any(up != 0.f)) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            start[e] = m == neg_inf() ? 0.f : -m / wide;
+            if constexpr (!CAREFUL) start[e] = m == neg_inf() ? 0.f : -m / wide;
             x[0][e] -= up;
             x[1][e] -= up;
           }
@@ -456,6 +567,15 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[d][e] *= alpha;
           exponentials();
+        }
+        if (spread) {  // the sum is of the probabilities alone
+          const int2* apart = notes.apart[i & 1] + 64 * half + 4 * opaque(h);
+          sum = 0.f;
+#pragma unroll
+          for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              sum += __builtin_amdgcn_exp2f(x[tb][e] - (float)apart[32 * tb + 8 * (e >> 2) + (e & 3)].y);
         }
       }
       l += sum;
@@ -477,10 +597,51 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
       });
       sched_products<V_AHEAD>();
     }
-    measure(i + 2, t);
-    k_unit = k_next;
-    v_unit = v_next;
+    if constexpr (CAREFUL) {
+      measure(i + 2, t);
+      k_unit = k_next;
+      v_unit = v_next;
+      spread = spread_next;
+    } else {
+      collect(t);
+    }
   }
+  if constexpr (!CAREFUL) {
+    if (__any(!k_sizes.fit(uk) || !v_sizes.fit(uv)) && lane == 0) notes.undone = 1;
+    __syncthreads();
+    return !__builtin_amdgcn_readfirstlane(notes.undone);
+  }
+  return true;
+}
+
+template <int D, int GS, int DT, int NW, int RW>
+__global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(AttentionParams p) {
+  constexpr bool PAIRED = RW < NW;
+  constexpr int ROW = D * 2, DB = D / 32;
+  __shared__ __attribute__((aligned(16))) char lds[kTileBytes<D, NW>];
+  __shared__ TileNotes notes;
+  static_assert(RW * 32 * ROW <= kTileBytes<D, NW> && (!PAIRED || RW * (D / 2 * 256 + 512) <= kTileBytes<D, NW>), "epilogue");
+  // The row tiles of a sequence and kv head on one XCD: its codes meet in one L2.
+  const int tid = threadIdx.x, workgroup = xcd_remap(blockIdx.x, gridDim.x);
+  const Rows<RW> own(p, tid, workgroup);
+  if (own.rows <= 0) return;
+  Gathered<D> got;
+  if (!gather_tiles<D, GS, DT, NW, RW, false>(p, own, tid, lds, notes, got)) {
+    __syncthreads();
+    const AttentionParams& again = params_again();
+    const int same = opaque(tid);
+    gather_tiles<D, GS, DT, NW, RW, true>(again, Rows<RW>(again, same, scalar_again(workgroup)), same, lds, notes, got);
+  }
+  f32x16_t(&o)[DB] = got.o;
+  float m = got.m, l = got.l;
+  int o_unit = got.unit;
+  const Work work = own.work;
+  const Extent ex = own.ex;
+  const int head = work.head, b = work.b;
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 31, h = lane >> 5;
+  const int wr = own.r0 + 32 * (wave % RW);
+  auto key_swz = [](int row) { return D == 64 ? (row >> 1) & 7 : row & 15; };
 
   l = across32(l, Add());
   if constexpr (PAIRED) {

@@ -236,3 +236,80 @@ def test_weight_on_one_token(kernel, D, at, bits, sinks):
             near(got[r, h], want, 1.01 * tol, f"head {h} of sequence {b}")
             total = torch.logsumexp(x, -1)
             near(lse[r, h], total, off[:, 0] + f32 * (n[:, 0] + 64) + 8 * f32 * total.abs(), "lse")
+
+
+def times(seq, side, tokens, factor):
+    """The keys (side 0) or values of those tokens of each sequence times a power of two."""
+    _, scale, bias = seq.sides[side]
+    for b, (_, kv) in enumerate(seq.lens):
+        for t in tokens:
+            if t < kv:
+                page, off = seq.table[b, t // seq.page].long(), t % seq.page
+                scale[page, :, off] *= factor
+                bias[page, :, off] *= factor
+
+
+def compare(seq, kernel, out=F32, only=None, window=0, sinks=0):
+    """Rows that `only` (of position and sequence) names, all without it, against 64 bits."""
+    scale = 1 / math.sqrt(seq.head_dim)
+    want, lse, tol, tol_lse = seq.reference(out, scale, window, sinks)
+    got, rows = T.attend(seq, seq.cache("cuda:0"), out, scale=scale, window=window, sinks=sinks, **bounds(kernel, seq))
+    ran(kernel)
+    keep = torch.ones(len(seq.q), dtype=torch.bool)
+    if only is not None:
+        for b, (nq, kv) in enumerate(seq.lens):
+            keep[int(seq.cu[b]):int(seq.cu[b + 1])] = only(torch.arange(kv - nq, kv))
+    assert keep.any()
+    near(got[keep], want[keep], tol[keep])
+    near(rows[keep], lse[keep], tol_lse[keep], "lse")
+
+
+EXTREMES = [2.0 ** 40, 2.0 ** 100, 2.0 ** -40, 2.0 ** -100]
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("D, group", [(64, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("factor", EXTREMES, ids=str)
+def test_extreme_token_after_a_query(kernel, D, group, factor):
+    """A row's result does not depend on a token behind it, whatever finite values that has."""
+    for first in (0, 150):
+        seq = U.Sequences([(45, first + 45), (1, 30)], q_heads=4, kv_heads=2, head_dim=D, group=group, page=16, dtype=BF16, seed=D)
+        at = first + 30
+        for side in range(2):
+            times(seq, side, [at, at + 5], factor)
+        compare(seq, kernel, only=lambda pos: pos < at)
+
+
+@pytest.mark.parametrize("kernel", ["rows", "tiles"])
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("factor", EXTREMES, ids=str)
+def test_extreme_token_before_the_window(kernel, nq, factor):
+    seq = U.Sequences([(nq, 400), (nq, 345)], q_heads=4, kv_heads=2, head_dim=128, group=64, page=32, dtype=BF16, seed=nq)
+    gone = [0, 1, 5, 283, 284, 230, 231, 232]
+    for side in range(2):
+        times(seq, side, gone, factor)
+    sees = lambda pos: ((torch.tensor(gone)[None] > pos[:, None] - 60)).any(-1)  # noqa: E731
+    compare(seq, kernel, only=lambda pos: ~sees(pos), window=60)
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("lens", [[(1, 700), (1, 40), (2, 3)], [(80, 300), (70, 70)]], ids=str)
+@pytest.mark.parametrize("factor", [2.0 ** 20, 2.0 ** 45, 2.0 ** 100, 2.0 ** -20, 2.0 ** -45, 2.0 ** -100], ids=str)
+@pytest.mark.parametrize("tokens", ["first", "one", "every other", "later half"])
+def test_values_of_many_sizes(kernel, lens, factor, tokens):
+    """Values of very different sizes that are seen: each as exact as its own size allows."""
+    seq = U.Sequences(lens, q_heads=4, kv_heads=2, head_dim=128, group=64, page=32, dtype=BF16, seed=2)
+    times(seq, 1, {"first": range(1), "one": [45], "every other": range(0, 800, 2), "later half": range(150, 800)}[tokens],
+          factor)
+    compare(seq, kernel)
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("lens", [[(1, 700), (1, 40), (2, 3)], [(80, 300), (70, 70)]], ids=str)
+@pytest.mark.parametrize("factor", [2.0 ** -12, 2.0 ** -20, 2.0 ** -60, 2.0 ** -100], ids=str)
+def test_keys_of_many_sizes(kernel, lens, factor):
+    """Small keys among large ones: every other token's, those of the first half, and one alone the larger."""
+    for tokens in (range(0, 800, 2), range(0, 150), [t for t in range(800) if t != 45]):
+        seq = U.Sequences(lens, q_heads=4, kv_heads=2, head_dim=64, group=64, page=32, dtype=BF16, seed=2)
+        times(seq, 0, tokens, factor)
+        compare(seq, kernel)
