@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import bit_matmul_amd as bm
+from tests import attn_exact as X
 from tests import attn_util as U
 from tests import test_attention_gpu as T
 from tests.test_attention_gpu import BF16, F16, F32, dev, near
@@ -313,3 +314,26 @@ def test_keys_of_many_sizes(kernel, lens, factor):
         seq = U.Sequences(lens, q_heads=4, kv_heads=2, head_dim=64, group=64, page=32, dtype=BF16, seed=2)
         times(seq, 0, tokens, factor)
         compare(seq, kernel)
+
+
+@pytest.mark.parametrize("window, sinks", X.WINDOWS)
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("name", list(X.CASES))
+def test_each_token_counts(name, kernel, window, sinks):
+    """tests/attn_exact.py; the rule's own kernel ("rows" stands for it) and the one for many rows."""
+    if window and kernel == "tiles, split":
+        pytest.skip("a window is not split")
+    seq = X.case(name)
+    got, lse = T.attend(seq, seq.cache("cuda:0"), F32, window=window, sinks=sinks, **bounds(kernel, seq))
+    if kernel != "rows":
+        ran(kernel)
+    got, lse = got.double().cpu(), lse.double().cpu()
+    for b, (nq, kv) in enumerate(seq.lens):
+        r = slice(int(seq.cu[b]), int(seq.cu[b + 1]))
+        runs, total = seq.counts(b, window, sinks)
+        for h in range(seq.q_heads):
+            want, want_lse = seq.expected(b, h * seq.kv_heads // seq.q_heads, runs, total)
+            assert ((got[r, h] - want).abs() <= X.OUT * want).all(), (b, h)
+            seen = total > 0
+            assert (lse[r, h][~seen] == -math.inf).all()
+            assert ((lse[r, h] - want_lse)[seen].abs() <= X.LSE).all(), (b, h)

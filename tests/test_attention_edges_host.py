@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import bit_matmul_amd as bm
+from tests import attn_exact as X
 
 
 def test_host_tensors_are_refused_on_any_stream():
@@ -32,3 +33,21 @@ def test_host_tensors_are_refused_on_any_stream():
         for options in ({}, dict(stream=0), dict(stream=0x1000)):
             with pytest.raises(ValueError, match="GPU|cuda"):
                 call(**options)
+
+
+@pytest.mark.parametrize("window, sinks", X.WINDOWS)
+@pytest.mark.parametrize("name", [n for n in X.CASES if not n[0].isdigit()])
+def test_a_lost_step_shows(name, window, sinks):
+    """The tolerances of tests/attn_exact.py are passed by any 32 tokens that are left out of the longest sequence, in
+    the output and in the lse of every row that sees one of them."""
+    seq = X.case(name)
+    b = max(range(len(seq.lens)), key=lambda i: seq.lens[i][1])
+    runs, total = seq.counts(b, window, sinks)
+    want, lse = seq.expected(b, 0, runs, total)
+    steps = -(-seq.lens[b][1] // X.STEP)
+    for lost in sorted({0, 1, steps // 3, steps // 2, steps - 2, steps - 1}):
+        less, left = seq.counts(b, window, sinks, lost)
+        out, short = seq.expected(b, 0, less, left)
+        sees = (runs - less).sum(-1) > 0
+        assert ((short - lse)[sees].abs() > 4 * X.LSE).all()
+        assert (((out - want).abs() > 4 * X.OUT * want).any(-1))[sees & (left > 0)].all()
