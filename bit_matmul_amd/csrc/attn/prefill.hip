@@ -4,9 +4,15 @@
 // s (c - 8) + (b + 8 s) two codes at a time; the products' sums are f32 and start from -m, so that
 // scores leave the matrix cores as the exponents of p = exp2(x - m). The sum of p is f32, taken
 // before the rounding; p is rounded to binary16 for the product with the values. m follows the
-// largest score only where a sum says that probabilities near the ends of binary16's range. Each of these roundings is 2^-12 of a value on
-// the average where the cache keeps 4 bits: with bf16 results the error is that of the result's
-// own rounding; binary16 results are off by 4.5e-4 of their size against 2.1e-4 for that alone.
+// largest score only where a sum says that probabilities near the ends of binary16's range. Each
+// of these roundings is 2^-12 of a value on the average where the cache keeps 4 bits: with bf16
+// results the error is that of the result's own rounding. Binary16 results would be off by 4.5e-4 of
+// their size against 2.1e-4 for their rounding alone. So with binary16 queries only values and
+// probabilities are rounded (3.0e-4): keys are s (c - 8) alone, which is exact, and b + 8 s goes through
+// one or two products more, in two parts, with the sums of the queries over each group; of the scores'
+// factor the queries take the power of two, and the scores the rest. That takes 3 to 7 % longer (4096
+// queries over 16384 tokens: 1.26 -> 1.32 ms). The factor on the keys instead, where f32 holds it, would
+// round the scales: 8.0e-4.
 //
 // Layout. A workgroup of eight waves (four for heads of 256 dims) takes up to 256 query rows of one
 // sequence and kv head (its new tokens times the query heads that share the kv head) and goes over
@@ -77,9 +83,14 @@ __device__ __forceinline__ void wait_lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// LDS of a workgroup: two tiles of keys and values.
+// LDS of a workgroup: two tiles of keys and values, and for binary16 results two of the keys' biases: four places
+// a group, in products' steps of 16.
 template <int D, int NW>
 constexpr int kTileBytes = NW * 64 * D * 2;
+template <int D, int GS, int DT>
+constexpr int kBiasSteps = DT == 1 ? (4 * D / GS + 15) / 16 : 0;
+template <int D, int GS, int DT, int NW>
+constexpr int kBiasBytes = NW * 32 * 32 * kBiasSteps<D, GS, DT>;
 
 // A workgroup's rows.
 template <int RW>
@@ -120,6 +131,10 @@ __device__ __forceinline__ bool gather_tiles(const AttentionParams& p, const Row
   constexpr int DB = D / 32;                  // blocks of output dims
   constexpr int V_AHEAD = 4;                  // value operands read before the first product
   static_assert(4 * SIDE == kTileBytes<D, NW>, "tiles");
+  // Binary16 results have bits enough to show the rounding of keys and of scaled queries.
+  constexpr bool EXACT = DT == 1;
+  constexpr int BS = kBiasSteps<D, GS, DT>, BIAS_ROW = 32 * BS;  // steps and bytes of a token's biases
+  static_assert(2 * TILE * BIAS_ROW == kBiasBytes<D, GS, DT, NW>, "biases");
   static_assert(!PAIRED || H == 2, "halves");
 
   const Work work = mine.work;
@@ -134,6 +149,9 @@ __device__ __forceinline__ bool gather_tiles(const AttentionParams& p, const Row
   const int32_t* table = p.page_table + (int64_t)b * p.pages_per_seq;
   if (tid < 4 * TileNotes::WORDS) reinterpret_cast<uint32_t*>(notes.tile)[tid] = 0;
   if (tid == 0) notes.undone = 0;
+  if constexpr (EXACT)  // also those that no group has
+    for (int at = 16 * tid; at < 2 * TILE * BIAS_ROW; at += 16 * L::THREADS)
+      *reinterpret_cast<u32x4_t*>(lds + 4 * SIDE + at) = u32x4_t{0, 0, 0, 0};
 
   // This wave's rows, and this lane's.
   const int wr = r0 + 32 * (wave % RW);
@@ -142,13 +160,16 @@ __device__ __forceinline__ bool gather_tiles(const AttentionParams& p, const Row
   const int hi_pos = position(ex, min(wr + 31, ex.rows - 1) / p.share);
   const int pos = position(ex, min(wr + c, ex.rows - 1) / p.share);
 
-  // The row as binary16 and times the scores' scale, for keys in units of 2^k_unit, so that the
+  // The row as binary16 and times the scores' factor, for keys in units of 2^k_unit, so that the
   // products are base-2 logarithms as they stand. Where that would pass binary16's range (scores
   // of 10^5 and more) the row is taken 2^-r fold, and its scores 2^r fold (`wide`). So it is where it
-  // would near the other end (scores below 2^-4, but for tokens of a larger unit of their own).
+  // would near the other end (scores below 2^-4, but for tokens of a larger unit of their own). EXACT: times
+  // the factor's power of two alone, the rest of which is in `wide`.
   f16x8_t q[D / 16];
+  [[maybe_unused]] f16x8_t q_sums[EXACT ? BS : 1];
   float wide = 1.f;
-  bool any_wide = false;
+  bool any_wide = EXACT;
+  const float factor = p.scale * kLog2e;
   auto load_query = [&] {  // as it is
     const RowOf row(p, head, opaque(min(wr + c, ex.rows - 1)));
     const uint16_t* qrow = p.q + (int64_t)(ex.q0 + row.i) * p.q_stride + (int64_t)row.head * D;
@@ -167,15 +188,20 @@ __device__ __forceinline__ bool gather_tiles(const AttentionParams& p, const Row
         big = fmaxf(big, fmaxf(fabsf(x), fabsf(y)));
       }
     }
-    const float factor = p.scale * kLog2e;
     big = across32(big, Max());
     int r = 0;
     if (big > 0.f && big < __uint_as_float(0x7F800000u) && factor != 0.f) {
       const int end = __builtin_amdgcn_frexp_expf(big) + __builtin_amdgcn_frexp_expf(factor) + k_unit;
       r = end > 15 ? end - 15 : end < -7 ? max(end, -80) : 0;
     }
+    int unit = k_unit - r;
     wide = ldexpf(1.f, r);
-    any_wide = __any(r != 0);
+    if constexpr (EXACT) {
+      unit = factor != 0.f ? unit + __builtin_amdgcn_frexp_expf(factor) : -300;
+      wide *= factor != 0.f ? __builtin_amdgcn_frexp_mantf(factor) : 1.f;
+    } else {
+      any_wide = __any(r != 0);
+    }
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
       const u32x4_t raw = __builtin_bit_cast(u32x4_t, q[s]);
@@ -183,7 +209,34 @@ __device__ __forceinline__ bool gather_tiles(const AttentionParams& p, const Row
 #pragma unroll
       for (int e = 0; e < 4; ++e) unpack_half2<DT>(raw[e], x[2 * e], x[2 * e + 1]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[s][e] = (_Float16)ldexpf(x[(e & 1) * 4 + e / 2] * factor, k_unit - r);
+      for (int e = 0; e < 8; ++e) {
+        const float y = x[(e & 1) * 4 + e / 2];
+        q[s][e] = (_Float16)ldexpf(EXACT ? y : y * factor, unit);
+      }
+    }
+    if constexpr (EXACT) {
+      constexpr int NG = D / GS, STEPS = GS / 16;
+      float sum[4 * BS];  // of the groups, over their dims' number
+#pragma unroll
+      for (int y = 0; y < 4 * BS; ++y) {
+        sum[y] = 0.f;
+        if (y < NG) {
+#pragma unroll
+          for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[y] += (float)q[y * STEPS + s][e];
+          sum[y] = across32(sum[y], Add()) * (1.f / GS);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < BS; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float y = h ? sum[4 * t + 2 + e] : sum[4 * t + e];
+          const _Float16 hi = (_Float16)y, lo = (_Float16)(y - (float)hi);
+          q_sums[t][4 * e] = q_sums[t][4 * e + 1] = hi;
+          q_sums[t][4 * e + 2] = q_sums[t][4 * e + 3] = lo;
+        }
     }
   };
   load_query();
@@ -302,9 +355,35 @@ __device__ __forceinline__ bool gather_tiles(const AttentionParams& p, const Row
   };
   auto key_swz = [](int row) { return D == 64 ? (row >> 1) & 7 : row & 15; };
   auto value_swz = [](int row) { return D == 64 ? 4 * ((row >> 1) & 1) : 4 * (row & 3); };
+  // EXACT: a scale's 8 bits times a code less eight are within binary16's 11. What is left of a key is the same for
+  // all dims of a group, b + 8 s: times their number and as two parts, twice, for the queries' sums over it.
+  [[maybe_unused]] char* biases = lds + 4 * SIDE;
+  [[maybe_unused]] auto expand_keys = [&](const L& t, char* row, char* bias_row) {
+#pragma unroll
+    for (int e = 0; e < L::PAIRS; ++e) {
+      const float s = bf16_lo(t.kp[e]) * uk.down(), b = fmaf(8.f, s, bf16_hi(t.kp[e]) * uk.down()) * GS;
+      const f16x2_t s2 = splat_f16(s);
+      constexpr int PER = L::W / L::PAIRS;
+#pragma unroll
+      for (int f = e * PER; f < (e + 1) * PER; ++f) {
+        const uint32_t w = t.k[f], w8 = w >> 8;
+        const u32x4_t a = {as_u32(codes_low(w) * s2), as_u32(codes_high(w) * s2), as_u32(codes_low(w8) * s2),
+                           as_u32(codes_high(w8) * s2)};
+        *reinterpret_cast<u32x4_t*>(row + (((lw + f) ^ key_swz(lt)) << 4)) = a;
+      }
+      if ((lw + e * PER) * 8 % GS == 0) {
+        const _Float16 hi = (_Float16)b;
+        const uint32_t parts = as_u32(f16x2_t{hi, (_Float16)(b - (float)hi)});
+        *reinterpret_cast<u32x2_t*>(bias_row + (lw + e * PER) * 8 / GS * 8) = u32x2_t{parts, parts};
+      }
+    }
+  };
   auto expand = [&](int i, const L& t) {
     char* base = lds + (i & 1) * 2 * SIDE;
-    expand_side(t.k, t.kp, uk.down(), base + lt * ROW, key_swz(lt));
+    if constexpr (EXACT)
+      expand_keys(t, base + lt * ROW, biases + ((i & 1) * TILE + lt) * BIAS_ROW);
+    else
+      expand_side(t.k, t.kp, uk.down(), base + lt * ROW, key_swz(lt));
     expand_side(t.v, t.vp, uv.down(), base + SIDE + lt * ROW, value_swz(lt));
   };
   // CAREFUL: where tokens of a tile were found not to fit the units: others for most of them, and units of
@@ -450,6 +529,16 @@ __device__ __forceinline__ bool gather_tiles(const AttentionParams& p, const Row
           sched_reads<1>();
         });
         sched_products<AHEAD>();
+      }
+      if constexpr (EXACT) {
+        const char* rows_at = biases + ((i & 1) * TILE + half * 64 + c) * BIAS_ROW + 16 * h;
+#pragma unroll
+        for (int t = 0; t < BS; ++t)
+#pragma unroll
+          for (int tb = 0; tb < 2; ++tb)
+            x[tb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                __builtin_bit_cast(f16x8_t, *reinterpret_cast<const u32x4_t*>(rows_at + tb * 32 * BIAS_ROW + 32 * t)), q_sums[t],
+                x[tb], 0, 0, 0);
       }
       __builtin_amdgcn_s_setprio(1);
       if constexpr (CAREFUL) {
@@ -618,7 +707,7 @@ template <int D, int GS, int DT, int NW, int RW>
 __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(AttentionParams p) {
   constexpr bool PAIRED = RW < NW;
   constexpr int ROW = D * 2, DB = D / 32;
-  __shared__ __attribute__((aligned(16))) char lds[kTileBytes<D, NW>];
+  __shared__ __attribute__((aligned(16))) char lds[kTileBytes<D, NW> + kBiasBytes<D, GS, DT, NW>];
   __shared__ TileNotes notes;
   static_assert(RW * 32 * ROW <= kTileBytes<D, NW> && (!PAIRED || RW * (D / 2 * 256 + 512) <= kTileBytes<D, NW>), "epilogue");
   // The row tiles of a sequence and kv head on one XCD: its codes meet in one L2.
@@ -744,7 +833,7 @@ hipError_t launch_tiles(const AttentionParams& p, unsigned workgroups, int dtype
     hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 0, NW, RW>), grid, dim3(64 * NW), 0, stream, p);
   else
     hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 1, NW, RW>), grid, dim3(64 * NW), 0, stream, p);
-  launch_log(grid, dim3(64 * NW), (size_t)(NW * 64 * D * 2 + sizeof(TileNotes)),
+  launch_log(grid, dim3(64 * NW), (size_t)(NW * 64 * D * 2 + (dtype ? kBiasBytes<D, GS, 1, NW> : 0) + sizeof(TileNotes)),
              "attention_tiles_kernel<%d, %d, %d, %d, %d>", D, GS, dtype, NW, RW);
   return hipGetLastError();
 }

@@ -337,3 +337,18 @@ def test_each_token_counts(name, kernel, window, sinks):
             seen = total > 0
             assert (lse[r, h][~seen] == -math.inf).all()
             assert ((lse[r, h] - want_lse)[seen].abs() <= X.LSE).all(), (b, h)
+
+
+@pytest.mark.parametrize("kernel", ["rows", "tiles"])
+@pytest.mark.parametrize("D, group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (256, 32), (256, 64), (256, 128)])
+def test_error_of_binary16_results(kernel, D, group):
+    """Over all, at most twice what the rounding of the result gives alone. A value has two roundings and its
+    probability one, each of which is in the mean, token by token, what the result's is relative to the same sum: three
+    and the result's own add up to sqrt(4) of it. Scores add nothing: their roundings have to be far below."""
+    seq = U.Sequences([(100, 700)] if kernel == "tiles" else [(4, 700), (1, 550)], q_heads=4, kv_heads=2, head_dim=D, group=group,
+                      page=16, dtype=F16, seed=D + group)
+    want, _, _, _ = seq.reference(F16, 1 / math.sqrt(D))
+    got, _ = T.attend(seq, seq.cache("cuda:0"), F16, scale=1 / math.sqrt(D), **bounds(kernel, seq))
+    ran(kernel)
+    off = (got.double().cpu() - want).norm()
+    assert off <= 2 * (want.to(F16).double() - want).norm(), (off / want.norm()).item()
