@@ -27,9 +27,11 @@
 // registers. Where they lie is held in scalar registers: 16 tokens of a half step share a page.
 //
 // What bounds it: with a long cache, HBM and the vector units together. Four sequences of 131072
-// tokens, 40 heads over 8 of 128 dims, groups of 64: 604 MB in 120 us, 5.0 TB/s, with vector
-// instructions issued in 61 % of the cycles; 6 us more for the join. Expanding keys and values to
-// binary16 with their scales, as the kernel for many rows does, took 217 us.
+// tokens, 40 heads over 8 of 128 dims, groups of 64: 604 MB in 121 us, 5.0 TB/s, with vector
+// instructions issued in 64 % of the cycles; 6 us more for the join. Expanding keys and values to
+// binary16 with their scales, as the kernel for many rows does, took 217 us. With short or windowed
+// spans, latency: vector instructions in 50 % (32 ragged sequences) and 46 % (windows of 4096 at 256
+// dims) of the cycles, waves waiting in 39 % and 37 % of theirs.
 #include "attention.hpp"
 
 #include <algorithm>
@@ -703,7 +705,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionParams p) 
     const int64_t at = s * all + row;
     const float2 part = ml[at];
     const f32x4_t o = *reinterpret_cast<const f32x4_t*>(p.part_o + at * D + 4 * t);
-    if (part.y == 0.f) continue;  // saw nothing: the outputs were not written
+    if (part.y == 0.f) continue;  // saw nothing
     const float w = part.x == mt ? 1.f : __builtin_amdgcn_exp2f(part.x - mt);
     lt += part.y * w;
 #pragma unroll
@@ -763,26 +765,28 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
   const int64_t tiles16 = (rows + kRows - 1) / kRows, steps = (span + kStep - 1) / kStep;
   // The kernel for few rows starts and ends sooner, and spreads over more CUs; tiles of many rows
   // read and expand the cache once for all of them. Up to 64 rows, or 64 steps for each CU, the
-  // first (40 heads over 8 of 128 dims, by queries of a sequence: 64 after 600 tokens 11 us against
-  // 27, 300 after 600 20 against 41, 64 after 4096 33 against 35; 32 sequences of 12 after 2048 59
-  // against 56), above that the second (32 sequences of 16 after 2048: 57 us against 112; 600 of
-  // 600: 25 against 42; 160 after 4096: 47 against 65).
+  // first, above that the second. Both sides, in us, for the last n of m tokens of one sequence, 40 heads
+  // over 8 of 128 dims: 64 of 600 11 and 24, 300 of 600 19 and 24, 48 of 4096 28 and 31, 8 sequences' 12 of
+  // 2048 31 and 31, 32 sequences' 4 of 2048 45 and 54; then 64 of 4096 33 and 33, 600 of 600 40 and 25, 160 of
+  // 4096 63 and 47, 32 sequences' 16 of 2048 112 and 57. Where 49 to 64 rows of many sequences make four row
+  // tiles, the rule takes the slower: 32 sequences' 12 of 2048 63 and 57.
   plan.tiles = rows > 64 && (double)groups * tiles16 * steps > 64 * CUS;
   plan.waves = 0;
   int64_t rows_each, fill, most;  // fill: workgroups at a time; most: parts of a tile's tokens
   if (plan.tiles) {
     // 256 rows a workgroup where that still gives every CU one, else half of them, with two waves
-    // for each 32 rows (a prompt of 600 tokens, 40 heads over 8: 26 us against 30).
+    // for each 32 rows (a prompt of 600 tokens, 40 heads over 8: 25 us against 30; always half, at 64 dims:
+    // ragged windowed chunks 150 against 102).
     rows_each = head_dim == 256 || groups * ((rows + 255) / 256) < CUS ? 128 : 256;
     fill = CUS;
-    // Over short spans the join costs more than the split saves (300 after 600: 41 us against 25).
+    // Over short spans the join costs more than the split saves (400 of 1600 tokens: 56 us against 43).
     most = span < 2048 ? 1 : span / 512;
   } else {
     // Few short sequences, as many workgroups as the chip holds at a time: eight waves each and no
-    // joining launch (573 tokens, 8 kv heads: 10.6 us against 7.8 + 3.5; 160 queries after 600
-    // tokens: 17 against 27). Otherwise four waves, and splits until the workgroups fill the chip once,
+    // joining launch (573 tokens, 8 kv heads: 9.5 us against 10.2 of four waves and the join; 160 of 600
+    // tokens: 16 against 27). Otherwise four waves, and splits until the workgroups fill the chip once,
     // as many as registers and LDS let a CU hold: at twice as many the second half waits (decode
-    // of 64 sequences, head dim 256: 61 us against 50). A wave has at least one step.
+    // of 64 sequences, head dim 256: 60 us against 51). A wave has at least one step.
     plan.waves = groups * tiles16 <= (head_dim == 256 ? CUS : 2 * CUS) && steps <= 32 ? 8 : 4;
     rows_each = kRows;
     fill = plan.waves == 8 ? 1 : head_dim == 256 ? 2 * CUS : 4 * CUS;
@@ -791,7 +795,7 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
   plan.rows_each = (int)rows_each;
   plan.row_tiles = (int)((rows + rows_each - 1) / rows_each);
   // Whole rounds of workgroups run as they are; the tiles left over for the last, partial round
-  // are split so that they fill it.
+  // are split so that they fill it (4096 of 16384 tokens: 1.34 -> 1.24 ms).
   const int64_t whole = std::min<int64_t>(plan.row_tiles, groups * plan.row_tiles / fill * fill / groups);
   plan.tail_tiles = (int)(plan.row_tiles - whole);
   plan.splits = plan.tail_tiles > 0 ? (int)std::min<int64_t>({fill / (groups * plan.tail_tiles), most, 128}) : 1;
@@ -800,9 +804,9 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
     plan.tail_tiles = 0;
   }
   // One row tile of each of several sequences: the workgroups are shared out by what each has to
-  // do, which the kernels find from the lengths, join included, for 2 us. 32 sequences of 512
-  // tokens but one of 32768: 120 us as equal splits, 32 so; of 1024 to 4096: 38 against 35; all of
-  // 4096: 42 against 44. A wave looks at 64 sequences, with step counts that add up in 31 bits.
+  // do, which the kernels find from the lengths, join included, for 1 us. 32 sequences of 512
+  // tokens but one of 32768: 103 us as equal splits, 28 so; of 1024 to 4096: 38 against 34; all of
+  // 4096: 41 against 42. A wave looks at 64 sequences, with step counts that add up in 31 bits.
   plan.balanced = !plan.tiles && plan.row_tiles == 1 && plan.splits > 1 && B > 1 && B <= 64 &&
                   B * (max_kv / kStep + 2) <= INT32_MAX;
   plan.tail_rows = (int)std::min<int64_t>(rows, plan.tail_tiles * rows_each);

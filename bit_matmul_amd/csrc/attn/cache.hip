@@ -7,9 +7,9 @@
 // it comes near the border of two, and the product with a reciprocal elsewhere.
 //
 // What bounds them: HBM, in requests as short as a slot's codes (head_dim / 2 bytes) and pairs.
-// 8192 tokens of 8 heads of 128 dims, scattered over pages: append 43 MB in 17.5 us, 2.5 TB/s;
-// read 43 MB in 11 us, 3.9 TB/s. One thread for both sides' pieces keeps two loads in flight and
-// finds the slot once.
+// 8192 tokens of 8 heads of 128 dims, scattered over pages: append 43 MB in 17 us, 2.5 TB/s, where
+// the loads also wait for the slot; read 43 MB in 12 us, 3.6 TB/s. One thread for both sides' pieces
+// keeps two loads in flight and finds the slot once.
 #include "attn.hpp"
 
 namespace bitmm {

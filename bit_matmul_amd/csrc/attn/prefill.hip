@@ -31,9 +31,10 @@
 // keys and queries alike; outputs are put in order when they are stored.
 //
 // What bounds it: the two waves of a SIMD between matrix cores and vector units. 4096 queries at
-// the end of 16384 tokens, 40 heads over 8 of 128 dims: 1.27 ms and 35 us for the join of the last
-// round's split tiles, 0.95 PFLOP/s, with the matrix cores busy in 44 % of the cycles (1.0 ms with
-// nothing but the products and their reads) and vector instructions issued in 40 %. Measured slower:
+// the end of 16384 tokens, 40 heads over 8 of 128 dims: 1.2 ms, 35 us of it for the join of the last
+// round's split tiles, 1.0 PFLOP/s, with the matrix cores busy in 44 % of the cycles (1.0 ms with
+// nothing but the products and their reads) and vector instructions issued in 45 %. LDS is busy in 39 % of
+// them, 29 % of that with bank conflicts. Measured slower:
 // the next scores formed beside the softmax of the last (1.9 ms), waves in two sets that take turns
 // behind barriers (2.1 ms), 64 tokens between barriers and a maximum looked for each time (1.53 ms).
 #include "attention.hpp"

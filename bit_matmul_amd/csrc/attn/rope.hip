@@ -13,9 +13,10 @@
 // position 2^20 an f32 product is off by up to 2^-5 radians. The fraction goes to sincospi
 // in f32.
 //
-// What bounds it: HBM. 8191 tokens of 16 + 2 heads of 256 dims: 151 MB in 30.5 us, 4.95 TB/s, the
+// What bounds it: HBM. 8191 tokens of 16 + 2 heads of 256 dims: 151 MB in 31 to 35 us, 4.3 to 4.9 TB/s, the
 // rate of a large copy (4.86); the heads of the next turn are loaded before the present ones are
-// finished. 8 tokens of 40 + 8 heads: 4 us, a launch and the latency of a load and a store.
+// finished. 8 tokens of 40 + 8 heads: 4 us, a launch and the latency of a load and a store. 600 tokens of
+// them: 7 us, where three waves a token take four turns each.
 #include "attn.hpp"
 
 namespace bitmm {

@@ -140,11 +140,12 @@ size_t bitmm_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t max_q, i
  * need no entry in the table. Rows of q that belong to no sequence are not written.
  * Scores, softmax and sums are f32; keys, values and probabilities enter the matrix cores
  * as binary16, and so do bf16 queries times `scale` in the form for many query rows (with
- * binary16 ones neither they nor keys are rounded there). Units are chosen from the stored scales so that a token's key and value have 11 bits, or an error of
- * 2^-18, of the largest 15 |scale| + |bias| among its head's groups, whatever other tokens
- * hold; probabilities have 11 bits, or an error of 2^-11 of the weight of 32 tokens near
- * them. Which form runs, how the tokens are split, and with it the
- * order of sums, follows from the arguments and all the lengths of the call.
+ * binary16 ones neither they nor keys are rounded there). Units are chosen from the stored
+ * scales so that a token's key and value have 11 bits, or an error of 2^-18, of the largest
+ * 15 |scale| + |bias| among its head's groups, whatever other tokens hold; probabilities have
+ * 11 bits, or an error of 2^-11 of the weight of 32 tokens near them. Which form runs, how the
+ * tokens are split, and with it the order of sums, follows from the arguments and all the
+ * lengths of the call; the values decide whether its units need a second pass over the tokens.
  * `workspace`: caller-owned device memory of bitmm_kv_attention_workspace_bytes(...) bytes,
  * 16-byte aligned, no initialisation needed (NULL if that is 0); two calls that share it
  * must be ordered on one stream.
