@@ -34,6 +34,11 @@ Also reported:
       ``--cpu-seconds``; ``per_config`` times one bounded sample of every workload on
       all cores and, for the tiny, hidden-5120 and 8-bit GEMVs, on one core.
 
+The one JSON line on stdout holds the headline, its roofline, the ceilings and each
+workload's time and rates: a few KB, which a log's tail keeps whole. ``--record FILE``
+writes the whole record (rooflines, launches, counters and repeats of every workload,
+``per_config``), 25 KB.
+
 Profiling helpers (no GPU needed for the second):
   ``--only NAMES``: run only the suite workloads whose names contain one of the
       comma-separated strings (no headline, no CPU legs): one workload per process
@@ -49,7 +54,7 @@ Profiling helpers (no GPU needed for the second):
 
 Usage: python bench.py [--gpus 1] [--steps K] [--warmup W] [--repeats R] [--no-suite]
                        [--no-cpu] [--no-ceilings] [--calibrate-copy] [--only NAMES]
-                       [--markers] [--summarize DIR [--bench-json FILE] [--workload NAME]
+                       [--markers] [--record FILE] [--summarize DIR [--bench-json FILE] [--workload NAME]
                                                     [--title TEXT] [--command CMD]]
 """
 
@@ -763,6 +768,21 @@ def summarize_profile(d: str, bench_json: str | None, command: str | None,
 
 # ---------------------------------------------------------------------------
 
+# What the printed line keeps of a workload: what --summarize reads, and the metric's rates.
+LINE_FIELDS = ("workload", "us_per_launch", "GB_s", "hbm_frac", "TFLOP_s", "mfma_frac", "bytes")
+
+
+def printed(record: dict) -> dict:
+    """The part of the whole record that goes into the line on stdout."""
+    out = dict(record)
+    for key in ("per_kernel", "suite"):
+        if key in record:
+            out[key] = [{f: e[f] for f in LINE_FIELDS if f in e} for e in record[key]]
+    if record.get("cpu_baseline"):
+        out["cpu_baseline"] = {k: v for k, v in record["cpu_baseline"].items() if k != "per_config"}
+    return out
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--gpus", type=int, default=1)
@@ -775,6 +795,7 @@ def main():
     ap.add_argument("--cpu-seconds", type=float, default=10.0)
     ap.add_argument("--only", default=None)
     ap.add_argument("--markers", action="store_true")
+    ap.add_argument("--record", default=None, metavar="FILE")
     ap.add_argument("--summarize", default=None, metavar="DIR")
     ap.add_argument("--bench-json", default=None)
     ap.add_argument("--command", default=None)
@@ -945,7 +966,10 @@ def main():
     elif only is None:
         result["cpu_baseline"] = None
 
-    print(json.dumps(result), flush=True)
+    if args.record:
+        with open(args.record, "w") as f:
+            f.write(json.dumps(result) + "\n")
+    print(json.dumps(printed(result)), flush=True)
 
 
 if __name__ == "__main__":
