@@ -1,0 +1,68 @@
+// C ABI of include/bitmm_beam.h: argument validation and dispatch, as in attn_api.cpp.
+#include "bitmm_beam.h"
+
+#include "beam.hpp"
+#include "checks.hpp"
+
+using namespace bitmm::attn;
+
+extern "C" {
+
+bitmm_status bitmm_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                       const void* v, int64_t v_stride, const void* q_weight,
+                                       const void* k_weight, const int32_t* positions,
+                                       const float* inv_freq, void* q_out, int64_t q_out_stride,
+                                       const int64_t* slots, const bitmm_kv_cache* cache, int64_t T,
+                                       int64_t q_heads, int64_t rot_dim, int interleaved, float eps,
+                                       float weight_offset, float rope_scale, bitmm_dtype dtype,
+                                       uint32_t* status, void* stream) {
+  try {
+    bitmm::launch_log_begin();
+    bitmm_status st = check_cache(cache);
+    if (st != BITMM_OK) return st;
+    if (!dtype_ok(dtype)) return BITMM_ERR_UNSUPPORTED;
+    const int64_t D = cache->head_dim, kv_heads = cache->kv_heads;
+    if (!fits_int(T) || !fits_int(q_heads)) return BITMM_ERR_SHAPE;
+    if (rot_dim < 0 || rot_dim > D || rot_dim % 8 != 0) return BITMM_ERR_SHAPE;
+    if (T * (q_heads + kv_heads) >= (int64_t)1 << 30) return BITMM_ERR_SHAPE;
+    if (T == 0) return BITMM_OK;
+    if (q_heads > 0) {
+      if ((st = check_rows(q, q_stride, q_heads, D)) != BITMM_OK) return st;
+      if ((st = check_rows(q_out, q_out_stride, q_heads, D)) != BITMM_OK) return st;
+    }
+    if ((st = check_rows(k, k_stride, kv_heads, D)) != BITMM_OK) return st;
+    if ((st = check_rows(v, v_stride, kv_heads, D)) != BITMM_OK) return st;
+    if (!slots || (rot_dim > 0 && (!positions || !inv_freq))) return BITMM_ERR_NULL;
+    if (!aligned(q_weight, 2) || !aligned(k_weight, 2) || !aligned(positions, 4) || !aligned(inv_freq, 4) ||
+        !aligned(slots, 8) || !aligned(status, 4))
+      return BITMM_ERR_ALIGN;
+    if ((st = device_check()) != BITMM_OK) return st;
+    RopeAppendParams p = {};
+    p.rope.q = static_cast<const uint16_t*>(q);
+    p.rope.k = static_cast<const uint16_t*>(k);
+    p.rope.q_weight = static_cast<const uint16_t*>(q_weight);
+    p.rope.k_weight = static_cast<const uint16_t*>(k_weight);
+    p.rope.positions = positions;
+    p.rope.inv_freq = inv_freq;
+    p.rope.q_out = static_cast<uint16_t*>(q_out);
+    p.rope.q_stride = q_stride;
+    p.rope.k_stride = k_stride;
+    p.rope.q_out_stride = q_out_stride;
+    p.rope.T = (int)T;
+    p.rope.q_heads = (int)q_heads;
+    p.rope.rot_dim = (int)rot_dim;
+    p.rope.eps = eps;
+    p.rope.weight_offset = weight_offset;
+    p.rope.rope_scale = rope_scale;
+    p.v = static_cast<const uint16_t*>(v);
+    p.v_stride = v_stride;
+    p.slots = slots;
+    p.cache = view(cache);
+    p.status = status;
+    return launched(launch_qk_norm_rope_append(p, interleaved != 0, (int)dtype, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return BITMM_ERR_LAUNCH;
+  }
+}
+
+}  // extern "C"

@@ -1,0 +1,85 @@
+"""Refusals of the calls of include/bitmm_beam.h, without a GPU: each bad argument is turned down with
+its status before the device is touched. Pointers are made up: validation follows none."""
+
+import os
+import re
+
+import pytest
+import torch
+
+import bit_matmul_amd as bm
+from tests.test_attention_host import CACHE_FAULTS, P, cache, status
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def L():
+    return bm.lib()
+
+
+def test_exports_every_declared_function(L):
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "bitmm_beam.h")).read(), flags=re.S)
+    names = set(re.findall(r"\b(bitmm_\w+)\s*\(", text))
+    assert names
+    for n in names:
+        assert hasattr(L, n) and n in bm.__all__
+
+
+def rope_append(L, desc="", **kw):
+    d = dict(q=P, qs=1024, k=P, ks=256, v=P, vs=256, qw=P, kw=P, pos=P, freq=P, qo=P, qos=1024, slots=P,
+             cache=cache() if desc == "" else desc, T=4, hq=8, rot=128, il=0, eps=1e-6, off=0.0, scale=1.0, dtype=0,
+             status=None, stream=None)
+    d.update(kw)
+    return L.bitmm_qk_norm_rope_append(*d.values())
+
+
+@pytest.mark.parametrize("kw, want", [
+    (dict(dtype=2), "UNSUPPORTED"), (dict(T=-1), "SHAPE"), (dict(hq=-1), "SHAPE"), (dict(rot=136), "SHAPE"),
+    (dict(rot=-8), "SHAPE"), (dict(rot=12), "SHAPE"), (dict(T=2 ** 30), "SHAPE"), (dict(T=2 ** 27), "SHAPE"),
+    (dict(hq=2 ** 29), "SHAPE"), (dict(qs=1016), "SHAPE"), (dict(ks=248), "SHAPE"), (dict(vs=248), "SHAPE"),
+    (dict(qs=1028), "ALIGN"), (dict(vs=260), "ALIGN"), (dict(q=P + 2), "ALIGN"), (dict(v=P + 8), "ALIGN"),
+    (dict(qo=P + 8), "ALIGN"), (dict(qw=P + 1), "ALIGN"), (dict(pos=P + 2), "ALIGN"), (dict(freq=P + 1), "ALIGN"),
+    (dict(slots=P + 4), "ALIGN"), (dict(status=P + 2), "ALIGN"), (dict(q=None), "NULL"), (dict(qo=None), "NULL"),
+    (dict(k=None), "NULL"), (dict(v=None), "NULL"), (dict(slots=None), "NULL"), (dict(pos=None), "NULL"),
+    (dict(freq=None), "NULL"), (dict(desc=None), "NULL"),
+])
+def test_rope_append_refusals(L, kw, want):
+    assert rope_append(L, **kw) == status(want)
+    assert bm.bitmm_last_launches() == []
+
+
+@pytest.mark.parametrize("kw, want", CACHE_FAULTS)
+def test_rope_append_cache_faults(L, kw, want):
+    assert rope_append(L, desc=cache(**kw)) == status(want)
+
+
+def test_rope_append_empty_and_without_a_device(L):
+    assert rope_append(L, T=0, q=None, k=None, v=None, slots=None) == bm.BITMM_OK
+    if not torch.cuda.is_available():
+        assert rope_append(L) == bm.BITMM_ERR_DEVICE
+        assert rope_append(L, hq=0, q=None, qo=None, rot=0, pos=None, freq=None, qw=None, kw=None) == bm.BITMM_ERR_DEVICE
+
+
+class _Host:
+    """What the binding asks of a cache, without device memory."""
+    kv_heads, head_dim, group_size, page_size, device_index = 2, 64, 32, 16, -1
+    desc = None
+
+
+def test_binding_refuses():
+    bf, i64, i32 = torch.bfloat16, torch.int64, torch.int32
+    q, k, v = (torch.zeros(3, n, 64, dtype=bf) for n in (4, 2, 2))
+    slots, pos, freq = torch.zeros(3, dtype=i64), torch.zeros(3, dtype=i32), torch.zeros(32)
+
+    def call(q=q, k=k, v=v, qw=None, kw=None, pos=pos, freq=freq, q_out=q, slots=slots):
+        return bm.bitmm_qk_norm_rope_append(q, k, v, qw, kw, pos, freq, q_out, slots, _Host())
+
+    for error, kw in [(TypeError, dict(k=k.float())), (TypeError, dict(v=v.half())), (TypeError, dict(q=q.half())),
+                      (TypeError, dict(slots=slots.int())), (TypeError, dict(pos=pos.long())), (TypeError, dict(freq=freq.half())),
+                      (ValueError, dict(k=k[:2])), (ValueError, dict(v=v[:, :1])), (ValueError, dict(q=q[:, :, :32])),
+                      (ValueError, dict(q=None)), (ValueError, dict(q_out=None)), (ValueError, dict(pos=pos[:2])),
+                      (ValueError, dict(qw=torch.zeros(32, dtype=bf))), (ValueError, dict(k=k.transpose(0, 1).contiguous().transpose(0, 1))),
+                      (ValueError, {})]:   # the last: tensors that are not on the GPU
+        with pytest.raises(error):
+            call(**kw)
