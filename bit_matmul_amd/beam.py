@@ -12,15 +12,20 @@ import ctypes
 from ._alloc import new as _new
 from .attention import KVCache, _CacheDesc, _dtype_code, _expect, _lib, _raise, _rows, _status_word, _stream, _torch
 
-__all__ = ["bitmm_qk_norm_rope_append", "qk_norm_rope_append"]
+__all__ = ["bitmm_qk_norm_rope_append", "qk_norm_rope_append", "bitmm_beam_select_workspace_bytes", "bitmm_beam_select",
+           "beam_select"]
 
 
 def declare(L) -> None:
     """Argument types of the calls of include/bitmm_beam.h in the loaded library."""
-    P, I64, I, F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    P, I64, I, F, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     C = ctypes.POINTER(_CacheDesc)
     L.bitmm_qk_norm_rope_append.argtypes = [P, I64, P, I64, P, I64, P, P, P, P, P, I64, P, C, I64, I64, I64, I, F, F, F, I, P, P]
     L.bitmm_qk_norm_rope_append.restype = I
+    L.bitmm_beam_select_workspace_bytes.argtypes = [I64, I64, I64, I64, I]
+    L.bitmm_beam_select_workspace_bytes.restype = SZ
+    L.bitmm_beam_select.argtypes = [P, I64, P, P, P, P, P, P, I64, I64, I64, I64, ctypes.c_int32, I, P, SZ, P, P]
+    L.bitmm_beam_select.restype = I
 
 
 def bitmm_qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, q_out, slots, cache: KVCache, *,
@@ -63,3 +68,66 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, slots,
     """Returns q_out, a new tensor."""
     return bitmm_qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, _new(q, q.shape, q.dtype, stream),
                                      slots, cache, stream=stream, **options)
+
+
+def _logits_code(t):
+    torch = _torch()
+    code = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"logits must be bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def bitmm_beam_select_workspace_bytes(groups, beams, vocab, k, logits_dtype) -> int:
+    """Of a call on logits [groups * beams, vocab] of a torch type."""
+    torch = _torch()
+    code = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}[logits_dtype]
+    return int(_lib().bitmm_beam_select_workspace_bytes(groups, beams, vocab, k, code))
+
+
+def bitmm_beam_select(logits, scores, scores_out, parents, tokens, workspace, *, beams: int, finished=None, finished_out=None,
+                      end_token: int = -1, status=None, stream=None):
+    """The k best continuations of each group of `beams` rows of logits [groups * beams, vocab] (rows any
+    stride apart), whose beams have scores [groups * beams] (float32): scores_out (float32), parents and
+    tokens (int32), all [groups, k], k being their second size. finished: bool [groups * beams] or None;
+    finished_out: bool [groups, k] or None. See include/bitmm_beam.h for what counts as a candidate.
+    workspace: uint8 of at least bitmm_beam_select_workspace_bytes(...)."""
+    torch = _torch()
+    if logits.dim() != 2 or parents.dim() != 2:
+        raise ValueError("logits must have two dims (beams of all groups, vocabulary), and parents two (groups, places)")
+    (rows, vocab), (groups, k) = logits.shape, parents.shape
+    index, code = logits.get_device(), _logits_code(logits)
+    if rows != groups * beams:
+        raise ValueError(f"{rows} rows of logits are not {groups} groups of {beams} beams")
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("the logits of a row must lie side by side")
+    row_stride = logits.stride(0) if rows > 1 else vocab
+    at = [_expect(scores, "scores", torch.float32, (rows,), index), _expect(scores_out, "scores_out", torch.float32, (groups, k), index),
+          _expect(parents, "parents", torch.int32, (groups, k), index), _expect(tokens, "tokens", torch.int32, (groups, k), index)]
+    done = None if finished is None else _expect(finished, "finished", torch.bool, (rows,), index)
+    done_out = None if finished_out is None else _expect(finished_out, "finished_out", torch.bool, (groups, k), index)
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
+    st = _lib().bitmm_beam_select(logits.data_ptr(), row_stride, at[0], done, *at[1:], done_out, groups, beams, vocab, k, end_token,
+                                  code, workspace.data_ptr(), workspace.numel(), _status_word(status, index),
+                                  _stream(stream, index))
+    if st:
+        _raise(st, "bitmm_beam_select")
+    return scores_out, parents, tokens, finished_out
+
+
+def beam_select(logits, scores, k: int, *, beams: int, finished=None, end_token: int = -1, workspace=None, status=None,
+                stream=None):
+    """Returns (scores, parents, tokens, finished), new tensors [groups, k]."""
+    torch = _torch()
+    rows, vocab = logits.shape
+    if beams < 1 or rows % beams:
+        raise ValueError(f"{rows} rows of logits are not groups of {beams} beams")
+    groups = rows // beams
+    out = [_new(logits, (groups, k), t, stream) for t in (torch.float32, torch.int32, torch.int32, torch.bool)]
+    if workspace is None:
+        need = int(_lib().bitmm_beam_select_workspace_bytes(groups, beams, vocab, k, _logits_code(logits)))
+        workspace = _new(logits, max(need, 16), torch.uint8, stream, returned=False)
+    bitmm_beam_select(logits, scores, *out[:3], workspace, beams=beams, finished=finished, finished_out=out[3],
+                      end_token=end_token, status=status, stream=stream)
+    return tuple(out)

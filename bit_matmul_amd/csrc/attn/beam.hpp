@@ -2,7 +2,10 @@
 // have validated every argument.
 #pragma once
 
+#include <algorithm>
+
 #include "attn.hpp"
+#include "bitmm_beam.h"
 
 namespace bitmm {
 namespace attn {
@@ -18,6 +21,28 @@ struct RopeAppendParams {
   unsigned kv_blocks;  // workgroups of all keys and values: the grid's first
 };
 hipError_t launch_qk_norm_rope_append(const RopeAppendParams& p, bool interleaved, int dtype, hipStream_t stream);
+
+struct SelectParams {
+  const void* logits;
+  int64_t row_stride;
+  const float* scores;
+  const uint8_t* finished;
+  float* scores_out;
+  int32_t* parents;
+  int32_t* tokens;
+  uint8_t* finished_out;
+  double* part_sum;    // [rows, parts, 2]: reference and sum of exponentials over it
+  uint64_t* part_top;  // [rows, parts, k]: (order of the logit, inverted token), largest first, 0 where none is left
+  uint32_t* status;
+  int beams, vocab, k, end_token;
+  int parts, each;     // as in SelectPlan
+};
+// How a row is cut up: `parts` workgroups, whose waves take `each` pieces of 16 bytes.
+struct SelectPlan {
+  int parts, each;
+};
+SelectPlan plan_select(int64_t rows, int64_t vocab, bitmm_out type);
+hipError_t launch_beam_select(SelectParams p, const SelectPlan& plan, int64_t groups, bitmm_out type, hipStream_t stream);
 
 }  // namespace attn
 }  // namespace bitmm

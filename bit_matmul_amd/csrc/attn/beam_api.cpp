@@ -6,6 +6,14 @@
 
 using namespace bitmm::attn;
 
+namespace {
+
+bool select_sizes_ok(int64_t groups, int64_t beams, int64_t vocab, int64_t k) {
+  return groups >= 0 && groups <= 1 << 20 && beams >= 1 && beams <= 64 && vocab >= 1 && vocab <= 1 << 30 && k >= 1 && k <= 64;
+}
+
+}  // namespace
+
 extern "C" {
 
 bitmm_status bitmm_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -60,6 +68,55 @@ bitmm_status bitmm_qk_norm_rope_append(const void* q, int64_t q_stride, const vo
     p.cache = view(cache);
     p.status = status;
     return launched(launch_qk_norm_rope_append(p, interleaved != 0, (int)dtype, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return BITMM_ERR_LAUNCH;
+  }
+}
+
+size_t bitmm_beam_select_workspace_bytes(int64_t groups, int64_t beams, int64_t vocab, int64_t k, bitmm_out logits_type) {
+  if (!select_sizes_ok(groups, beams, vocab, k) || groups == 0) return 0;
+  const SelectPlan plan = plan_select(groups * beams, vocab, logits_type);
+  return (size_t)(groups * beams) * plan.parts * (16 + 8 * (size_t)k);
+}
+
+bitmm_status bitmm_beam_select(const void* logits, int64_t row_stride, const float* scores,
+                               const uint8_t* finished, float* scores_out, int32_t* parents,
+                               int32_t* tokens, uint8_t* finished_out, int64_t groups, int64_t beams,
+                               int64_t vocab, int64_t k, int32_t end_token, bitmm_out logits_type,
+                               void* workspace, size_t workspace_bytes, uint32_t* status, void* stream) {
+  try {
+    bitmm::launch_log_begin();
+    if (logits_type != BITMM_OUT_BF16 && logits_type != BITMM_OUT_F32 && logits_type != BITMM_OUT_F16)
+      return BITMM_ERR_UNSUPPORTED;
+    if (!select_sizes_ok(groups, beams, vocab, k)) return BITMM_ERR_SHAPE;
+    if (row_stride < vocab) return BITMM_ERR_SHAPE;
+    if (groups == 0) return BITMM_OK;
+    if (!logits || !scores || !scores_out || !parents || !tokens) return BITMM_ERR_NULL;
+    if (!aligned(logits, logits_type == BITMM_OUT_F32 ? 4 : 2) || !aligned(scores, 4) || !aligned(scores_out, 4) ||
+        !aligned(parents, 4) || !aligned(tokens, 4) || !aligned(status, 4) || !aligned(workspace, 16))
+      return BITMM_ERR_ALIGN;
+    if (!workspace || workspace_bytes < bitmm_beam_select_workspace_bytes(groups, beams, vocab, k, logits_type))
+      return BITMM_ERR_WORKSPACE;
+    bitmm_status st;
+    if ((st = device_check()) != BITMM_OK) return st;
+    const SelectPlan plan = plan_select(groups * beams, vocab, logits_type);
+    SelectParams p = {};
+    p.logits = logits;
+    p.row_stride = row_stride;
+    p.scores = scores;
+    p.finished = finished;
+    p.scores_out = scores_out;
+    p.parents = parents;
+    p.tokens = tokens;
+    p.finished_out = finished_out;
+    p.part_sum = static_cast<double*>(workspace);
+    p.part_top = reinterpret_cast<uint64_t*>(p.part_sum + 2 * groups * beams * plan.parts);
+    p.status = status;
+    p.beams = (int)beams;
+    p.vocab = (int)vocab;
+    p.k = (int)k;
+    p.end_token = end_token;
+    return launched(launch_beam_select(p, plan, groups, logits_type, static_cast<hipStream_t>(stream)));
   } catch (...) {
     return BITMM_ERR_LAUNCH;
   }

@@ -4,6 +4,7 @@
  * the activation rows and the status word of bitmm_attn.h hold here too.
  *
  *   bitmm_qk_norm_rope_append   head norms, position rotation and the append to the cache
+ *   bitmm_beam_select           the best continuations of a group of beams
  *
  * The calls are for inference: there is no backward form.
  */
@@ -38,6 +39,34 @@ bitmm_status bitmm_qk_norm_rope_append(const void* q, int64_t q_stride, const vo
                                        int64_t q_heads, int64_t rot_dim, int interleaved, float eps,
                                        float weight_offset, float rope_scale, bitmm_dtype dtype,
                                        uint32_t* status, void* stream);
+
+/*
+ * Beam search's selection. Row r = g * beams + b holds the logits of beam b of group g (a prompt),
+ * rows `row_stride` values apart, of which the first `vocab` count. A candidate is a token t after a
+ * beam b, and stands for
+ *   total = scores[g, b] + (logits[r, t] - log sum_u exp(logits[r, u]))
+ * Of each group the k candidates of the largest total come out, in order: scores_out, parents (the
+ * beam, 0 .. beams - 1) and tokens, all [groups, k]. Equal totals go to the lowest (beam, token); of
+ * one beam the order is that of its logits. Sums, totals and comparisons are f64 (exact to 1e-10),
+ * scores_out is rounded once.
+ * A beam whose finished[r] (uint8 [groups, beams], or NULL for none) is not 0 has one candidate: end_token with
+ * its score as it is; its logits are not read. finished_out (uint8 [groups, k], or NULL) is 1
+ * where the parent was finished or the token is end_token (-1: no such token).
+ * No candidates are: logits of -infinity, beams whose score is -infinity, and beams with a NaN or
+ * +infinity among score or logits, which set *status. Where fewer than k are left the last places
+ * hold -infinity, parent -1 and token -1.
+ * With k = beams the outputs may be the inputs of the same kind; otherwise they do not overlap.
+ * beams and k 1 to 64, vocab up to 2^30, groups up to 2^20 (else BITMM_ERR_SHAPE); logits aligned to
+ * their type. `workspace`: at least bitmm_beam_select_workspace_bytes(...) bytes, 16-byte aligned,
+ * no initialisation needed; two calls that share it must be ordered on one stream.
+ */
+size_t bitmm_beam_select_workspace_bytes(int64_t groups, int64_t beams, int64_t vocab, int64_t k,
+                                         bitmm_out logits_type);
+bitmm_status bitmm_beam_select(const void* logits, int64_t row_stride, const float* scores,
+                               const uint8_t* finished, float* scores_out, int32_t* parents,
+                               int32_t* tokens, uint8_t* finished_out, int64_t groups, int64_t beams,
+                               int64_t vocab, int64_t k, int32_t end_token, bitmm_out logits_type,
+                               void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -83,3 +83,60 @@ def test_binding_refuses():
                       (ValueError, {})]:   # the last: tensors that are not on the GPU
         with pytest.raises(error):
             call(**kw)
+
+
+def select(L, **kw):
+    d = dict(logits=P, stride=1000, scores=P, fin=P, so=P, par=P, tok=P, fo=P, G=3, K=4, V=1000, k=8, end=2, type=0, ws=P,
+             ws_bytes=1 << 30, status=None, stream=None)
+    d.update(kw)
+    return L.bitmm_beam_select(*d.values())
+
+
+@pytest.mark.parametrize("kw, want", [
+    (dict(type=3), "UNSUPPORTED"), (dict(type=-1), "UNSUPPORTED"), (dict(G=-1), "SHAPE"), (dict(G=2 ** 20 + 1), "SHAPE"),
+    (dict(K=0), "SHAPE"), (dict(K=65), "SHAPE"), (dict(V=0), "SHAPE"), (dict(V=2 ** 30 + 1), "SHAPE"), (dict(k=0), "SHAPE"),
+    (dict(k=65), "SHAPE"), (dict(stride=999), "SHAPE"), (dict(logits=None), "NULL"), (dict(scores=None), "NULL"),
+    (dict(so=None), "NULL"), (dict(par=None), "NULL"), (dict(tok=None), "NULL"), (dict(logits=P + 1), "ALIGN"),
+    (dict(logits=P + 2, type=1), "ALIGN"), (dict(scores=P + 2), "ALIGN"), (dict(so=P + 1), "ALIGN"), (dict(par=P + 2), "ALIGN"),
+    (dict(tok=P + 2), "ALIGN"), (dict(status=P + 1), "ALIGN"), (dict(ws=P + 8), "ALIGN"), (dict(ws=None), "WORKSPACE"),
+    (dict(ws_bytes=100), "WORKSPACE"),
+])
+def test_select_refusals(L, kw, want):
+    assert select(L, **kw) == status(want)
+    assert bm.bitmm_last_launches() == []
+
+
+def test_select_empty_and_workspace(L):
+    assert select(L, G=0, logits=None, ws=None) == bm.BITMM_OK
+    need = bm.bitmm_beam_select_workspace_bytes
+    assert need(0, 4, 1000, 8, torch.float32) == 0 and need(1, 65, 1000, 8, torch.float32) == 0
+    for groups, beams, vocab, k in [(1, 1, 1, 1), (1, 4, 32000, 4), (300, 64, 131072, 64), (1 << 20, 64, 1 << 30, 64)]:
+        for dtype in (torch.bfloat16, torch.float32):
+            n = need(groups, beams, vocab, k, dtype)
+            # a part of a row has a sum and k pairs, and a row at most 64 parts
+            assert groups * beams * (16 + 8 * k) <= n <= 64 * groups * beams * (16 + 8 * k)
+            if not torch.cuda.is_available():
+                assert select(L, G=groups, K=beams, V=vocab, stride=vocab, k=k, type=1 if dtype is torch.float32 else 0,
+                              ws_bytes=n) == bm.BITMM_ERR_DEVICE
+                assert select(L, G=groups, K=beams, V=vocab, stride=vocab, k=k, type=1 if dtype is torch.float32 else 0,
+                              ws_bytes=n - 1) == bm.BITMM_ERR_WORKSPACE
+
+
+def test_select_binding_refuses():
+    f32, i32 = torch.float32, torch.int32
+    logits, scores = torch.zeros(6, 50), torch.zeros(6)
+    so, par, tok = torch.zeros(2, 3), torch.zeros(2, 3, dtype=i32), torch.zeros(2, 3, dtype=i32)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+
+    def call(logits=logits, scores=scores, so=so, par=par, tok=tok, ws=ws, **kw):
+        return bm.bitmm_beam_select(logits, scores, so, par, tok, ws, **{"beams": 3, **kw})
+
+    for error, kw in [(TypeError, dict(logits=logits.double())), (TypeError, dict(scores=scores.half())),
+                      (TypeError, dict(tok=tok.long())), (TypeError, dict(finished=torch.zeros(6, dtype=torch.uint8))),
+                      (ValueError, dict(beams=2)), (ValueError, dict(scores=scores[:5])), (ValueError, dict(so=so[:, :2])),
+                      (ValueError, dict(logits=torch.zeros(50, 6).t())), (ValueError, dict(par=par[0])), (ValueError, dict(ws=ws[::2])),
+                      (ValueError, dict(finished=torch.zeros(2, 3, dtype=torch.bool))), (ValueError, {})]:
+        with pytest.raises(error):
+            call(**kw)
+    with pytest.raises(ValueError):
+        bm.beam_select(logits, scores, 3, beams=4)
