@@ -13,7 +13,7 @@ from ._alloc import new as _new
 from .attention import KVCache, _CacheDesc, _dtype_code, _expect, _lib, _raise, _rows, _status_word, _stream, _torch
 
 __all__ = ["bitmm_qk_norm_rope_append", "qk_norm_rope_append", "bitmm_beam_select_workspace_bytes", "bitmm_beam_select",
-           "beam_select"]
+           "beam_select", "KVLayers", "bitmm_kv_beam_reorder_workspace_bytes", "bitmm_kv_beam_reorder", "kv_beam_reorder"]
 
 
 def declare(L) -> None:
@@ -26,6 +26,10 @@ def declare(L) -> None:
     L.bitmm_beam_select_workspace_bytes.restype = SZ
     L.bitmm_beam_select.argtypes = [P, I64, P, P, P, P, P, P, I64, I64, I64, I64, ctypes.c_int32, I, P, SZ, P, P]
     L.bitmm_beam_select.restype = I
+    L.bitmm_kv_beam_reorder_workspace_bytes.argtypes = [I64, I64]
+    L.bitmm_kv_beam_reorder_workspace_bytes.restype = SZ
+    L.bitmm_kv_beam_reorder.argtypes = [C, I64, P, P, I64, P, P, P, P, I64, I64, I64, I64, P, SZ, P, P]
+    L.bitmm_kv_beam_reorder.restype = I
 
 
 def bitmm_qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, q_out, slots, cache: KVCache, *,
@@ -131,3 +135,58 @@ def beam_select(logits, scores, k: int, *, beams: int, finished=None, end_token:
     bitmm_beam_select(logits, scores, *out[:3], workspace, beams=beams, finished=finished, finished_out=out[3],
                       end_token=end_token, status=status, stream=stream)
     return tuple(out)
+
+
+class KVLayers:
+    """The caches of a model's layers, of the same sizes, whose pages share one table."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if not self.caches:
+            raise ValueError("at least one cache is needed")
+        sizes = [(c.num_pages, c.page_size, c.kv_heads, c.head_dim, c.group_size, c.device_index) for c in self.caches]
+        if any(s != sizes[0] for s in sizes):
+            raise ValueError("the layers' caches must have the same sizes and lie on one device")
+        self.device_index, self.page_size = self.caches[0].device_index, self.caches[0].page_size
+        self.desc = (_CacheDesc * len(self.caches))(*(c.desc for c in self.caches))
+
+
+def bitmm_kv_beam_reorder_workspace_bytes(groups, beams) -> int:
+    return int(_lib().bitmm_kv_beam_reorder_workspace_bytes(groups, beams))
+
+
+def bitmm_kv_beam_reorder(layers: KVLayers, page_table, lens, parents, page_table_out, lens_out, slots, workspace, *,
+                          first_page: int, pages_per_group: int, status=None, stream=None):
+    """The cached states in the order of parents [groups, beams] (int32; the beam that each row goes on
+    from, -1 for none), with room for one more token each. page_table: int32 [groups * beams, pages];
+    lens: int32 [groups * beams]; slots: int64 [groups * beams], where the next tokens go; lens_out counts
+    them. Outputs may be their inputs. New pages come from the group's pool of pages_per_group pages; see
+    include/bitmm_beam.h. workspace: uint8 of at least bitmm_kv_beam_reorder_workspace_bytes(...)."""
+    torch = _torch()
+    if parents.dim() != 2 or page_table.dim() != 2:
+        raise ValueError("parents must have two dims (groups, beams), and page_table two (rows, pages)")
+    (groups, beams), pages, index = parents.shape, page_table.shape[1], layers.device_index
+    rows, int32 = groups * beams, torch.int32
+    at = [_expect(page_table, "page_table", int32, (rows, pages), index), _expect(page_table_out, "page_table_out", int32, (rows, pages), index),
+          _expect(lens, "lens", int32, (rows,), index), _expect(lens_out, "lens_out", int32, (rows,), index),
+          _expect(parents, "parents", int32, (groups, beams), index), _expect(slots, "slots", torch.int64, (rows,), index)]
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
+    st = _lib().bitmm_kv_beam_reorder(layers.desc, len(layers.caches), at[0], at[1], pages, *at[2:], groups, beams, first_page,
+                                      pages_per_group, workspace.data_ptr(), workspace.numel(), _status_word(status, index),
+                                      _stream(stream, index))
+    if st:
+        _raise(st, "bitmm_kv_beam_reorder")
+    return page_table_out, lens_out, slots
+
+
+def kv_beam_reorder(layers: KVLayers, page_table, lens, parents, *, first_page: int, pages_per_group: int, workspace=None,
+                    status=None, stream=None):
+    """Returns (page_table, lens, slots), new tensors; the caches' copies are made in place."""
+    torch = _torch()
+    table, lens_out = _new(page_table, page_table.shape, torch.int32, stream), _new(lens, lens.shape, torch.int32, stream)
+    slots = _new(lens, lens.shape, torch.int64, stream)
+    if workspace is None:
+        workspace = _new(lens, max(16 * lens.numel(), 16), torch.uint8, stream, returned=False)
+    return bitmm_kv_beam_reorder(layers, page_table, lens, parents, table, lens_out, slots, workspace, first_page=first_page,
+                                 pages_per_group=pages_per_group, status=status, stream=stream)

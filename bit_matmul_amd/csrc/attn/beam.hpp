@@ -44,5 +44,31 @@ struct SelectPlan {
 SelectPlan plan_select(int64_t rows, int64_t vocab, bitmm_out type);
 hipError_t launch_beam_select(SelectParams p, const SelectPlan& plan, int64_t groups, bitmm_out type, hipStream_t stream);
 
+struct ReorderParams {
+  const int32_t* table;
+  int32_t* table_out;
+  const int32_t* lens;
+  int32_t* lens_out;
+  const int32_t* parents;
+  int64_t* slots;
+  void* copies;  // 16 bytes a row
+  uint32_t* status;
+  int64_t pages_per_seq;
+  int beams, page_shift, num_pages, first_page, pages_per_group;
+  int kv_heads, code_pieces, groups_of_head;  // pieces of 16 bytes of a head's codes
+};
+// The caches of some layers, by value: they may change with the program's every call.
+struct ReorderLayers {
+  static constexpr int MOST = 64;
+  struct Side {
+    uint32_t *codes, *scales;
+  };
+  struct Layer {
+    Side side[2];
+  } at[MOST];
+};
+hipError_t launch_beam_reorder(const ReorderParams& p, const bitmm_kv_cache* caches, int64_t layers, int64_t groups,
+                               hipStream_t stream);
+
 }  // namespace attn
 }  // namespace bitmm

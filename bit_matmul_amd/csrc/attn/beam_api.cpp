@@ -8,8 +8,13 @@ using namespace bitmm::attn;
 
 namespace {
 
+// A launch's threads are counted in 32 bits, and a row takes 256 at least.
+bool beam_rows_ok(int64_t groups, int64_t beams) {
+  return groups >= 0 && beams >= 1 && beams <= 64 && groups <= (1 << 22) / beams;
+}
+
 bool select_sizes_ok(int64_t groups, int64_t beams, int64_t vocab, int64_t k) {
-  return groups >= 0 && groups <= 1 << 20 && beams >= 1 && beams <= 64 && vocab >= 1 && vocab <= 1 << 30 && k >= 1 && k <= 64;
+  return beam_rows_ok(groups, beams) && vocab >= 1 && vocab <= 1 << 30 && k >= 1 && k <= 64;
 }
 
 }  // namespace
@@ -32,7 +37,7 @@ bitmm_status bitmm_qk_norm_rope_append(const void* q, int64_t q_stride, const vo
     const int64_t D = cache->head_dim, kv_heads = cache->kv_heads;
     if (!fits_int(T) || !fits_int(q_heads)) return BITMM_ERR_SHAPE;
     if (rot_dim < 0 || rot_dim > D || rot_dim % 8 != 0) return BITMM_ERR_SHAPE;
-    if (T * (q_heads + kv_heads) >= (int64_t)1 << 30) return BITMM_ERR_SHAPE;
+    if (T > 1 << 24 || T * (q_heads + kv_heads) >= (int64_t)1 << 30) return BITMM_ERR_SHAPE;
     if (T == 0) return BITMM_OK;
     if (q_heads > 0) {
       if ((st = check_rows(q, q_stride, q_heads, D)) != BITMM_OK) return st;
@@ -117,6 +122,65 @@ bitmm_status bitmm_beam_select(const void* logits, int64_t row_stride, const flo
     p.k = (int)k;
     p.end_token = end_token;
     return launched(launch_beam_select(p, plan, groups, logits_type, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return BITMM_ERR_LAUNCH;
+  }
+}
+
+size_t bitmm_kv_beam_reorder_workspace_bytes(int64_t groups, int64_t beams) {
+  return beam_rows_ok(groups, beams) ? (size_t)(groups * beams) * 16 : 0;
+}
+
+bitmm_status bitmm_kv_beam_reorder(const bitmm_kv_cache* caches, int64_t layers, const int32_t* page_table,
+                                   int32_t* page_table_out, int64_t pages_per_seq, const int32_t* lens,
+                                   int32_t* lens_out, const int32_t* parents, int64_t* slots,
+                                   int64_t groups, int64_t beams, int64_t first_page,
+                                   int64_t pages_per_group, void* workspace, size_t workspace_bytes,
+                                   uint32_t* status, void* stream) {
+  try {
+    bitmm::launch_log_begin();
+    if (layers < 1 || layers > 4096) return BITMM_ERR_SHAPE;
+    if (!caches) return BITMM_ERR_NULL;
+    bitmm_status st;
+    for (int64_t i = 0; i < layers; ++i) {
+      if ((st = check_cache(caches + i)) != BITMM_OK) return st;
+      const bitmm_kv_cache &a = caches[0], &b = caches[i];
+      if (a.num_pages != b.num_pages || a.page_size != b.page_size || a.kv_heads != b.kv_heads || a.head_dim != b.head_dim ||
+          a.group_size != b.group_size)
+        return BITMM_ERR_SHAPE;
+    }
+    if (!beam_rows_ok(groups, beams)) return BITMM_ERR_SHAPE;
+    if (pages_per_seq < 1 || pages_per_seq > (int64_t)1 << 22) return BITMM_ERR_SHAPE;
+    if (first_page < 0 || pages_per_group < 0 || pages_per_group > 1 << 18 || first_page > caches->num_pages ||
+        groups * pages_per_group > caches->num_pages - first_page)
+      return BITMM_ERR_SHAPE;
+    if (groups == 0) return BITMM_OK;
+    if (!page_table || !page_table_out || !lens || !lens_out || !parents || !slots) return BITMM_ERR_NULL;
+    if (!aligned(page_table, 4) || !aligned(page_table_out, 4) || !aligned(lens, 4) || !aligned(lens_out, 4) ||
+        !aligned(parents, 4) || !aligned(slots, 8) || !aligned(status, 4) || !aligned(workspace, 16))
+      return BITMM_ERR_ALIGN;
+    if (!workspace || workspace_bytes < bitmm_kv_beam_reorder_workspace_bytes(groups, beams)) return BITMM_ERR_WORKSPACE;
+    if ((st = device_check()) != BITMM_OK) return st;
+    const Cache c = view(caches);
+    ReorderParams p = {};
+    p.table = page_table;
+    p.table_out = page_table_out;
+    p.lens = lens;
+    p.lens_out = lens_out;
+    p.parents = parents;
+    p.slots = slots;
+    p.copies = workspace;
+    p.status = status;
+    p.pages_per_seq = pages_per_seq;
+    p.beams = (int)beams;
+    p.page_shift = c.page_shift;
+    p.num_pages = c.num_pages;
+    p.first_page = (int)first_page;
+    p.pages_per_group = (int)pages_per_group;
+    p.kv_heads = c.kv_heads;
+    p.code_pieces = c.head_dim / 32;
+    p.groups_of_head = c.head_dim / c.group;
+    return launched(launch_beam_reorder(p, caches, layers, groups, static_cast<hipStream_t>(stream)));
   } catch (...) {
     return BITMM_ERR_LAUNCH;
   }

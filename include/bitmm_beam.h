@@ -5,6 +5,7 @@
  *
  *   bitmm_qk_norm_rope_append   head norms, position rotation and the append to the cache
  *   bitmm_beam_select           the best continuations of a group of beams
+ *   bitmm_kv_beam_reorder       the cached states in the order of the beams that go on
  *
  * The calls are for inference: there is no backward form.
  */
@@ -29,7 +30,7 @@ extern "C" {
  * not stored, nor is one whose slot lies outside the cache, which sets *status; their q_out is
  * written all the same. Slots of one call are distinct (of two tokens with one slot, which
  * one's pieces stay is not defined). A key or value that is not finite makes its group NaN.
- * T * (q_heads + kv_heads) < 2^30.
+ * T <= 2^24 and T * (q_heads + kv_heads) < 2^30.
  */
 bitmm_status bitmm_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                        const void* v, int64_t v_stride, const void* q_weight,
@@ -56,8 +57,8 @@ bitmm_status bitmm_qk_norm_rope_append(const void* q, int64_t q_stride, const vo
  * +infinity among score or logits, which set *status. Where fewer than k are left the last places
  * hold -infinity, parent -1 and token -1.
  * With k = beams the outputs may be the inputs of the same kind; otherwise they do not overlap.
- * beams and k 1 to 64, vocab up to 2^30, groups up to 2^20 (else BITMM_ERR_SHAPE); logits aligned to
- * their type. `workspace`: at least bitmm_beam_select_workspace_bytes(...) bytes, 16-byte aligned,
+ * beams and k 1 to 64, vocab up to 2^30, groups * beams up to 2^22 (else BITMM_ERR_SHAPE); logits aligned
+ * to their type. `workspace`: at least bitmm_beam_select_workspace_bytes(...) bytes, 16-byte aligned,
  * no initialisation needed; two calls that share it must be ordered on one stream.
  */
 size_t bitmm_beam_select_workspace_bytes(int64_t groups, int64_t beams, int64_t vocab, int64_t k,
@@ -67,6 +68,37 @@ bitmm_status bitmm_beam_select(const void* logits, int64_t row_stride, const flo
                                int32_t* tokens, uint8_t* finished_out, int64_t groups, int64_t beams,
                                int64_t vocab, int64_t k, int32_t end_token, bitmm_out logits_type,
                                void* workspace, size_t workspace_bytes, uint32_t* status, void* stream);
+
+/*
+ * The cached states in the order of the beams that go on, with room for one more token each.
+ * Row r = g * beams + j, beam j of group g, has lens[r] tokens on the pages that page_table
+ * [groups * beams, pages_per_seq] names. After the call it has those of beam parents[r] of its
+ * group (0 .. beams - 1; -1: none, an empty row) and one more, which is to be stored at slots[r]
+ * (as bitmm_kv_append takes it) and which lens_out counts. Pages that are full are shared: rows of
+ * the table name the same ones. A last page that is partly filled is kept by the first row that
+ * has it; the others get a page each, to which the tokens are copied, in all `layers` caches (one for
+ * each layer of a model, of the same sizes; their pages share one table). A row whose last page is full,
+ * or that is empty, gets a page for the next token.
+ * New pages are the lowest ones of the group's pool that no row of the group holds afterwards, in the
+ * order of the rows: pages [first_page + g * pages_per_group, + pages_per_group). A pool of beams *
+ * pages_per_seq pages never ends. Pages outside it, as those of a prompt, may be named and are never written;
+ * a page that one row holds partly filled is no other row's full one.
+ * A row for which no page or no place in the table is left keeps its parent's tokens and gets no room:
+ * its slot is -1, lens_out is its parent's, and *status is set, as it is by parents and lengths out of range
+ * (taken as -1, and cut) and by a partly filled page outside the cache. Empty rows have slot -1 and a length of 0.
+ * Entries of the table past a row's pages are passed on as they are. An output may be its input (same
+ * pointer), otherwise they do not overlap.
+ * beams 1 to 64, groups * beams up to 2^22, layers up to 4096, pages_per_seq up to 2^22, pages_per_group up to 2^18
+ * (else BITMM_ERR_SHAPE). `workspace`: bitmm_kv_beam_reorder_workspace_bytes(...) bytes, 16-byte aligned, no
+ * initialisation needed; two calls that share it must be ordered on one stream.
+ */
+size_t bitmm_kv_beam_reorder_workspace_bytes(int64_t groups, int64_t beams);
+bitmm_status bitmm_kv_beam_reorder(const bitmm_kv_cache* caches, int64_t layers, const int32_t* page_table,
+                                   int32_t* page_table_out, int64_t pages_per_seq, const int32_t* lens,
+                                   int32_t* lens_out, const int32_t* parents, int64_t* slots,
+                                   int64_t groups, int64_t beams, int64_t first_page,
+                                   int64_t pages_per_group, void* workspace, size_t workspace_bytes,
+                                   uint32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

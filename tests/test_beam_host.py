@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import bit_matmul_amd as bm
+from bit_matmul_amd import attention as A
 from tests.test_attention_host import CACHE_FAULTS, P, cache, status
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -36,7 +37,7 @@ def rope_append(L, desc="", **kw):
 
 @pytest.mark.parametrize("kw, want", [
     (dict(dtype=2), "UNSUPPORTED"), (dict(T=-1), "SHAPE"), (dict(hq=-1), "SHAPE"), (dict(rot=136), "SHAPE"),
-    (dict(rot=-8), "SHAPE"), (dict(rot=12), "SHAPE"), (dict(T=2 ** 30), "SHAPE"), (dict(T=2 ** 27), "SHAPE"),
+    (dict(rot=-8), "SHAPE"), (dict(rot=12), "SHAPE"), (dict(T=2 ** 30), "SHAPE"), (dict(T=2 ** 24 + 1), "SHAPE"),
     (dict(hq=2 ** 29), "SHAPE"), (dict(qs=1016), "SHAPE"), (dict(ks=248), "SHAPE"), (dict(vs=248), "SHAPE"),
     (dict(qs=1028), "ALIGN"), (dict(vs=260), "ALIGN"), (dict(q=P + 2), "ALIGN"), (dict(v=P + 8), "ALIGN"),
     (dict(qo=P + 8), "ALIGN"), (dict(qw=P + 1), "ALIGN"), (dict(pos=P + 2), "ALIGN"), (dict(freq=P + 1), "ALIGN"),
@@ -93,7 +94,7 @@ def select(L, **kw):
 
 
 @pytest.mark.parametrize("kw, want", [
-    (dict(type=3), "UNSUPPORTED"), (dict(type=-1), "UNSUPPORTED"), (dict(G=-1), "SHAPE"), (dict(G=2 ** 20 + 1), "SHAPE"),
+    (dict(type=3), "UNSUPPORTED"), (dict(type=-1), "UNSUPPORTED"), (dict(G=-1), "SHAPE"), (dict(G=2 ** 20 + 1), "SHAPE"), (dict(G=2 ** 62), "SHAPE"),
     (dict(K=0), "SHAPE"), (dict(K=65), "SHAPE"), (dict(V=0), "SHAPE"), (dict(V=2 ** 30 + 1), "SHAPE"), (dict(k=0), "SHAPE"),
     (dict(k=65), "SHAPE"), (dict(stride=999), "SHAPE"), (dict(logits=None), "NULL"), (dict(scores=None), "NULL"),
     (dict(so=None), "NULL"), (dict(par=None), "NULL"), (dict(tok=None), "NULL"), (dict(logits=P + 1), "ALIGN"),
@@ -110,7 +111,7 @@ def test_select_empty_and_workspace(L):
     assert select(L, G=0, logits=None, ws=None) == bm.BITMM_OK
     need = bm.bitmm_beam_select_workspace_bytes
     assert need(0, 4, 1000, 8, torch.float32) == 0 and need(1, 65, 1000, 8, torch.float32) == 0
-    for groups, beams, vocab, k in [(1, 1, 1, 1), (1, 4, 32000, 4), (300, 64, 131072, 64), (1 << 20, 64, 1 << 30, 64)]:
+    for groups, beams, vocab, k in [(1, 1, 1, 1), (1, 4, 32000, 4), (300, 64, 131072, 64), (1 << 16, 64, 1 << 30, 64)]:
         for dtype in (torch.bfloat16, torch.float32):
             n = need(groups, beams, vocab, k, dtype)
             # a part of a row has a sum and k pairs, and a row at most 64 parts
@@ -140,3 +141,62 @@ def test_select_binding_refuses():
             call(**kw)
     with pytest.raises(ValueError):
         bm.beam_select(logits, scores, 3, beams=4)
+
+
+def reorder(L, n=3, caches=None, **kw):
+    array = (A._CacheDesc * n)(*(caches or [cache(num_pages=1000)] * n))
+    d = dict(caches=array, layers=n, table=P, table_out=P + 4096, pages=8, lens=P, lens_out=P, parents=P, slots=P, G=4, K=4,
+             first=3, each=32, ws=P, ws_bytes=256, status=None, stream=None)
+    d.update(kw)
+    return L.bitmm_kv_beam_reorder(*d.values())
+
+
+@pytest.mark.parametrize("kw, want", [
+    (dict(caches=None), "NULL"), (dict(layers=0), "SHAPE"), (dict(layers=4097), "SHAPE"), (dict(G=-1), "SHAPE"),
+    (dict(G=2 ** 20 + 1), "SHAPE"), (dict(K=0), "SHAPE"), (dict(K=65), "SHAPE"), (dict(pages=0), "SHAPE"),
+    (dict(pages=2 ** 22 + 1), "SHAPE"), (dict(first=-1), "SHAPE"), (dict(first=1001), "SHAPE"), (dict(each=-1), "SHAPE"),
+    (dict(each=250), "SHAPE"), (dict(first=873), "SHAPE"), (dict(each=2 ** 18 + 1), "SHAPE"), (dict(table=None), "NULL"),
+    (dict(table_out=None), "NULL"), (dict(lens=None), "NULL"), (dict(lens_out=None), "NULL"), (dict(parents=None), "NULL"),
+    (dict(slots=None), "NULL"), (dict(table=P + 2), "ALIGN"), (dict(lens_out=P + 1), "ALIGN"), (dict(slots=P + 4), "ALIGN"),
+    (dict(status=P + 2), "ALIGN"), (dict(ws=P + 8), "ALIGN"), (dict(ws=None), "WORKSPACE"), (dict(ws_bytes=255), "WORKSPACE"),
+])
+def test_reorder_refusals(L, kw, want):
+    if "caches" in kw:
+        assert L.bitmm_kv_beam_reorder(None, 1, P, P, 8, P, P, P, P, 4, 4, 3, 32, P, 256, None, None) == status(want)
+    else:
+        assert reorder(L, **kw) == status(want)
+    assert bm.bitmm_last_launches() == []
+
+
+def test_reorder_caches(L):
+    for kw, want in CACHE_FAULTS:
+        faulty = [cache(num_pages=1000), cache(**{"num_pages": 1000, **kw})]
+        assert reorder(L, n=2, caches=faulty) == status(want)
+    for kw in (dict(num_pages=1001), dict(page_size=32), dict(kv_heads=3), dict(head_dim=64), dict(group_size=32)):
+        assert reorder(L, n=2, caches=[cache(num_pages=1000), cache(**{"num_pages": 1000, **kw})]) == status("SHAPE")
+    assert reorder(L, G=0, table=None) == bm.BITMM_OK
+    assert bm.bitmm_kv_beam_reorder_workspace_bytes(4, 4) == 256 and bm.bitmm_kv_beam_reorder_workspace_bytes(4, 65) == 0
+    if not torch.cuda.is_available():
+        assert reorder(L) == bm.BITMM_ERR_DEVICE
+        assert reorder(L, first=872) == bm.BITMM_ERR_DEVICE
+
+
+def test_reorder_binding_refuses():
+    i32, i64 = torch.int32, torch.int64
+    with pytest.raises(ValueError):
+        bm.KVLayers([])
+
+    class Layers:
+        caches, desc, device_index, page_size = [None], None, -1, 16
+
+    table, lens, parents = torch.zeros(6, 4, dtype=i32), torch.zeros(6, dtype=i32), torch.zeros(2, 3, dtype=i32)
+    slots, ws = torch.zeros(6, dtype=i64), torch.zeros(96, dtype=torch.uint8)
+
+    def call(table=table, lens=lens, parents=parents, table_out=table, lens_out=lens, slots=slots, ws=ws):
+        return bm.bitmm_kv_beam_reorder(Layers(), table, lens, parents, table_out, lens_out, slots, ws, first_page=0, pages_per_group=4)
+
+    for error, kw in [(TypeError, dict(table=table.long())), (TypeError, dict(slots=slots.int())), (ValueError, dict(parents=parents[0])),
+                      (ValueError, dict(parents=parents[:1])), (ValueError, dict(lens=lens[:5])), (ValueError, dict(table_out=table[:, :3])),
+                      (TypeError, dict(parents=parents.long())), (ValueError, dict(ws=ws[::2])), (ValueError, {})]:
+        with pytest.raises(error):
+            call(**kw)
