@@ -8,11 +8,13 @@ the outputs.
 from __future__ import annotations
 
 import ctypes
+import math
 
 from ._alloc import new as _new
 from .attention import KVCache, _CacheDesc, _dtype_code, _expect, _lib, _raise, _rows, _status_word, _stream, _torch
 
-__all__ = ["bitmm_qk_norm_rope_append", "qk_norm_rope_append", "bitmm_beam_select_workspace_bytes", "bitmm_beam_select",
+__all__ = ["bitmm_qk_norm_rope_append", "qk_norm_rope_append", "bitmm_kv_attention_shared_workspace_bytes",
+           "bitmm_kv_attention_shared", "kv_attention_shared", "bitmm_beam_select_workspace_bytes", "bitmm_beam_select",
            "beam_select", "KVLayers", "bitmm_kv_beam_reorder_workspace_bytes", "bitmm_kv_beam_reorder", "kv_beam_reorder"]
 
 
@@ -22,6 +24,11 @@ def declare(L) -> None:
     C = ctypes.POINTER(_CacheDesc)
     L.bitmm_qk_norm_rope_append.argtypes = [P, I64, P, I64, P, I64, P, P, P, P, P, I64, P, C, I64, I64, I64, I, F, F, F, I, P, P]
     L.bitmm_qk_norm_rope_append.restype = I
+    L.bitmm_kv_attention_shared_workspace_bytes.argtypes = [I64] * 10
+    L.bitmm_kv_attention_shared_workspace_bytes.restype = SZ
+    L.bitmm_kv_attention_shared.argtypes = [P, I64, C, P, I64, P, P, P, I64, P, P, P, I64, P, I64, I64, I64, I64, I64, I64, I64,
+                                            I64, F, I, I, P, SZ, P, P]
+    L.bitmm_kv_attention_shared.restype = I
     L.bitmm_beam_select_workspace_bytes.argtypes = [I64, I64, I64, I64, I]
     L.bitmm_beam_select_workspace_bytes.restype = SZ
     L.bitmm_beam_select.argtypes = [P, I64, P, P, P, P, P, P, I64, I64, I64, I64, ctypes.c_int32, I, P, SZ, P, P]
@@ -72,6 +79,65 @@ def qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, slots,
     """Returns q_out, a new tensor."""
     return bitmm_qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, _new(q, q.shape, q.dtype, stream),
                                      slots, cache, stream=stream, **options)
+
+
+def bitmm_kv_attention_shared_workspace_bytes(T, B, groups, max_group_q, max_prefix, max_q, max_kv, q_heads, kv_heads, head_dim) -> int:
+    return int(_lib().bitmm_kv_attention_shared_workspace_bytes(T, B, groups, max_group_q, max_prefix, max_q, max_kv, q_heads,
+                                                                kv_heads, head_dim))
+
+
+def bitmm_kv_attention_shared(q, cache: KVCache, prefix_table, prefix_lens, cu_groups, page_table, kv_lens, cu_q, out, workspace, *,
+                              max_group_q: int, max_prefix: int, max_q: int, max_kv: int, scale=None, lse=None, status=None,
+                              stream=None):
+    """Attention of q [T, q_heads, D] over tokens that the sequences of a group share and each one's own.
+    prefix_table: int32 [groups, pages], prefix_lens: int32 [groups], cu_groups: int32 [groups + 1] (the
+    sequences of each group); page_table: int32 [B, pages], kv_lens: int32 [B], cu_q: int32 [B + 1] as in
+    bitmm_kv_attention, of the own tokens. max_group_q: a bound of a group's queries, max_prefix of the
+    shared tokens, max_q and max_kv of a sequence's queries and own tokens. out, lse, scale: as there;
+    workspace: uint8 of at least bitmm_kv_attention_shared_workspace_bytes(...)."""
+    torch = _torch()
+    T, heads, D = shape = q.shape
+    B, groups = kv_lens.shape[0], prefix_lens.shape[0]
+    index, int32 = cache.device_index, torch.int32
+    if D != cache.head_dim:
+        raise ValueError(f"q has heads of {D} dims, the cache of {cache.head_dim}")
+    code = _dtype_code(q, "q")
+    out_code = 0 if out.dtype is torch.bfloat16 else 2 if out.dtype is torch.float16 else 1
+    if out_code == 1 and out.dtype is not torch.float32:
+        raise TypeError(f"out must be bfloat16, float16 or float32, got {out.dtype}")
+    q_stride, out_stride = _rows(q, "q", q.dtype, shape, index), _rows(out, "out", out.dtype, shape, index)
+    if page_table.dim() != 2 or prefix_table.dim() != 2:
+        raise ValueError("page_table and prefix_table must have two dims (sequences or groups, pages)")
+    pages, prefix_pages = page_table.shape[1], prefix_table.shape[1]
+    at = [_expect(prefix_lens, "prefix_lens", int32, (groups,), index), _expect(cu_groups, "cu_groups", int32, (groups + 1,), index),
+          _expect(page_table, "page_table", int32, (B, pages), index)]
+    lens, cu = _expect(kv_lens, "kv_lens", int32, (B,), index), _expect(cu_q, "cu_q", int32, (B + 1,), index)
+    prefix = _expect(prefix_table, "prefix_table", int32, (groups, prefix_pages), index)
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
+    st = _lib().bitmm_kv_attention_shared(
+        q.data_ptr(), q_stride, cache.desc, prefix, prefix_pages, *at, pages, lens, cu, out.data_ptr(), out_stride,
+        None if lse is None else _expect(lse, "lse", torch.float32, (T, heads), index), T, B, groups, heads, max_group_q, max_prefix,
+        max_q, max_kv, 1.0 / math.sqrt(D) if scale is None else scale, code, out_code, workspace.data_ptr(), workspace.numel(),
+        _status_word(status, index), _stream(stream, index))
+    if st:
+        _raise(st, "bitmm_kv_attention_shared")
+    return out
+
+
+def kv_attention_shared(q, cache: KVCache, prefix_table, prefix_lens, cu_groups, page_table, kv_lens, cu_q, *, max_group_q: int,
+                        max_prefix: int, max_q: int, max_kv: int, scale=None, out_dtype=None, workspace=None, lse=None,
+                        status=None, stream=None):
+    """Returns the output, a new tensor of q's type unless out_dtype is given. Rows of q that
+    belong to no sequence are left uninitialised."""
+    out = _new(q, q.shape, q.dtype if out_dtype is None else out_dtype, stream)
+    if workspace is None:
+        need = bitmm_kv_attention_shared_workspace_bytes(q.shape[0], kv_lens.shape[0], prefix_lens.shape[0], max_group_q, max_prefix,
+                                                         max_q, max_kv, q.shape[1], cache.kv_heads, cache.head_dim)
+        workspace = _new(q, max(need, 16), _torch().uint8, stream, returned=False)
+    return bitmm_kv_attention_shared(q, cache, prefix_table, prefix_lens, cu_groups, page_table, kv_lens, cu_q, out, workspace,
+                                     max_group_q=max_group_q, max_prefix=max_prefix, max_q=max_q, max_kv=max_kv, scale=scale,
+                                     lse=lse, status=status, stream=stream)
 
 
 def _logits_code(t):

@@ -55,6 +55,7 @@ struct Extent {
   int rows;   // query rows of one kv head: queries * share
   int first;  // position of the first query (may be negative)
   int kv;     // tokens
+  int step;   // of the positions from query to query: 1, or 0 where all queries see all tokens
 };
 
 __device__ __forceinline__ Extent extent_of(const AttentionParams& p, int b, bool report) {
@@ -69,13 +70,41 @@ __device__ __forceinline__ Extent extent_of(const AttentionParams& p, int b, boo
   e.kv = min(max(len, 0), most);
   e.rows = min(n, p.max_q) * p.share;
   e.first = e.kv - n;
+  e.step = 1;
   if (report && p.status && (q0 != c0 || q1 != c1 || n > p.max_q || e.kv != len)) *p.status = 1;
   return e;
 }
 
+// What a group of sequences has: all their queries, and the tokens that all of them see.
+__device__ __forceinline__ Extent extent_of_group(const AttentionParams& p, int g, bool report) {
+  Extent e;
+  const int g0 = p.cu_groups[g], g1 = p.cu_groups[g + 1], len = p.kv_lens[g];
+  const int b0 = min(max(g0, 0), p.sequences), b1 = min(max(g1, b0), p.sequences);
+  const int c0 = p.cu_q[b0], c1 = p.cu_q[b1];
+  const int64_t room = p.pages_per_seq << p.cache.page_shift;
+  const int most = (int)(room < p.max_kv ? room : p.max_kv);
+  const int q0 = min(max(c0, 0), p.T);
+  const int q1 = min(max(c1, q0), p.T);
+  const int n = q1 - q0;
+  e.q0 = q0;
+  e.kv = min(max(len, 0), most);
+  e.rows = min(n, p.max_q) * p.share;
+  e.first = e.kv - 1;
+  e.step = 0;
+  if (report && p.status && (b0 != g0 || b1 != g1 || q0 != c0 || q1 != c1 || n > p.max_q || e.kv != len)) *p.status = 1;
+  return e;
+}
+// Of a sequence, or with SHARED of whichever of the two the pass is over.
+template <bool SHARED>
+__device__ __forceinline__ Extent extent_in_pass(const AttentionParams& p, int b, bool report) {
+  if constexpr (SHARED)
+    if (p.cu_groups) return extent_of_group(p, b, report);
+  return extent_of(p, b, report);
+}
+
 // Position of the sequence's query i. Those before the first token see nothing, wherever they are: all at
 // -1, so that a window's width can be taken off any position in 32 bits.
-__device__ __forceinline__ int position(const Extent& e, int i) { return max(e.first + i, -1); }
+__device__ __forceinline__ int position(const Extent& e, int i) { return max(e.first + i * e.step, -1); }
 
 // Row r of a sequence and kv head: query i of the sequence, one of the heads that share.
 struct RowOf {
@@ -126,7 +155,7 @@ struct Shares {
   int count, end;  // slots of lane b's sequence, and up to its end
 
   __device__ __forceinline__ Shares(const AttentionParams& p, int lane, bool report) {
-    mine = lane < p.B ? extent_of(p, lane, report) : Extent{0, 0, 0, 0};
+    mine = lane < p.B ? extent_of(p, lane, report) : Extent{0, 0, 0, 0, 1};
     int steps = 0;
     if (mine.rows > 0) {
       steps = Steps<32>(position(mine, 0), position(mine, (mine.rows - 1) / p.share), p.window, p.sinks).count;
@@ -162,7 +191,7 @@ struct Shares {
   }
   __device__ __forceinline__ Extent extent(int b) const {
     return {__builtin_amdgcn_readlane(mine.q0, b), __builtin_amdgcn_readlane(mine.rows, b),
-            __builtin_amdgcn_readlane(mine.first, b), __builtin_amdgcn_readlane(mine.kv, b)};
+            __builtin_amdgcn_readlane(mine.first, b), __builtin_amdgcn_readlane(mine.kv, b), 1};
   }
 };
 

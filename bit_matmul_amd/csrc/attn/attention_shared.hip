@@ -1,0 +1,154 @@
+// Attention of groups of sequences that share their first tokens.
+//
+// The tokens that a group shares are gone over once for all its queries, as if these were one sequence's
+// whose every query sees every token; then each sequence's own tokens as in attention.hip. With both passes'
+// references m, sums l and outputs o (of exponents to the base 2, not normalised) a row is
+//   sum_s o_s 2^(m_s - m) / sum_s l_s 2^(m_s - m),  m = max_s m_s
+// over the parts s of both, which attention_join_shared_kernel adds up in f32.
+#include "attention_rows.hpp"
+
+namespace bitmm {
+namespace attn {
+namespace {
+
+// Joins a row's parts of both passes, as attention_join_kernel does those of one.
+template <int D>
+__global__ __launch_bounds__(256) void attention_join_shared_kernel(SharedParams both) {
+  constexpr int TPR = D / 4, GROUPS = 256 / TPR;
+  __shared__ f32x4_t sums[GROUPS][TPR];
+  __shared__ float part_l[GROUPS];
+  const AttentionParams &p = both.own, &shared = both.prefix;
+  const int unit = blockIdx.x / p.tail_rows, r = blockIdx.x - unit * p.tail_rows;
+  const int b = unit / p.cache.kv_heads, head = unit - b * p.cache.kv_heads;
+  const int lane = threadIdx.x & 63;
+  const int t = threadIdx.x % TPR, grp = threadIdx.x / TPR;
+  // The row's parts: every `step`-th from `first` on.
+  Extent ex;
+  int first = b, step = p.B, parts = p.splits;
+  if (p.balanced) {
+    const Shares shares(p, lane, blockIdx.x == 0);
+    const Share mine = shares.of_sequence(b);
+    ex = shares.extent(b);
+    first = mine.first;
+    step = 1;
+    parts = mine.count;
+  } else {
+    ex = extent_of(p, b, threadIdx.x == 0);
+  }
+  if (r >= ex.rows) return;
+  const int64_t row = part_row(p, first, head, r), all = part_row(p, step, 0, 0);
+  // Those of its group, the first that has the sequence.
+  int64_t shared_row = 0;
+  int shared_parts = 0;
+  for (int g0 = 0; g0 < shared.B; g0 += 64) {
+    const int g = g0 + lane;
+    const bool in = g < shared.B && shared.cu_groups[g] <= b && b < shared.cu_groups[g + 1];
+    const uint64_t found = __ballot(in);
+    if (!found) continue;
+    const int mine = g0 + __builtin_ctzll(found);
+    const Extent group = extent_of_group(shared, mine, threadIdx.x == 0);
+    const int64_t at = (int64_t)(ex.q0 - group.q0) * p.share + r;
+    if (at < 0 || at >= group.rows) return;  // past the bound of a group's queries
+    shared_row = part_row(shared, mine, head, (int)at);
+    shared_parts = shared.splits;
+    break;
+  }
+  const int64_t shared_all = part_row(shared, shared.B, 0, 0);
+  auto ml = [&](int s) {
+    return s < parts ? reinterpret_cast<const float2*>(p.part_ml)[s * all + row]
+                     : reinterpret_cast<const float2*>(shared.part_ml)[(s - parts) * shared_all + shared_row];
+  };
+  auto outputs = [&](int s) {
+    return (s < parts ? p.part_o + (s * all + row) * D : shared.part_o + ((s - parts) * shared_all + shared_row) * D) + 4 * t;
+  };
+  const int count = parts + shared_parts;
+  float mt = neg_inf();
+  for (int s = lane; s < count; s += 64) mt = fmaxf(mt, ml(s).x);
+  mt = reduce_lanes<64>(mt, Max());
+  f32x4_t y = {0.f, 0.f, 0.f, 0.f};
+  float lt = 0.f;
+#pragma unroll 4
+  for (int s = grp; s < count; s += GROUPS) {
+    const float2 part = ml(s);
+    const f32x4_t o = *reinterpret_cast<const f32x4_t*>(outputs(s));
+    if (part.y == 0.f) continue;  // saw nothing
+    const float w = part.x == mt ? 1.f : __builtin_amdgcn_exp2f(part.x - mt);
+    lt += part.y * w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] += o[e] * w;
+  }
+  sums[grp][t] = y;
+  if (t == 0) part_l[grp] = lt;
+  __syncthreads();
+  if (grp != 0) return;
+  lt = 0.f;
+  y = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < GROUPS; ++w) {
+    lt += part_l[w];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] += sums[w][t][e];
+  }
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  const RowOf out_row(p, head, r);
+  if (p.lse && t == 0) p.lse[(int64_t)(ex.q0 + out_row.i) * p.q_heads + out_row.head] = kLn2 * (mt + __builtin_amdgcn_logf(lt));
+  store4(p, (int64_t)(ex.q0 + out_row.i) * p.out_stride + (int64_t)out_row.head * D + 4 * t, y[0] * inv, y[1] * inv, y[2] * inv,
+         y[3] * inv);
+}
+
+void take(AttentionParams& p, const AttentionPlan& plan) {
+  p.row_tiles = plan.row_tiles;
+  p.tail_tiles = plan.tail_tiles;
+  p.tail_rows = plan.tail_rows;
+  p.splits = plan.splits;
+  p.balanced = plan.balanced;
+}
+
+hipError_t launch_pass(const AttentionParams& p, const AttentionPlan& plan, int dtype, hipStream_t stream) {
+  const unsigned n = (unsigned)plan.workgroups((int64_t)p.B * p.cache.kv_heads);
+  return plan.tiles ? launch_attention_tiles_shared(p, plan.rows_each, n, dtype, stream)
+                    : launch_attention_rows<true>(p, n, plan.waves, dtype, stream);
+}
+
+template <int D>
+void launch_join(const SharedParams& p, dim3 grid, hipStream_t stream) {
+  hipLaunchKernelGGL(attention_join_shared_kernel<D>, grid, dim3(256), 0, stream, p);
+  launch_log(grid, dim3(256), 256 * 16 + 256 / (D / 4) * 4, "attention_join_shared_kernel<%d>", D);
+}
+
+}  // namespace
+
+SharedPlan plan_attention_shared(int64_t groups, int64_t B, int64_t max_group_q, int64_t max_prefix, int64_t max_q,
+                                 int64_t max_kv, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+  auto pass = [&](int64_t n, int64_t queries, int64_t tokens) {
+    if (n == 0 || queries == 0) {
+      AttentionPlan none = {};
+      none.splits = 1;
+      return none;
+    }
+    AttentionPlan plan = plan_attention(n, queries, tokens, q_heads, kv_heads, head_dim, 0, 0);
+    // Whole rounds of row tiles are as partial as the last ones here: the other pass has the rest of their rows.
+    const int64_t tiles = n * kv_heads * plan.row_tiles;
+    plan.tail_tiles = plan.row_tiles;
+    plan.tail_rows = (int)(queries * (q_heads / kv_heads));
+    if (!plan.balanced) plan.splits = (int)std::max<int64_t>(1, std::min<int64_t>(plan.fill / tiles, plan.most));
+    return plan;
+  };
+  return {pass(groups, max_group_q, max_prefix), pass(B, max_q, max_kv)};
+}
+
+hipError_t launch_kv_attention_shared(SharedParams p, const SharedPlan& plan, int dtype, hipStream_t stream) {
+  take(p.prefix, plan.prefix);
+  take(p.own, plan.own);
+  hipError_t err = hipSuccess;
+  if (plan.prefix.row_tiles > 0) err = launch_pass(p.prefix, plan.prefix, dtype, stream);
+  if (err == hipSuccess) err = launch_pass(p.own, plan.own, dtype, stream);
+  if (err != hipSuccess) return err;
+  const dim3 grid((unsigned)((int64_t)p.own.B * p.own.cache.kv_heads * plan.own.tail_rows));
+  const int D = p.own.cache.head_dim;
+  D == 64 ? launch_join<64>(p, grid, stream) : D == 128 ? launch_join<128>(p, grid, stream) : launch_join<256>(p, grid, stream);
+  return hipGetLastError();
+}
+
+}  // namespace attn
+}  // namespace bitmm

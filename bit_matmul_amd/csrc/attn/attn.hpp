@@ -82,6 +82,10 @@ struct AttentionParams {
   bool balanced;
   int otype;
   float scale;
+  // In a pass over what groups of sequences share, else null: the sequences of group g are cu_groups[g] ..
+  // cu_groups[g + 1] of `sequences`, cu_q has the rows of each, and all else is the groups'.
+  const int32_t* cu_groups;
+  int sequences;
 };
 
 // How a call is cut up, from sizes alone, so that the workspace query and the call agree: the
@@ -91,6 +95,8 @@ struct AttentionParams {
 struct AttentionPlan {
   bool tiles;      // the kernel for many query rows
   int waves;       // of a workgroup, in the kernel for few rows
+  int fill;        // workgroups at a time
+  int most;        // parts that a tile's tokens may be split into
   int rows_each;   // rows of a tile
   int row_tiles;
   int tail_tiles;  // 0 where nothing is split
@@ -103,6 +109,22 @@ AttentionPlan plan_attention(int64_t B, int64_t max_q, int64_t max_kv, int64_t q
                              int64_t kv_heads, int64_t head_dim, int64_t window, int64_t sinks);
 hipError_t launch_kv_attention(AttentionParams p, const AttentionPlan& plan, int dtype,
                                hipStream_t stream);
+
+// Attention of groups of sequences that share their first tokens: a pass over what they share and a pass over
+// what each has of its own, whose partial results are joined.
+struct SharedParams {
+  AttentionParams prefix, own;
+};
+struct SharedPlan {
+  AttentionPlan prefix, own;  // all row tiles are partial
+};
+SharedPlan plan_attention_shared(int64_t groups, int64_t B, int64_t max_group_q, int64_t max_prefix, int64_t max_q,
+                                 int64_t max_kv, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+hipError_t launch_kv_attention_shared(SharedParams p, const SharedPlan& plan, int dtype, hipStream_t stream);
+
+// The same kernel's passes for many query rows (prefill_shared.hip).
+hipError_t launch_attention_tiles_shared(const AttentionParams& p, int rows_each, unsigned workgroups, int dtype,
+                                         hipStream_t stream);
 
 // The kernel for many query rows (prefill.hip).
 hipError_t launch_attention_tiles(const AttentionParams& p, int rows_each, unsigned workgroups, int dtype,

@@ -17,6 +17,15 @@ bool select_sizes_ok(int64_t groups, int64_t beams, int64_t vocab, int64_t k) {
   return beam_rows_ok(groups, beams) && vocab >= 1 && vocab <= 1 << 30 && k >= 1 && k <= 64;
 }
 
+bool shared_sizes_ok(int64_t T, int64_t B, int64_t groups, int64_t max_group_q, int64_t max_prefix, int64_t max_q,
+                     int64_t max_kv, int64_t q_heads, int64_t kv_heads) {
+  return attention_sizes_ok(T, B, max_q, max_kv, q_heads, kv_heads, 0, 0) &&
+         attention_sizes_ok(T, groups, max_group_q, max_prefix, q_heads, kv_heads, 0, 0);
+}
+
+// Floats of a pass's partial results: outputs, then references and sums.
+int64_t part_rows(const AttentionPlan& plan, int64_t B, int64_t kv_heads) { return (int64_t)plan.splits * B * kv_heads * plan.tail_rows; }
+
 }  // namespace
 
 extern "C" {
@@ -181,6 +190,95 @@ bitmm_status bitmm_kv_beam_reorder(const bitmm_kv_cache* caches, int64_t layers,
     p.code_pieces = c.head_dim / 32;
     p.groups_of_head = c.head_dim / c.group;
     return launched(launch_beam_reorder(p, caches, layers, groups, static_cast<hipStream_t>(stream)));
+  } catch (...) {
+    return BITMM_ERR_LAUNCH;
+  }
+}
+
+size_t bitmm_kv_attention_shared_workspace_bytes(int64_t T, int64_t B, int64_t groups, int64_t max_group_q,
+                                                 int64_t max_prefix, int64_t max_q, int64_t max_kv,
+                                                 int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+  if (!shared_sizes_ok(T, B, groups, max_group_q, max_prefix, max_q, max_kv, q_heads, kv_heads) || !head_dim_ok(head_dim)) return 0;
+  if (T == 0 || B == 0 || max_q == 0) return 0;
+  const SharedPlan plan = plan_attention_shared(groups, B, max_group_q, max_prefix, max_q, max_kv, q_heads, kv_heads, head_dim);
+  const size_t rows = (size_t)(part_rows(plan.prefix, groups, kv_heads) + part_rows(plan.own, B, kv_heads));
+  return (rows * (size_t)(head_dim + 2) * 4 + 255) / 256 * 256;
+}
+
+bitmm_status bitmm_kv_attention_shared(const void* q, int64_t q_stride, const bitmm_kv_cache* cache,
+                                       const int32_t* prefix_table, int64_t pages_per_prefix,
+                                       const int32_t* prefix_lens, const int32_t* cu_groups,
+                                       const int32_t* page_table, int64_t pages_per_seq,
+                                       const int32_t* kv_lens, const int32_t* cu_q, void* out,
+                                       int64_t out_stride, float* lse, int64_t T, int64_t B, int64_t groups,
+                                       int64_t q_heads, int64_t max_group_q, int64_t max_prefix,
+                                       int64_t max_q, int64_t max_kv, float scale, bitmm_dtype dtype,
+                                       bitmm_out out_type, void* workspace, size_t workspace_bytes,
+                                       uint32_t* status, void* stream) {
+  try {
+    bitmm::launch_log_begin();
+    bitmm_status st = check_cache(cache);
+    if (st != BITMM_OK) return st;
+    if (!dtype_ok(dtype)) return BITMM_ERR_UNSUPPORTED;
+    if (out_type != BITMM_OUT_BF16 && out_type != BITMM_OUT_F32 && out_type != BITMM_OUT_F16) return BITMM_ERR_UNSUPPORTED;
+    const int64_t kv_heads = cache->kv_heads, D = cache->head_dim;
+    if (!shared_sizes_ok(T, B, groups, max_group_q, max_prefix, max_q, max_kv, q_heads, kv_heads) || !fits_int(pages_per_prefix) ||
+        !fits_int(pages_per_seq))
+      return BITMM_ERR_SHAPE;
+    if (q_heads / kv_heads > 64 || B > 65535 || groups > 65535) return BITMM_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0 || max_q == 0) return BITMM_OK;
+    if ((st = check_rows(q, q_stride, q_heads, D)) != BITMM_OK) return st;
+    if ((st = check_rows(out, out_stride, q_heads, D)) != BITMM_OK) return st;
+    if ((pages_per_seq > 0 && !page_table) || !kv_lens || !cu_q) return BITMM_ERR_NULL;
+    if (groups > 0 && ((pages_per_prefix > 0 && !prefix_table) || !prefix_lens || !cu_groups)) return BITMM_ERR_NULL;
+    if (!aligned(prefix_table, 4) || !aligned(prefix_lens, 4) || !aligned(cu_groups, 4) || !aligned(page_table, 4) ||
+        !aligned(kv_lens, 4) || !aligned(cu_q, 4) || !aligned(lse, 4) || !aligned(status, 4) || !aligned(workspace, 16))
+      return BITMM_ERR_ALIGN;
+    const SharedPlan plan = plan_attention_shared(groups, B, max_group_q, max_prefix, max_q, max_kv, q_heads, kv_heads, D);
+    // A launch's threads are counted in 32 bits.
+    const int64_t limit = ((int64_t)1 << 32) / 512 - 1;
+    if (plan.prefix.workgroups(groups * kv_heads) > limit || plan.own.workgroups(B * kv_heads) > limit ||
+        groups * kv_heads * plan.prefix.tail_rows > INT32_MAX || B * kv_heads * plan.own.tail_rows > limit)
+      return BITMM_ERR_UNSUPPORTED;
+    const size_t need = bitmm_kv_attention_shared_workspace_bytes(T, B, groups, max_group_q, max_prefix, max_q, max_kv, q_heads,
+                                                                  kv_heads, D);
+    if (!workspace || workspace_bytes < need) return BITMM_ERR_WORKSPACE;
+    if ((st = device_check()) != BITMM_OK) return st;
+    AttentionParams p = {};
+    p.q = static_cast<const uint16_t*>(q);
+    p.cache = view(cache);
+    p.page_table = page_table;
+    p.kv_lens = kv_lens;
+    p.cu_q = cu_q;
+    p.out = out;
+    p.lse = lse;
+    p.status = status;
+    p.q_stride = q_stride;
+    p.out_stride = out_stride;
+    p.pages_per_seq = pages_per_seq;
+    p.T = (int)T;
+    p.B = (int)B;
+    p.q_heads = (int)q_heads;
+    p.share = (int)(q_heads / kv_heads);
+    p.max_q = (int)max_q;
+    p.max_kv = (int)max_kv;
+    p.otype = out_type == BITMM_OUT_F32 ? bitmm::kOutF32 : (out_type == BITMM_OUT_F16 ? bitmm::kOutF16 : bitmm::kOutBf16);
+    p.scale = scale;
+    SharedParams both = {p, p};
+    both.prefix.page_table = prefix_table;
+    both.prefix.kv_lens = prefix_lens;
+    both.prefix.pages_per_seq = pages_per_prefix;
+    both.prefix.B = (int)groups;
+    both.prefix.max_q = (int)max_group_q;
+    both.prefix.max_kv = (int)max_prefix;
+    both.prefix.cu_groups = cu_groups;
+    both.prefix.sequences = (int)B;
+    const int64_t prefix_rows = part_rows(plan.prefix, groups, kv_heads), own_rows = part_rows(plan.own, B, kv_heads);
+    both.prefix.part_o = static_cast<float*>(workspace);
+    both.own.part_o = both.prefix.part_o + prefix_rows * D;
+    both.prefix.part_ml = both.own.part_o + own_rows * D;
+    both.own.part_ml = both.prefix.part_ml + 2 * prefix_rows;
+    return launched(launch_kv_attention_shared(both, plan, (int)dtype, static_cast<hipStream_t>(stream)));
   } catch (...) {
     return BITMM_ERR_LAUNCH;
   }

@@ -79,5 +79,13 @@ inline bitmm_status check_rows(const void* p, int64_t stride, int64_t heads, int
 
 inline bitmm_status launched(hipError_t e) { return e == hipSuccess ? BITMM_OK : BITMM_ERR_LAUNCH; }
 
+inline bool attention_sizes_ok(int64_t T, int64_t B, int64_t max_q, int64_t max_kv, int64_t q_heads,
+                        int64_t kv_heads, int64_t window, int64_t sinks) {
+  // max_kv leaves room for the last step past it.
+  return fits_int(T) && fits_int(B) && fits_int(max_q) && max_kv >= 0 && max_kv <= INT32_MAX - 1024 &&
+         q_heads >= 1 && q_heads <= INT32_MAX && kv_heads >= 1 && kv_heads <= 65535 && q_heads % kv_heads == 0 &&
+         fits_int(window) && fits_int(sinks) && max_q * (q_heads / kv_heads) <= INT32_MAX - 1024;
+}
+
 }  // namespace attn
 }  // namespace bitmm

@@ -4,6 +4,7 @@
  * the activation rows and the status word of bitmm_attn.h hold here too.
  *
  *   bitmm_qk_norm_rope_append   head norms, position rotation and the append to the cache
+ *   bitmm_kv_attention_shared   attention of sequences that share their first tokens, in groups
  *   bitmm_beam_select           the best continuations of a group of beams
  *   bitmm_kv_beam_reorder       the cached states in the order of the beams that go on
  *
@@ -39,6 +40,41 @@ bitmm_status bitmm_qk_norm_rope_append(const void* q, int64_t q_stride, const vo
                                        const int64_t* slots, const bitmm_kv_cache* cache, int64_t T,
                                        int64_t q_heads, int64_t rot_dim, int interleaved, float eps,
                                        float weight_offset, float rope_scale, bitmm_dtype dtype,
+                                       uint32_t* status, void* stream);
+
+/*
+ * Attention of sequences that share their first tokens with the others of their group: a prompt's
+ * beams or samples, or requests behind one system prompt. What they share is stored and read once.
+ *   cu_groups    int32 [groups + 1]: the sequences of group g are cu_groups[g] .. cu_groups[g + 1] - 1
+ *   prefix_table int32 [groups, pages_per_prefix], prefix_lens int32 [groups]: the shared tokens' pages and
+ *                their number
+ *   page_table   int32 [B, pages_per_seq], kv_lens int32 [B]: each sequence's own tokens, the queries' among
+ *                them, on pages of their own (a prefix may end within a page)
+ *   cu_q         int32 [B + 1]: the rows of each sequence's queries
+ * q, out, lse, scale, types and status are bitmm_kv_attention's. A query sees all shared tokens of its group
+ * and its sequence's own ones up to its own position, which is that of bitmm_kv_attention over the own
+ * tokens alone. A sequence of no group has its own tokens alone. The result is that of bitmm_kv_attention
+ * over shared and own tokens in a row, with another order of sums; there is no window (the shared part of one
+ * is short: use bitmm_kv_attention).
+ * max_group_q bounds the queries of a group, max_prefix the shared tokens, max_q and max_kv the queries
+ * and own tokens of a sequence; what passes them is cut and sets *status, and rows past them are not written.
+ * `workspace`: bitmm_kv_attention_shared_workspace_bytes(...) bytes, 16-byte aligned, no initialisation
+ * needed; two calls that share it must be ordered on one stream.
+ * Limits (else BITMM_ERR_UNSUPPORTED): q_heads / kv_heads <= 64; B and groups <= 65535; B times kv_heads times the
+ * query rows of a sequence's kv head < 2^23.
+ */
+size_t bitmm_kv_attention_shared_workspace_bytes(int64_t T, int64_t B, int64_t groups, int64_t max_group_q,
+                                                 int64_t max_prefix, int64_t max_q, int64_t max_kv,
+                                                 int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+bitmm_status bitmm_kv_attention_shared(const void* q, int64_t q_stride, const bitmm_kv_cache* cache,
+                                       const int32_t* prefix_table, int64_t pages_per_prefix,
+                                       const int32_t* prefix_lens, const int32_t* cu_groups,
+                                       const int32_t* page_table, int64_t pages_per_seq,
+                                       const int32_t* kv_lens, const int32_t* cu_q, void* out,
+                                       int64_t out_stride, float* lse, int64_t T, int64_t B, int64_t groups,
+                                       int64_t q_heads, int64_t max_group_q, int64_t max_prefix,
+                                       int64_t max_q, int64_t max_kv, float scale, bitmm_dtype dtype,
+                                       bitmm_out out_type, void* workspace, size_t workspace_bytes,
                                        uint32_t* status, void* stream);
 
 /*

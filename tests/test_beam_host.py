@@ -200,3 +200,65 @@ def test_reorder_binding_refuses():
                       (TypeError, dict(parents=parents.long())), (ValueError, dict(ws=ws[::2])), (ValueError, {})]:
         with pytest.raises(error):
             call(**kw)
+
+
+def shared(L, desc="", **kw):
+    d = dict(q=P, qs=1024, cache=cache() if desc == "" else desc, pt=P, pp=4, pl=P, cg=P, table=P, pages=4, lens=P, cu=P, out=P,
+             os=1024, lse=P, T=12, B=6, G=2, hq=8, mgq=6, mp=100, mq=2, mkv=50, scale=0.1, dtype=0, otype=0, ws=P, ws_bytes=1 << 40,
+             status=None, stream=None)
+    d.update(kw)
+    return L.bitmm_kv_attention_shared(*d.values())
+
+
+@pytest.mark.parametrize("kw, want", [
+    (dict(desc=None), "NULL"), (dict(dtype=2), "UNSUPPORTED"), (dict(otype=3), "UNSUPPORTED"), (dict(T=-1), "SHAPE"), (dict(B=-1), "SHAPE"),
+    (dict(G=-1), "SHAPE"), (dict(hq=0), "SHAPE"), (dict(hq=7), "SHAPE"), (dict(mgq=-1), "SHAPE"), (dict(mp=-1), "SHAPE"),
+    (dict(mp=2 ** 31 - 1), "SHAPE"), (dict(mq=-1), "SHAPE"), (dict(mkv=2 ** 31), "SHAPE"), (dict(pp=-1), "SHAPE"), (dict(pages=2 ** 31), "SHAPE"),
+    (dict(mgq=2 ** 30), "SHAPE"), (dict(hq=130, qs=130 * 128, os=130 * 128), "UNSUPPORTED"), (dict(B=65536), "UNSUPPORTED"),
+    (dict(G=65536), "UNSUPPORTED"), (dict(qs=1016), "SHAPE"), (dict(os=1020), "SHAPE"), (dict(qs=1028), "ALIGN"), (dict(q=None), "NULL"),
+    (dict(out=None), "NULL"), (dict(pt=None), "NULL"), (dict(pl=None), "NULL"), (dict(cg=None), "NULL"), (dict(table=None), "NULL"),
+    (dict(lens=None), "NULL"), (dict(cu=None), "NULL"), (dict(q=P + 8), "ALIGN"), (dict(pt=P + 2), "ALIGN"), (dict(pl=P + 2), "ALIGN"),
+    (dict(cg=P + 1), "ALIGN"), (dict(lse=P + 2), "ALIGN"), (dict(ws=P + 8), "ALIGN"), (dict(status=P + 2), "ALIGN"),
+    (dict(ws=None), "WORKSPACE"), (dict(ws_bytes=1024), "WORKSPACE"), (dict(B=60000, T=2 ** 24, mq=200), "UNSUPPORTED"),
+])
+def test_shared_refusals(L, kw, want):
+    assert shared(L, **kw) == status(want)
+    assert bm.bitmm_last_launches() == []
+
+
+def test_shared_empty_and_workspace(L):
+    for kw in (dict(T=0), dict(B=0), dict(mq=0)):
+        assert shared(L, **kw, q=None, out=None, ws=None) == bm.BITMM_OK
+    for kw, want in CACHE_FAULTS:
+        assert shared(L, desc=cache(**kw)) == status(want)
+    need = bm.bitmm_kv_attention_shared_workspace_bytes
+    assert need(12, 6, 2, 6, 100, 2, 50, 7, 2, 128) == 0 and need(12, 6, 2, 6, 100, 2, 50, 8, 2, 96) == 0 and need(0, 6, 2, 6, 100, 2, 50, 8, 2, 128) == 0
+    for G, mgq, mp, mkv in ((0, 0, 0, 50), (2, 0, 0, 0), (2, 6, 0, 0), (2, 6, 100, 50), (1, 12, 10 ** 6, 0), (6, 2, 1, 10 ** 6)):
+        n = need(12, 6, G, mgq, mp, 2, mkv, 8, 2, 128)
+        # a partial result of each query row of both passes at least
+        assert n >= 4 * 130 * 2 * (G * mgq * 4 + 6 * 2 * 4)
+        if not torch.cuda.is_available():
+            kw = dict(G=G, mgq=mgq, mp=mp, mkv=mkv, ws_bytes=n)
+            if G == 0:
+                kw.update(pt=None, pl=None, cg=None)
+            assert shared(L, **kw) == bm.BITMM_ERR_DEVICE
+            assert shared(L, **{**kw, "ws_bytes": n - 1}) == bm.BITMM_ERR_WORKSPACE
+
+
+def test_shared_binding_refuses():
+    i32, bf = torch.int32, torch.bfloat16
+    q, out = torch.zeros(6, 4, 64, dtype=bf), torch.zeros(6, 4, 64, dtype=bf)
+    pt, pl, cg = torch.zeros(2, 3, dtype=i32), torch.zeros(2, dtype=i32), torch.zeros(3, dtype=i32)
+    table, lens, cu, ws = torch.zeros(6, 2, dtype=i32), torch.zeros(6, dtype=i32), torch.zeros(7, dtype=i32), torch.zeros(1 << 20, dtype=torch.uint8)
+
+    def call(q=q, pt=pt, pl=pl, cg=cg, table=table, lens=lens, cu=cu, out=out, ws=ws, lse=None):
+        return bm.bitmm_kv_attention_shared(q, _Host(), pt, pl, cg, table, lens, cu, out, ws, max_group_q=3, max_prefix=40, max_q=1,
+                                            max_kv=30, lse=lse)
+
+    for error, kw in [(TypeError, dict(q=q.float())), (TypeError, dict(out=out.double())), (ValueError, dict(q=q[:, :, :32])),
+                      (ValueError, dict(out=out[:5])), (ValueError, dict(pt=pt[0])), (ValueError, dict(pt=pt[:1])), (TypeError, dict(pl=pl.long())),
+                      (ValueError, dict(cg=cg[:2])), (ValueError, dict(table=table[0])), (ValueError, dict(table=table[:5])),
+                      (ValueError, dict(cu=cu[:6])), (ValueError, dict(ws=ws[::2])), (ValueError, dict(lse=torch.zeros(6, 3))),
+                      (ValueError, {})]:
+        with pytest.raises(error):
+            call(**kw)
