@@ -140,7 +140,7 @@ hipError_t launch_kv_attention(AttentionParams p, const AttentionPlan& plan, int
   const int64_t groups = (int64_t)p.B * p.cache.kv_heads;
   const unsigned n = (unsigned)plan.workgroups(groups);
   hipError_t err = plan.tiles ? launch_attention_tiles(p, plan.rows_each, n, dtype, stream)
-                              : launch_attention_rows<false>(p, n, plan.waves, dtype, stream);
+                              : launch_attention_rows<kAlone>(p, p.cache, n, plan.waves, dtype, stream);
   if (err != hipSuccess || plan.splits == 1) return err;
   const dim3 grid((unsigned)(groups * plan.tail_rows)), block(256);
   if (D == 64)

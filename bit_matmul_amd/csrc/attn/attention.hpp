@@ -94,12 +94,9 @@ __device__ __forceinline__ Extent extent_of_group(const AttentionParams& p, int 
   if (report && p.status && (b0 != g0 || b1 != g1 || q0 != c0 || q1 != c1 || n > p.max_q || e.kv != len)) *p.status = 1;
   return e;
 }
-// Of a sequence, or with SHARED of whichever of the two the pass is over.
-template <bool SHARED>
+template <int PASS>
 __device__ __forceinline__ Extent extent_in_pass(const AttentionParams& p, int b, bool report) {
-  if constexpr (SHARED)
-    if (p.cu_groups) return extent_of_group(p, b, report);
-  return extent_of(p, b, report);
+  return PASS == kPrefix ? extent_of_group(p, b, report) : extent_of(p, b, report);
 }
 
 // Position of the sequence's query i. Those before the first token see nothing, wherever they are: all at
@@ -242,6 +239,42 @@ struct Work {
 __device__ __forceinline__ int64_t part_row(const AttentionParams& p, int part, int head, int r) {
   return ((int64_t)part * p.cache.kv_heads + head) * p.tail_rows + r;
 }
+
+// The same in the pass over shared tokens: the first parts of all rows, then the others of those that have more.
+__device__ __forceinline__ int64_t prefix_row(const AttentionParams& p, int split, int g, int head, int r) {
+  const int64_t rows = (int64_t)p.max_q * p.share;
+  return split == 0 ? ((int64_t)g * p.cache.kv_heads + head) * rows + r
+                    : (int64_t)p.B * p.cache.kv_heads * rows + (((int64_t)(split - 1) * p.B + g) * p.cache.kv_heads + head) * p.tail_rows + r;
+}
+template <int PASS>
+__device__ __forceinline__ int64_t partial_row(const AttentionParams& p, const Work& work, int part, int r) {
+  return PASS == kPrefix ? prefix_row(p, work.split, work.b, work.head, r) : part_row(p, part, work.head, r);
+}
+
+// The results over shared tokens that belong to a sequence's rows: those of its group, the first that has it.
+struct SharedRows {  // made by a whole wave
+  int group = -1;
+  int64_t first = 0;  // the group's row that is the sequence's first
+  int rows = 0;       // of the group
+  __device__ __forceinline__ SharedRows() {}
+  __device__ __forceinline__ SharedRows(const AttentionParams& prefix, const Extent& ex, int b, int lane, bool report) {
+    for (int g0 = 0; g0 < prefix.B; g0 += 64) {
+      const int g = g0 + lane;
+      const uint64_t found = __ballot(g < prefix.B && prefix.cu_groups[g] <= b && b < prefix.cu_groups[g + 1]);
+      if (!found) continue;
+      group = g0 + __builtin_ctzll(found);
+      const Extent e = extent_of_group(prefix, group, report);
+      first = (int64_t)(ex.q0 - e.q0) * prefix.share;
+      rows = e.rows;
+      return;
+    }
+  }
+  // Rows past the bound of a group's queries have no result over the shared tokens: they are not written.
+  __device__ __forceinline__ bool has(int r) const { return group < 0 || (first + r >= 0 && first + r < rows); }
+  __device__ __forceinline__ int parts(const AttentionParams& prefix, int r) const {
+    return group < 0 ? 0 : first + r < prefix.tail_rows ? prefix.splits : 1;
+  }
+};
 
 // The steps [first, last) of part `split` of `splits`: the first ones take one more where the
 // count does not divide.

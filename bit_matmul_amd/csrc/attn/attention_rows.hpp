@@ -187,12 +187,12 @@ struct Rows {
   Extent ex;
   int part, r0, rows;  // no rows: nothing to do
 };
-template <bool SHARED>
+template <int PASS>
 __device__ __forceinline__ Rows rows_of(const AttentionParams& p, int tid, int workgroup) {
   Work work(p, workgroup);
   Extent ex;
   int part = work.split * p.B + work.b;
-  if (p.balanced) {
+  if (PASS != kPrefix && p.balanced) {
     part = workgroup / p.cache.kv_heads;
     work.head = workgroup - part * p.cache.kv_heads;
     const Shares shares(p, tid & 63, workgroup == 0);
@@ -203,7 +203,7 @@ __device__ __forceinline__ Rows rows_of(const AttentionParams& p, int tid, int w
     ex = shares.extent(work.b);
     if (mine.b < 0) ex.rows = 0;
   } else {
-    ex = extent_in_pass<SHARED>(p, work.b, tid == 0);
+    ex = extent_in_pass<PASS>(p, work.b, tid == 0);
   }
   const int r0 = work.row_tile * kRows;
   return {work, ex, part, r0, min(kRows, ex.rows - r0)};
@@ -593,18 +593,18 @@ __device__ __forceinline__ bool gather_rows(const AttentionParams& p, const Rows
   return CAREFUL || !__any(!k_sizes.fit(uk) || !v_sizes.fit(uv));
 }
 
-// SHARED: one of two passes, whose results are joined with the other's: all are partial.
-template <int D, int GS, int DT, int WAVES, bool SHARED>
-__global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_kernel(AttentionParams p) {
+template <int D, int GS, int DT, int WAVES, int PASS>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_kernel(typename PassParams<PASS>::Type params) {
+  const AttentionParams& p = params_of(params);
   constexpr int J = D / 16;
   __shared__ RowsLds<D, GS, WAVES> mem;
-  const Rows own = rows_of<SHARED>(p, threadIdx.x, blockIdx.x);
+  const Rows own = rows_of<PASS>(p, threadIdx.x, blockIdx.x);
   if (own.rows <= 0) return;
   Gathered<D> got;
   if (!gather_rows<D, GS, DT, WAVES, false>(p, own, threadIdx.x, mem, got)) {
     const AttentionParams& again = params_again();
     const int same = opaque((int)threadIdx.x);
-    gather_rows<D, GS, DT, WAVES, true>(again, rows_of<SHARED>(again, same, scalar_again(blockIdx.x)), same, mem, got);
+    gather_rows<D, GS, DT, WAVES, true>(again, rows_of<PASS>(again, same, scalar_again(blockIdx.x)), same, mem, got);
   }
   f32x4_t(&o)[J] = got.o;
   float m = got.m, l = got.l;
@@ -638,6 +638,10 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
 #pragma unroll
     for (int e = 0; e < 4; ++e) o_lds[wave][4 * j + e][lane] = o[j][e] * mine;
   __syncthreads();
+  auto partial = [&] { return PASS == kPrefix || (p.splits > 1 && (p.balanced || work.splits > 1)); };
+  SharedRows shared;
+  if constexpr (PASS == kOwn)
+    if (!partial()) shared = SharedRows(params.prefix, ex, work.b, lane, threadIdx.x == 0);  // with all lanes
   if (r0 + n >= ex.rows) return;
   constexpr int PARTS = WAVES / 4 < J / 4 ? WAVES / 4 : J / 4;  // of a lane's J dims, four or more each
   constexpr int JP = J / PARTS;
@@ -653,8 +657,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   const int dim0 = (4 * g + i4) * J + j0;
   const bool speaker = g == 0 && wave == 0;
   const int row = opaque(r0 + n);
-  if (SHARED || (p.splits > 1 && (p.balanced || work.splits > 1))) {
-    const int64_t at = part_row(p, own.part, head, row);
+  if (partial()) {
+    const int64_t at = partial_row<PASS>(p, work, own.part, row);
     if (speaker) {
       p.part_ml[2 * at] = mt;
       p.part_ml[2 * at + 1] = lt;
@@ -664,6 +668,26 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
       *reinterpret_cast<f32x4_t*>(p.part_o + at * D + dim0 + j) = f32x4_t{y[j], y[j + 1], y[j + 2], y[j + 3]};
     return;
   }
+  if constexpr (PASS == kOwn) {
+    const AttentionParams& prefix = params.prefix;
+    if (!shared.has(row)) return;
+    const int parts = shared.parts(prefix, row);
+#pragma unroll 2
+    for (int s = 0; s < parts; ++s) {
+      const int64_t at = prefix_row(prefix, s, shared.group, head, (int)shared.first + row);
+      const float2 ml = *reinterpret_cast<const float2*>(prefix.part_ml + 2 * at);
+      f32x4_t o4[JP / 4];
+#pragma unroll
+      for (int j = 0; j < JP / 4; ++j) o4[j] = *reinterpret_cast<const f32x4_t*>(prefix.part_o + at * D + dim0 + 4 * j);
+      if (ml.y == 0.f) continue;  // saw nothing
+      const float top = fmaxf(mt, ml.x);
+      const float mine = mt == top ? 1.f : __builtin_amdgcn_exp2f(mt - top), other = ml.x == top ? 1.f : __builtin_amdgcn_exp2f(ml.x - top);
+      mt = top;
+      lt = lt * mine + ml.y * other;
+#pragma unroll
+      for (int j = 0; j < JP; ++j) y[j] = y[j] * mine + o4[j / 4][j % 4] * other;
+    }
+  }
   const RowOf out_row(p, head, row);
   const float inv = lt == 0.f ? 0.f : 1.f / lt;
   if (p.lse && speaker) p.lse[(int64_t)(ex.q0 + out_row.i) * p.q_heads + out_row.head] = kLn2 * (mt + __builtin_amdgcn_logf(lt));
@@ -672,36 +696,41 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   for (int j = 0; j < JP; j += 4) store4(p, at + j, y[j] * inv, y[j + 1] * inv, y[j + 2] * inv, y[j + 3] * inv);
 }
 
-template <int D, int GS, int WAVES, bool SHARED>
-hipError_t launch_rows(const AttentionParams& p, unsigned workgroups, int dtype, hipStream_t stream) {
+template <int D, int GS, int WAVES, int PASS>
+hipError_t launch_rows(const typename PassParams<PASS>::Type& p, unsigned workgroups, int dtype, hipStream_t stream) {
   const dim3 grid(workgroups), block(64 * WAVES);
   if (dtype == 0)
-    hipLaunchKernelGGL((attention_rows_kernel<D, GS, 0, WAVES, SHARED>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((attention_rows_kernel<D, GS, 0, WAVES, PASS>), grid, block, 0, stream, p);
   else
-    hipLaunchKernelGGL((attention_rows_kernel<D, GS, 1, WAVES, SHARED>), grid, block, 0, stream, p);
-  launch_log(grid, block, sizeof(RowsLds<D, GS, WAVES>), SHARED ? "attention_rows_kernel<%d, %d, %d, %d, 1>" : "attention_rows_kernel<%d, %d, %d, %d>", D, GS, dtype, WAVES);
+    hipLaunchKernelGGL((attention_rows_kernel<D, GS, 1, WAVES, PASS>), grid, block, 0, stream, p);
+  static const char* const names[] = {"attention_rows_kernel<%d, %d, %d, %d>", "attention_rows_kernel<%d, %d, %d, %d, prefix>",
+                                      "attention_rows_kernel<%d, %d, %d, %d, own>"};
+  launch_log(grid, block, sizeof(RowsLds<D, GS, WAVES>), names[PASS], D, GS, dtype, WAVES);
   return hipGetLastError();
 }
 
-template <int D, int GS, bool SHARED>
-hipError_t launch_waves(const AttentionParams& p, unsigned workgroups, int waves, int dtype, hipStream_t stream) {
-  return waves == 4 ? launch_rows<D, GS, 4, SHARED>(p, workgroups, dtype, stream) : launch_rows<D, GS, 8, SHARED>(p, workgroups, dtype, stream);
+template <int D, int GS, int PASS>
+hipError_t launch_waves(const typename PassParams<PASS>::Type& p, unsigned workgroups, int waves, int dtype, hipStream_t stream) {
+  return waves == 4 ? launch_rows<D, GS, 4, PASS>(p, workgroups, dtype, stream)
+                    : launch_rows<D, GS, 8, PASS>(p, workgroups, dtype, stream);
 }
 
-template <int D, bool SHARED>
-hipError_t launch_groups(const AttentionParams& p, unsigned workgroups, int waves, int dtype, hipStream_t stream) {
-  if (p.cache.group == 32) return launch_waves<D, 32, SHARED>(p, workgroups, waves, dtype, stream);
-  if (p.cache.group == 64) return launch_waves<D, 64, SHARED>(p, workgroups, waves, dtype, stream);
-  if constexpr (D >= 128) return launch_waves<D, 128, SHARED>(p, workgroups, waves, dtype, stream);
+template <int D, int PASS>
+hipError_t launch_groups(const typename PassParams<PASS>::Type& p, int group, unsigned workgroups, int waves, int dtype,
+                         hipStream_t stream) {
+  if (group == 32) return launch_waves<D, 32, PASS>(p, workgroups, waves, dtype, stream);
+  if (group == 64) return launch_waves<D, 64, PASS>(p, workgroups, waves, dtype, stream);
+  if constexpr (D >= 128) return launch_waves<D, 128, PASS>(p, workgroups, waves, dtype, stream);
   return hipErrorInvalidValue;
 }
 
 // The kernel for few query rows.
-template <bool SHARED>
-hipError_t launch_attention_rows(const AttentionParams& p, unsigned workgroups, int waves, int dtype, hipStream_t stream) {
-  return p.cache.head_dim == 64    ? launch_groups<64, SHARED>(p, workgroups, waves, dtype, stream)
-         : p.cache.head_dim == 128 ? launch_groups<128, SHARED>(p, workgroups, waves, dtype, stream)
-                                   : launch_groups<256, SHARED>(p, workgroups, waves, dtype, stream);
+template <int PASS>
+hipError_t launch_attention_rows(const typename PassParams<PASS>::Type& p, const Cache& c, unsigned workgroups, int waves,
+                                 int dtype, hipStream_t stream) {
+  return c.head_dim == 64    ? launch_groups<64, PASS>(p, c.group, workgroups, waves, dtype, stream)
+         : c.head_dim == 128 ? launch_groups<128, PASS>(p, c.group, workgroups, waves, dtype, stream)
+                             : launch_groups<256, PASS>(p, c.group, workgroups, waves, dtype, stream);
 }
 
 }  // namespace

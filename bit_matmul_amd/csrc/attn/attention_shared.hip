@@ -4,7 +4,8 @@
 // whose every query sees every token; then each sequence's own tokens as in attention.hip. With both passes'
 // references m, sums l and outputs o (of exponents to the base 2, not normalised) a row is
 //   sum_s o_s 2^(m_s - m) / sum_s l_s 2^(m_s - m),  m = max_s m_s
-// over the parts s of both, which attention_join_shared_kernel adds up in f32.
+// over the parts s of both, added up in f32: by the second pass where it ends a row, else, where a row's own tokens
+// are split, by attention_join_shared_kernel.
 #include "attention_rows.hpp"
 
 namespace bitmm {
@@ -17,7 +18,7 @@ __global__ __launch_bounds__(256) void attention_join_shared_kernel(SharedParams
   constexpr int TPR = D / 4, GROUPS = 256 / TPR;
   __shared__ f32x4_t sums[GROUPS][TPR];
   __shared__ float part_l[GROUPS];
-  const AttentionParams &p = both.own, &shared = both.prefix;
+  const AttentionParams &p = both.own, &prefix = both.prefix;
   const int unit = blockIdx.x / p.tail_rows, r = blockIdx.x - unit * p.tail_rows;
   const int b = unit / p.cache.kv_heads, head = unit - b * p.cache.kv_heads;
   const int lane = threadIdx.x & 63;
@@ -37,40 +38,22 @@ __global__ __launch_bounds__(256) void attention_join_shared_kernel(SharedParams
   }
   if (r >= ex.rows) return;
   const int64_t row = part_row(p, first, head, r), all = part_row(p, step, 0, 0);
-  // Those of its group, the first that has the sequence.
-  int64_t shared_row = 0;
-  int shared_parts = 0;
-  for (int g0 = 0; g0 < shared.B; g0 += 64) {
-    const int g = g0 + lane;
-    const bool in = g < shared.B && shared.cu_groups[g] <= b && b < shared.cu_groups[g + 1];
-    const uint64_t found = __ballot(in);
-    if (!found) continue;
-    const int mine = g0 + __builtin_ctzll(found);
-    const Extent group = extent_of_group(shared, mine, threadIdx.x == 0);
-    const int64_t at = (int64_t)(ex.q0 - group.q0) * p.share + r;
-    if (at < 0 || at >= group.rows) return;  // past the bound of a group's queries
-    shared_row = part_row(shared, mine, head, (int)at);
-    shared_parts = shared.splits;
-    break;
-  }
-  const int64_t shared_all = part_row(shared, shared.B, 0, 0);
-  auto ml = [&](int s) {
-    return s < parts ? reinterpret_cast<const float2*>(p.part_ml)[s * all + row]
-                     : reinterpret_cast<const float2*>(shared.part_ml)[(s - parts) * shared_all + shared_row];
-  };
-  auto outputs = [&](int s) {
-    return (s < parts ? p.part_o + (s * all + row) * D : shared.part_o + ((s - parts) * shared_all + shared_row) * D) + 4 * t;
-  };
+  const SharedRows shared(prefix, ex, b, lane, threadIdx.x == 0);
+  if (!shared.has(r)) return;
+  const int shared_parts = shared.parts(prefix, r);
+  // A part's place among those of its pass.
+  auto at = [&](int s) { return s < parts ? s * all + row : prefix_row(prefix, s - parts, shared.group, head, (int)shared.first + r); };
   const int count = parts + shared_parts;
   float mt = neg_inf();
-  for (int s = lane; s < count; s += 64) mt = fmaxf(mt, ml(s).x);
+  for (int s = lane; s < count; s += 64) mt = fmaxf(mt, (s < parts ? p : prefix).part_ml[2 * at(s)]);
   mt = reduce_lanes<64>(mt, Max());
   f32x4_t y = {0.f, 0.f, 0.f, 0.f};
   float lt = 0.f;
 #pragma unroll 4
   for (int s = grp; s < count; s += GROUPS) {
-    const float2 part = ml(s);
-    const f32x4_t o = *reinterpret_cast<const f32x4_t*>(outputs(s));
+    const AttentionParams& from = s < parts ? p : prefix;
+    const float2 part = *reinterpret_cast<const float2*>(from.part_ml + 2 * at(s));
+    const f32x4_t o = *reinterpret_cast<const f32x4_t*>(from.part_o + at(s) * D + 4 * t);
     if (part.y == 0.f) continue;  // saw nothing
     const float w = part.x == mt ? 1.f : __builtin_amdgcn_exp2f(part.x - mt);
     lt += part.y * w;
@@ -104,12 +87,6 @@ void take(AttentionParams& p, const AttentionPlan& plan) {
   p.balanced = plan.balanced;
 }
 
-hipError_t launch_pass(const AttentionParams& p, const AttentionPlan& plan, int dtype, hipStream_t stream) {
-  const unsigned n = (unsigned)plan.workgroups((int64_t)p.B * p.cache.kv_heads);
-  return plan.tiles ? launch_attention_tiles_shared(p, plan.rows_each, n, dtype, stream)
-                    : launch_attention_rows<true>(p, n, plan.waves, dtype, stream);
-}
-
 template <int D>
 void launch_join(const SharedParams& p, dim3 grid, hipStream_t stream) {
   hipLaunchKernelGGL(attention_join_shared_kernel<D>, grid, dim3(256), 0, stream, p);
@@ -120,33 +97,32 @@ void launch_join(const SharedParams& p, dim3 grid, hipStream_t stream) {
 
 SharedPlan plan_attention_shared(int64_t groups, int64_t B, int64_t max_group_q, int64_t max_prefix, int64_t max_q,
                                  int64_t max_kv, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
-  auto pass = [&](int64_t n, int64_t queries, int64_t tokens) {
-    if (n == 0 || queries == 0) {
-      AttentionPlan none = {};
-      none.splits = 1;
-      return none;
-    }
-    AttentionPlan plan = plan_attention(n, queries, tokens, q_heads, kv_heads, head_dim, 0, 0);
-    // Whole rounds of row tiles are as partial as the last ones here: the other pass has the rest of their rows.
-    const int64_t tiles = n * kv_heads * plan.row_tiles;
-    plan.tail_tiles = plan.row_tiles;
-    plan.tail_rows = (int)(queries * (q_heads / kv_heads));
-    if (!plan.balanced) plan.splits = (int)std::max<int64_t>(1, std::min<int64_t>(plan.fill / tiles, plan.most));
-    return plan;
-  };
-  return {pass(groups, max_group_q, max_prefix), pass(B, max_q, max_kv)};
+  SharedPlan plan = {};
+  plan.own = plan_attention(B, max_q, max_kv, q_heads, kv_heads, head_dim, 0, 0);
+  if (groups > 0 && max_group_q > 0) {
+    plan.prefix = plan_attention(groups, max_group_q, max_prefix, q_heads, kv_heads, head_dim, 0, 0);
+    plan.prefix.balanced = false;
+  }
+  return plan;
 }
 
 hipError_t launch_kv_attention_shared(SharedParams p, const SharedPlan& plan, int dtype, hipStream_t stream) {
   take(p.prefix, plan.prefix);
   take(p.own, plan.own);
-  hipError_t err = hipSuccess;
-  if (plan.prefix.row_tiles > 0) err = launch_pass(p.prefix, plan.prefix, dtype, stream);
-  if (err == hipSuccess) err = launch_pass(p.own, plan.own, dtype, stream);
-  if (err != hipSuccess) return err;
-  const dim3 grid((unsigned)((int64_t)p.own.B * p.own.cache.kv_heads * plan.own.tail_rows));
-  const int D = p.own.cache.head_dim;
-  D == 64 ? launch_join<64>(p, grid, stream) : D == 128 ? launch_join<128>(p, grid, stream) : launch_join<256>(p, grid, stream);
+  const Cache& c = p.own.cache;
+  if (plan.prefix.row_tiles > 0) {
+    const unsigned n = (unsigned)plan.prefix.workgroups((int64_t)p.prefix.B * c.kv_heads);
+    const hipError_t err = plan.prefix.tiles ? launch_attention_tiles_prefix(p.prefix, plan.prefix.rows_each, n, dtype, stream)
+                                             : launch_attention_rows<kPrefix>(p.prefix, c, n, plan.prefix.waves, dtype, stream);
+    if (err != hipSuccess) return err;
+  }
+  const int64_t groups = (int64_t)p.own.B * c.kv_heads;
+  const unsigned n = (unsigned)plan.own.workgroups(groups);
+  const hipError_t err = plan.own.tiles ? launch_attention_tiles_own(p, plan.own.rows_each, n, dtype, stream)
+                                        : launch_attention_rows<kOwn>(p, c, n, plan.own.waves, dtype, stream);
+  if (err != hipSuccess || plan.own.splits == 1) return err;
+  const dim3 grid((unsigned)(groups * plan.own.tail_rows));
+  c.head_dim == 64 ? launch_join<64>(p, grid, stream) : c.head_dim == 128 ? launch_join<128>(p, grid, stream) : launch_join<256>(p, grid, stream);
   return hipGetLastError();
 }
 

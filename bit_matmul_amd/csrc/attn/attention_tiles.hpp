@@ -96,13 +96,13 @@ template <int D, int GS, int DT, int NW>
 constexpr int kBiasBytes = NW * 32 * 32 * kBiasSteps<D, GS, DT>;
 
 // A workgroup's rows.
-template <int RW, bool SHARED>
+template <int RW, int PASS>
 struct TileRows {
   Work work;
   Extent ex;
   int r0, rows;
   __device__ __forceinline__ TileRows(const AttentionParams& p, int tid, int workgroup)
-      : work(p, workgroup), ex(extent_in_pass<SHARED>(p, work.b, tid == 0)), r0(work.row_tile * 32 * RW), rows(min(32 * RW, ex.rows - r0)) {}
+      : work(p, workgroup), ex(extent_in_pass<PASS>(p, work.b, tid == 0)), r0(work.row_tile * 32 * RW), rows(min(32 * RW, ex.rows - r0)) {}
 };
 
 __device__ __forceinline__ float larger(float a, float b) {
@@ -121,8 +121,8 @@ struct TileGathered {
 // the first 64 tokens of each tile, the other the rest, and they join at the end.
 // CAREFUL: with units that change and tokens that have their own. Without, the first tile's units have to do for
 // all, and it returns false where they do not.
-template <int D, int GS, int DT, int NW, int RW, bool CAREFUL, bool SHARED>
-__device__ __forceinline__ bool gather_tiles(const AttentionParams& p, const TileRows<RW, SHARED>& mine, int tid, char* lds,
+template <int D, int GS, int DT, int NW, int RW, bool CAREFUL, int PASS>
+__device__ __forceinline__ bool gather_tiles(const AttentionParams& p, const TileRows<RW, PASS>& mine, int tid, char* lds,
                                              TileNotes& notes, TileGathered<D>& out) {
   // A tile is one or two halves of 64 tokens, as LDS allows: with two, waves run freely between
   // barriers for twice as long.
@@ -706,9 +706,9 @@ __device__ __forceinline__ bool gather_tiles(const AttentionParams& p, const Til
   return true;
 }
 
-// SHARED: as in attention_rows_kernel.
-template <int D, int GS, int DT, int NW, int RW, bool SHARED>
-__global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(AttentionParams p) {
+template <int D, int GS, int DT, int NW, int RW, int PASS>
+__global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(typename PassParams<PASS>::Type params) {
+  const AttentionParams& p = params_of(params);
   constexpr bool PAIRED = RW < NW;
   constexpr int ROW = D * 2, DB = D / 32;
   __shared__ __attribute__((aligned(16))) char lds[kTileBytes<D, NW> + kBiasBytes<D, GS, DT, NW>];
@@ -716,14 +716,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
   static_assert(RW * 32 * ROW <= kTileBytes<D, NW> && (!PAIRED || RW * (D / 2 * 256 + 512) <= kTileBytes<D, NW>), "epilogue");
   // The row tiles of a sequence and kv head on one XCD: its codes meet in one L2.
   const int tid = threadIdx.x, workgroup = xcd_remap(blockIdx.x, gridDim.x);
-  const TileRows<RW, SHARED> own(p, tid, workgroup);
+  const TileRows<RW, PASS> own(p, tid, workgroup);
   if (own.rows <= 0) return;
   TileGathered<D> got;
-  if (!gather_tiles<D, GS, DT, NW, RW, false, SHARED>(p, own, tid, lds, notes, got)) {
+  if (!gather_tiles<D, GS, DT, NW, RW, false, PASS>(p, own, tid, lds, notes, got)) {
     __syncthreads();
     const AttentionParams& again = params_again();
     const int same = opaque(tid);
-    gather_tiles<D, GS, DT, NW, RW, true, SHARED>(again, TileRows<RW, SHARED>(again, same, scalar_again(workgroup)), same, lds, notes, got);
+    gather_tiles<D, GS, DT, NW, RW, true, PASS>(again, TileRows<RW, PASS>(again, same, scalar_again(workgroup)), same, lds, notes, got);
   }
   f32x16_t(&o)[DB] = got.o;
   float m = got.m, l = got.l;
@@ -764,13 +764,48 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
     }
   }
   const RowOf mine_row(p, head, opaque(min(wr + c, ex.rows - 1)));
-  const bool live = wr + c < ex.rows && wave < RW;
-  const float out_scale = SHARED || work.splits > 1 ? ldexpf(1.f, o_unit) : (l == 0.f ? 0.f : ldexpf(1.f / l, o_unit));
+  bool live = wr + c < ex.rows && wave < RW;
+  const bool partial = PASS == kPrefix || work.splits > 1;
+  if constexpr (PASS == kOwn) {
+    if (!partial) {
+      const AttentionParams& prefix = params.prefix;
+      const SharedRows shared(prefix, ex, work.b, lane, tid == 0);
+      const int row = min(wr + c, ex.rows - 1);
+      live = live && shared.has(row);
+      if (wave < RW && shared.group >= 0) {
+        // Both halves of a row's lanes go round its parts together.
+        const int parts = live ? shared.parts(prefix, row) : 0;
+        for (int s = 0; s < parts; ++s) {
+          const int64_t at = prefix_row(prefix, s, shared.group, head, (int)shared.first + row);
+          const float2 ml = *reinterpret_cast<const float2*>(prefix.part_ml + 2 * at);
+          if (ml.y == 0.f) continue;  // saw nothing
+          const float top = fmaxf(m, ml.x);
+          const float mine = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top), other = ml.x == top ? 1.f : __builtin_amdgcn_exp2f(ml.x - top);
+          const float own_part = ldexpf(mine, o_unit);
+          o_unit = 0;
+          m = top;
+          l = l * mine + ml.y * other;
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float* from = prefix.part_o + at * D + 32 * d + 2 * e + 2 * h;
+              const float2 a = *reinterpret_cast<const float2*>(from), b2 = *reinterpret_cast<const float2*>(from + 4);
+              o[d][e] = o[d][e] * own_part + a.x * other;
+              o[d][e + 2] = o[d][e + 2] * own_part + a.y * other;
+              o[d][e + 1] = o[d][e + 1] * own_part + b2.x * other;
+              o[d][e + 3] = o[d][e + 3] * own_part + b2.y * other;
+            }
+        }
+      }
+    }
+  }
+  const float out_scale = partial ? ldexpf(1.f, o_unit) : (l == 0.f ? 0.f : ldexpf(1.f / l, o_unit));
   // Dims of a lane's registers: block d, eight dims e / 4, of which (0, 4, 1, 5) for h = 0 and
   // (2, 6, 3, 7) for h = 1, so that registers (0, 2) and (1, 3) are neighbouring dims.
-  if (SHARED || work.splits > 1) {
+  if (partial) {
     if (!live) return;
-    const int64_t at = part_row(p, work.split * p.B + b, head, wr + c);
+    const int64_t at = partial_row<PASS>(p, work, work.split * p.B + b, wr + c);
     if (h == 0) {
       p.part_ml[2 * at] = m;
       p.part_ml[2 * at + 1] = l;
@@ -830,34 +865,37 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(Attent
   }
 }
 
-template <int D, int GS, int NW, int RW, bool SHARED>
-hipError_t launch_tiles(const AttentionParams& p, unsigned workgroups, int dtype, hipStream_t stream) {
+template <int D, int GS, int NW, int RW, int PASS>
+hipError_t launch_tiles(const typename PassParams<PASS>::Type& p, unsigned workgroups, int dtype, hipStream_t stream) {
   const dim3 grid(workgroups);
   if (dtype == 0)
-    hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 0, NW, RW, SHARED>), grid, dim3(64 * NW), 0, stream, p);
+    hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 0, NW, RW, PASS>), grid, dim3(64 * NW), 0, stream, p);
   else
-    hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 1, NW, RW, SHARED>), grid, dim3(64 * NW), 0, stream, p);
+    hipLaunchKernelGGL((attention_tiles_kernel<D, GS, 1, NW, RW, PASS>), grid, dim3(64 * NW), 0, stream, p);
+  static const char* const names[] = {"attention_tiles_kernel<%d, %d, %d, %d, %d>", "attention_tiles_kernel<%d, %d, %d, %d, %d, prefix>",
+                                      "attention_tiles_kernel<%d, %d, %d, %d, %d, own>"};
   launch_log(grid, dim3(64 * NW), (size_t)(NW * 64 * D * 2 + (dtype ? kBiasBytes<D, GS, 1, NW> : 0) + sizeof(TileNotes)),
-             SHARED ? "attention_tiles_kernel<%d, %d, %d, %d, %d, 1>" : "attention_tiles_kernel<%d, %d, %d, %d, %d>", D, GS, dtype, NW, RW);
+             names[PASS], D, GS, dtype, NW, RW);
   return hipGetLastError();
 }
 
-template <int D, int NW, int RW, bool SHARED>
-hipError_t launch_tile_groups(const AttentionParams& p, unsigned workgroups, int dtype, hipStream_t stream) {
-  if (p.cache.group == 32) return launch_tiles<D, 32, NW, RW, SHARED>(p, workgroups, dtype, stream);
-  if (p.cache.group == 64) return launch_tiles<D, 64, NW, RW, SHARED>(p, workgroups, dtype, stream);
-  if constexpr (D >= 128) return launch_tiles<D, 128, NW, RW, SHARED>(p, workgroups, dtype, stream);
+template <int D, int NW, int RW, int PASS>
+hipError_t launch_tile_groups(const typename PassParams<PASS>::Type& p, int group, unsigned workgroups, int dtype, hipStream_t stream) {
+  if (group == 32) return launch_tiles<D, 32, NW, RW, PASS>(p, workgroups, dtype, stream);
+  if (group == 64) return launch_tiles<D, 64, NW, RW, PASS>(p, workgroups, dtype, stream);
+  if constexpr (D >= 128) return launch_tiles<D, 128, NW, RW, PASS>(p, workgroups, dtype, stream);
   return hipErrorInvalidValue;
 }
 
-template <bool SHARED>
-hipError_t launch_tiles_of(const AttentionParams& p, int rows_each, unsigned workgroups, int dtype, hipStream_t stream) {
-  if (p.cache.head_dim == 256) return launch_tile_groups<256, 4, 4, SHARED>(p, workgroups, dtype, stream);
-  if (p.cache.head_dim == 128)
-    return rows_each == 256 ? launch_tile_groups<128, 8, 8, SHARED>(p, workgroups, dtype, stream)
-                            : launch_tile_groups<128, 8, 4, SHARED>(p, workgroups, dtype, stream);
-  return rows_each == 256 ? launch_tile_groups<64, 8, 8, SHARED>(p, workgroups, dtype, stream)
-                          : launch_tile_groups<64, 8, 4, SHARED>(p, workgroups, dtype, stream);
+template <int PASS>
+hipError_t launch_tiles_of(const typename PassParams<PASS>::Type& p, const Cache& c, int rows_each, unsigned workgroups, int dtype,
+                           hipStream_t stream) {
+  if (c.head_dim == 256) return launch_tile_groups<256, 4, 4, PASS>(p, c.group, workgroups, dtype, stream);
+  if (c.head_dim == 128)
+    return rows_each == 256 ? launch_tile_groups<128, 8, 8, PASS>(p, c.group, workgroups, dtype, stream)
+                            : launch_tile_groups<128, 8, 4, PASS>(p, c.group, workgroups, dtype, stream);
+  return rows_each == 256 ? launch_tile_groups<64, 8, 8, PASS>(p, c.group, workgroups, dtype, stream)
+                          : launch_tile_groups<64, 8, 4, PASS>(p, c.group, workgroups, dtype, stream);
 }
 
 }  // namespace

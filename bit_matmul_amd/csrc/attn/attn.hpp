@@ -113,18 +113,33 @@ hipError_t launch_kv_attention(AttentionParams p, const AttentionPlan& plan, int
 // Attention of groups of sequences that share their first tokens: a pass over what they share and a pass over
 // what each has of its own, whose partial results are joined.
 struct SharedParams {
-  AttentionParams prefix, own;
+  AttentionParams own, prefix;  // in this order: a kernel's parameters begin with those of its pass
 };
 struct SharedPlan {
-  AttentionPlan prefix, own;  // all row tiles are partial
+  AttentionPlan own, prefix;
 };
+// A kernel's part in it: none, the pass over the shared tokens, whose results are all partial, or that over the own
+// ones, whose results take in the former's.
+enum Pass { kAlone = 0, kPrefix = 1, kOwn = 2 };
+template <int PASS>
+struct PassParams {
+  typedef AttentionParams Type;
+};
+template <>
+struct PassParams<kOwn> {
+  typedef SharedParams Type;
+};
+__device__ __forceinline__ const AttentionParams& params_of(const AttentionParams& p) { return p; }
+__device__ __forceinline__ const AttentionParams& params_of(const SharedParams& p) { return p.own; }
 SharedPlan plan_attention_shared(int64_t groups, int64_t B, int64_t max_group_q, int64_t max_prefix, int64_t max_q,
                                  int64_t max_kv, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
 hipError_t launch_kv_attention_shared(SharedParams p, const SharedPlan& plan, int dtype, hipStream_t stream);
 
-// The same kernel's passes for many query rows (prefill_shared.hip).
-hipError_t launch_attention_tiles_shared(const AttentionParams& p, int rows_each, unsigned workgroups, int dtype,
+// Its passes for many query rows (prefill_shared.hip).
+hipError_t launch_attention_tiles_prefix(const AttentionParams& p, int rows_each, unsigned workgroups, int dtype,
                                          hipStream_t stream);
+hipError_t launch_attention_tiles_own(const SharedParams& p, int rows_each, unsigned workgroups, int dtype,
+                                      hipStream_t stream);
 
 // The kernel for many query rows (prefill.hip).
 hipError_t launch_attention_tiles(const AttentionParams& p, int rows_each, unsigned workgroups, int dtype,

@@ -23,8 +23,15 @@ bool shared_sizes_ok(int64_t T, int64_t B, int64_t groups, int64_t max_group_q, 
          attention_sizes_ok(T, groups, max_group_q, max_prefix, q_heads, kv_heads, 0, 0);
 }
 
-// Floats of a pass's partial results: outputs, then references and sums.
-int64_t part_rows(const AttentionPlan& plan, int64_t B, int64_t kv_heads) { return (int64_t)plan.splits * B * kv_heads * plan.tail_rows; }
+// Rows of partial results: a first part of each over the shared tokens, the others of those that are split, and
+// the parts of split rows over the own tokens.
+struct PartRows {
+  int64_t prefix, own;
+};
+PartRows part_rows(const SharedPlan& plan, int64_t B, int64_t groups, int64_t max_group_q, int64_t q_heads, int64_t kv_heads) {
+  return {groups * kv_heads * (max_group_q * (q_heads / kv_heads) + (int64_t)std::max(plan.prefix.splits - 1, 0) * plan.prefix.tail_rows),
+          plan.own.splits > 1 ? (int64_t)plan.own.splits * B * kv_heads * plan.own.tail_rows : 0};
+}
 
 }  // namespace
 
@@ -201,8 +208,8 @@ size_t bitmm_kv_attention_shared_workspace_bytes(int64_t T, int64_t B, int64_t g
   if (!shared_sizes_ok(T, B, groups, max_group_q, max_prefix, max_q, max_kv, q_heads, kv_heads) || !head_dim_ok(head_dim)) return 0;
   if (T == 0 || B == 0 || max_q == 0) return 0;
   const SharedPlan plan = plan_attention_shared(groups, B, max_group_q, max_prefix, max_q, max_kv, q_heads, kv_heads, head_dim);
-  const size_t rows = (size_t)(part_rows(plan.prefix, groups, kv_heads) + part_rows(plan.own, B, kv_heads));
-  return (rows * (size_t)(head_dim + 2) * 4 + 255) / 256 * 256;
+  const PartRows rows = part_rows(plan, B, groups, max_group_q, q_heads, kv_heads);
+  return ((size_t)(rows.prefix + rows.own) * (size_t)(head_dim + 2) * 4 + 255) / 256 * 256;
 }
 
 bitmm_status bitmm_kv_attention_shared(const void* q, int64_t q_stride, const bitmm_kv_cache* cache,
@@ -238,11 +245,11 @@ bitmm_status bitmm_kv_attention_shared(const void* q, int64_t q_stride, const bi
     // A launch's threads are counted in 32 bits.
     const int64_t limit = ((int64_t)1 << 32) / 512 - 1;
     if (plan.prefix.workgroups(groups * kv_heads) > limit || plan.own.workgroups(B * kv_heads) > limit ||
-        groups * kv_heads * plan.prefix.tail_rows > INT32_MAX || B * kv_heads * plan.own.tail_rows > limit)
+        groups * kv_heads * max_group_q * (q_heads / kv_heads) > INT32_MAX || B * kv_heads * plan.own.tail_rows > limit)
       return BITMM_ERR_UNSUPPORTED;
     const size_t need = bitmm_kv_attention_shared_workspace_bytes(T, B, groups, max_group_q, max_prefix, max_q, max_kv, q_heads,
                                                                   kv_heads, D);
-    if (!workspace || workspace_bytes < need) return BITMM_ERR_WORKSPACE;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return BITMM_ERR_WORKSPACE;
     if ((st = device_check()) != BITMM_OK) return st;
     AttentionParams p = {};
     p.q = static_cast<const uint16_t*>(q);
@@ -273,11 +280,11 @@ bitmm_status bitmm_kv_attention_shared(const void* q, int64_t q_stride, const bi
     both.prefix.max_kv = (int)max_prefix;
     both.prefix.cu_groups = cu_groups;
     both.prefix.sequences = (int)B;
-    const int64_t prefix_rows = part_rows(plan.prefix, groups, kv_heads), own_rows = part_rows(plan.own, B, kv_heads);
+    const PartRows rows = part_rows(plan, B, groups, max_group_q, q_heads, kv_heads);
     both.prefix.part_o = static_cast<float*>(workspace);
-    both.own.part_o = both.prefix.part_o + prefix_rows * D;
-    both.prefix.part_ml = both.own.part_o + own_rows * D;
-    both.own.part_ml = both.prefix.part_ml + 2 * prefix_rows;
+    both.own.part_o = both.prefix.part_o + rows.prefix * D;
+    both.prefix.part_ml = both.own.part_o + rows.own * D;
+    both.own.part_ml = both.prefix.part_ml + 2 * rows.prefix;
     return launched(launch_kv_attention_shared(both, plan, (int)dtype, static_cast<hipStream_t>(stream)));
   } catch (...) {
     return BITMM_ERR_LAUNCH;

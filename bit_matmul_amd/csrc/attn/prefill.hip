@@ -6,7 +6,7 @@ namespace attn {
 
 hipError_t launch_attention_tiles(const AttentionParams& p, int rows_each, unsigned workgroups, int dtype,
                                   hipStream_t stream) {
-  return launch_tiles_of<false>(p, rows_each, workgroups, dtype, stream);
+  return launch_tiles_of<kAlone>(p, p.cache, rows_each, workgroups, dtype, stream);
 }
 
 }  // namespace attn

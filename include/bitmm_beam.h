@@ -60,8 +60,8 @@ bitmm_status bitmm_qk_norm_rope_append(const void* q, int64_t q_stride, const vo
  * and own tokens of a sequence; what passes them is cut and sets *status, and rows past them are not written.
  * `workspace`: bitmm_kv_attention_shared_workspace_bytes(...) bytes, 16-byte aligned, no initialisation
  * needed; two calls that share it must be ordered on one stream.
- * Limits (else BITMM_ERR_UNSUPPORTED): q_heads / kv_heads <= 64; B and groups <= 65535; B times kv_heads times the
- * query rows of a sequence's kv head < 2^23.
+ * Limits (else BITMM_ERR_UNSUPPORTED): q_heads / kv_heads <= 64; B and groups <= 65535; launches of
+ * less than 2^23 workgroups.
  */
 size_t bitmm_kv_attention_shared_workspace_bytes(int64_t T, int64_t B, int64_t groups, int64_t max_group_q,
                                                  int64_t max_prefix, int64_t max_q, int64_t max_kv,
