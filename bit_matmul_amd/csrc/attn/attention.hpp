@@ -210,6 +210,12 @@ __device__ __forceinline__ const AttentionParams& params_again() {
   asm volatile("" : "+s"(p));
   return *(const AttentionParams*)p;
 }
+__device__ __forceinline__ const SharedParams& shared_params_again() {
+  typedef __attribute__((address_space(4))) SharedParams Params;
+  const Params* p = (const Params*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const SharedParams*)p;
+}
 __device__ __forceinline__ int scalar_again(unsigned v) { return __builtin_amdgcn_readfirstlane(opaque((int)v)); }
 
 // A workgroup's work: a sequence and kv head, one of its row tiles, and which part of how many of
@@ -251,28 +257,42 @@ __device__ __forceinline__ int64_t partial_row(const AttentionParams& p, const W
   return PASS == kPrefix ? prefix_row(p, work.split, work.b, work.head, r) : part_row(p, part, work.head, r);
 }
 
-// The results over shared tokens that belong to a sequence's rows: those of its group, the first that has it.
-struct SharedRows {  // made by a whole wave
+// Where no pass over the groups reports what is wrong with them, each workgroup looks at some, by its last wave.
+__device__ __forceinline__ void report_groups(const AttentionParams& prefix, int tid) {
+  if (tid != (int)blockDim.x - 64 || !prefix.status) return;
+  for (int g = blockIdx.x; g < prefix.B; g += gridDim.x) extent_of_group(prefix, g, true);
+}
+
+// The group of a sequence, the first that has it, and where its rows lie among the group's. Made by a whole wave,
+// in two parts, so that loads of the second, which depend on the first's, need not be waited for in between.
+struct SharedRows {
   int group = -1;
-  int64_t first = 0;  // the group's row that is the sequence's first
-  int rows = 0;       // of the group
+  int from = 0, to = 0;  // the group's first row of q, and the one past its last
   __device__ __forceinline__ SharedRows() {}
-  __device__ __forceinline__ SharedRows(const AttentionParams& prefix, const Extent& ex, int b, int lane, bool report) {
+  __device__ __forceinline__ SharedRows(const AttentionParams& prefix, int b, int lane) {
     for (int g0 = 0; g0 < prefix.B; g0 += 64) {
       const int g = g0 + lane;
-      const uint64_t found = __ballot(g < prefix.B && prefix.cu_groups[g] <= b && b < prefix.cu_groups[g + 1]);
+      const int lo = g < prefix.B ? prefix.cu_groups[g] : INT32_MAX, hi = g < prefix.B ? prefix.cu_groups[g + 1] : 0;
+      const uint64_t found = __ballot(lo <= b && b < hi);
       if (!found) continue;
-      group = g0 + __builtin_ctzll(found);
-      const Extent e = extent_of_group(prefix, group, report);
-      first = (int64_t)(ex.q0 - e.q0) * prefix.share;
-      rows = e.rows;
+      const int at = __builtin_ctzll(found);
+      group = g0 + at;
+      // b lies between them, so the one is not past the last sequence, nor the other before the first
+      from = prefix.cu_q[max(__builtin_amdgcn_readlane(lo, at), 0)];
+      to = prefix.cu_q[min(__builtin_amdgcn_readlane(hi, at), prefix.sequences)];
       return;
     }
   }
-  // Rows past the bound of a group's queries have no result over the shared tokens: they are not written.
-  __device__ __forceinline__ bool has(int r) const { return group < 0 || (first + r >= 0 && first + r < rows); }
-  __device__ __forceinline__ int parts(const AttentionParams& prefix, int r) const {
-    return group < 0 ? 0 : first + r < prefix.tail_rows ? prefix.splits : 1;
+  // The group's row of a kv head that is row r of a sequence whose queries begin at q0.
+  __device__ __forceinline__ int64_t row(const AttentionParams& prefix, int q0, int r) const {
+    return (int64_t)(q0 - min(max(from, 0), prefix.T)) * prefix.share + r;
+  }
+  // How many parts that row has. Rows past the bound of a group's queries have none (-1): they are not written.
+  __device__ __forceinline__ int parts(const AttentionParams& prefix, int64_t row) const {
+    if (group < 0) return 0;
+    const int q0 = min(max(from, 0), prefix.T), q1 = min(max(to, q0), prefix.T);
+    if (row < 0 || row >= (int64_t)min(q1 - q0, prefix.max_q) * prefix.share) return -1;
+    return row < prefix.tail_rows ? prefix.splits : 1;
   }
 };
 

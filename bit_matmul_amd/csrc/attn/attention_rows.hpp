@@ -180,6 +180,22 @@ struct RowsLds {
   float ml[WAVES][2][16];
 };
 
+// One result on top of another's: outputs of units 2^unit, which may differ, the sum of lane group g alone where the
+// other's is whole.
+template <int J, typename F>
+__device__ __forceinline__ void take_in(f32x4_t (&o)[J], float& m, float& l, int& unit, float m2, float l2, F outputs) {
+  const float top = fmaxf(m, m2);
+  const float mine = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top), other = m2 == top ? 1.f : __builtin_amdgcn_exp2f(m2 - top);
+  const float ours = ldexpf(mine, unit);
+  unit = 0;  // theirs may be far from it
+  m = top;
+  l = l * mine + l2 * other;
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[j][e] = o[j][e] * ours + outputs(j, e) * other;
+}
+
 // A workgroup's rows: those of a row tile, and which part of how many of the tokens; `part` is its place in the
 // partial results.
 struct Rows {
@@ -209,6 +225,19 @@ __device__ __forceinline__ Rows rows_of(const AttentionParams& p, int tid, int w
   return {work, ex, part, r0, min(kRows, ex.rows - r0)};
 }
 
+// The same rows over the tokens that their group shares, all of which they see.
+__device__ __forceinline__ Rows shared_rows_of(const AttentionParams& prefix, const Rows& own, int group) {
+  Rows rows = own;
+  rows.work.b = group;
+  rows.work.split = 0;
+  rows.work.splits = 1;
+  const int64_t room = prefix.pages_per_seq << prefix.cache.page_shift;
+  rows.ex.kv = min(max(prefix.kv_lens[group], 0), (int)(room < prefix.max_kv ? room : prefix.max_kv));
+  rows.ex.first = rows.ex.kv - 1;
+  rows.ex.step = 0;
+  return rows;
+}
+
 // What a wave gathers: outputs in units of 2^unit, the exponents' reference and the sum.
 template <int D>
 struct Gathered {
@@ -218,10 +247,14 @@ struct Gathered {
 };
 
 // A wave's share of the tokens. CAREFUL: with units that change and tokens that have their own. Without, those of
-// the wave's first step have to do for all its tokens, and it returns false where they do not.
-template <int D, int GS, int DT, int WAVES, bool CAREFUL>
+// the wave's first step have to do for all its tokens, and it returns false where they do not. SHARE: the wave takes
+// turns with those that its Turn says, not with all of the workgroup.
+struct Turn {
+  int index, count;
+};
+template <int D, int GS, int DT, int WAVES, bool CAREFUL, bool SHARE = false>
 __device__ __forceinline__ bool gather_rows(const AttentionParams& p, const Rows& mine, int tid, RowsLds<D, GS, WAVES>& mem,
-                                            Gathered<D>& out) {
+                                            Gathered<D>& out, Turn turn = {}) {
   constexpr int NG = D / GS;                         // groups of a head
   constexpr int J = D / 16;                          // output tiles
   constexpr int KW = D / 32, WG = GS / 32;           // a lane's key words, and those of a group
@@ -253,7 +286,17 @@ __device__ __forceinline__ bool gather_rows(const AttentionParams& p, const Rows
   bool outside = false;
   auto seen = [&](int from, int to) { return any_sees(from, to, lo_pos, hi_pos, p.window, p.sinks); };
   const int head_row = head << p.cache.page_shift;
-  const int first = i0 + wave;
+  const int first = i0 + (SHARE ? turn.index : wave), each = SHARE ? turn.count : WAVES;
+  if constexpr (SHARE) {
+    if (first >= i1) {  // nothing to do, nor to prepare for it
+#pragma unroll
+      for (int j = 0; j < J; ++j) out.o[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      out.m = neg_inf();
+      out.l = 0.f;
+      out.unit = 0;
+      return true;
+    }
+  }
   auto copy = [&](int stage) {
     char* to = ring + stage * 2 * SIDE;
     copy_codes<D>(p.cache.k_codes, place, lane, to);
@@ -264,7 +307,7 @@ __device__ __forceinline__ bool gather_rows(const AttentionParams& p, const Rows
   if (first < i1) {
     pages = step_pages(p, table, ex.kv, steps.base(first));
     place = step_place(p.cache, head_row, ex.kv, steps.base(first), pages, seen, outside);
-    if (first + WAVES < i1) pages = step_pages(p, table, ex.kv, steps.base(first + WAVES));
+    if (first + each < i1) pages = step_pages(p, table, ex.kv, steps.base(first + each));
     copy(0);
   }
 
@@ -336,7 +379,7 @@ __device__ __forceinline__ bool gather_rows(const AttentionParams& p, const Rows
   // Steps past it and up to lo_pos are visible to every row.
   const int window_edge = p.window > 0 ? hi_pos - p.window : -1;
   int stage = 0;
-  for (int i = first; i < i1; i += WAVES) {
+  for (int i = first; i < i1; i += each) {
     const int base = steps.base(i);
     const bool ok0 = place.ok[0], ok1 = place.ok[1];
     const char* kc = ring + stage * 2 * SIDE;
@@ -421,9 +464,9 @@ __device__ __forceinline__ bool gather_rows(const AttentionParams& p, const Rows
       }
     }
     __builtin_amdgcn_wave_barrier();
-    if (i + WAVES < i1) {
-      place = step_place(p.cache, head_row, ex.kv, steps.base(i + WAVES), pages, seen, outside);
-      if (i + 2 * WAVES < i1) pages = step_pages(p, table, ex.kv, steps.base(i + 2 * WAVES));
+    if (i + each < i1) {
+      place = step_place(p.cache, head_row, ex.kv, steps.base(i + each), pages, seen, outside);
+      if (i + 2 * each < i1) pages = step_pages(p, table, ex.kv, steps.base(i + 2 * each));
       copy(stage);
     }
 
@@ -599,9 +642,36 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   constexpr int J = D / 16;
   __shared__ RowsLds<D, GS, WAVES> mem;
   const Rows own = rows_of<PASS>(p, threadIdx.x, blockIdx.x);
+  if constexpr (PASS == kBoth) report_groups(params.prefix, threadIdx.x);
   if (own.rows <= 0) return;
+  [[maybe_unused]] SharedRows shared;
+  if constexpr (PASS == kOwn || PASS == kBoth) shared = SharedRows(params.prefix, own.work.b, threadIdx.x & 63);
   Gathered<D> got;
-  if (!gather_rows<D, GS, DT, WAVES, false>(p, own, threadIdx.x, mem, got)) {
+  if constexpr (PASS == kBoth) {
+    // The first waves take the shared tokens, the last ones the sequence's own, as many as these are a part of all.
+    Rows mine = own;
+    const SharedParams& all_params = shared_params_again();  // in memory: one of its two is taken by the wave
+    const AttentionParams* tokens = &all_params.own;
+    Turn turn = {__builtin_amdgcn_readfirstlane(threadIdx.x >> 6), WAVES};
+    if (shared.group >= 0) {
+      const Rows before = shared_rows_of(params.prefix, own, shared.group);
+      const int own_steps = (position(own.ex, (own.r0 + own.rows - 1) / p.share) + kStep) / kStep;
+      const int shared_steps = (before.ex.kv + kStep - 1) / kStep, all = max(own_steps + shared_steps, 1);
+      const int last = max(min((WAVES * own_steps + all / 2) / all, shared_steps > 0 ? WAVES - 1 : WAVES), own_steps > 0 ? 1 : 0);
+      const bool late = turn.index >= WAVES - last;
+      turn = late ? Turn{turn.index - (WAVES - last), last} : Turn{turn.index, WAVES - last};
+      if (!late) {
+        mine = before;
+        tokens = &all_params.prefix;
+      }
+    }
+    if (!gather_rows<D, GS, DT, WAVES, false, true>(*tokens, mine, threadIdx.x, mem, got, turn)) {
+      const bool late = tokens == &all_params.own;
+      const SharedParams& again = shared_params_again();
+      const int same = opaque((int)threadIdx.x);
+      gather_rows<D, GS, DT, WAVES, true, true>(late ? again.own : again.prefix, mine, same, mem, got, turn);
+    }
+  } else if (!gather_rows<D, GS, DT, WAVES, false>(p, own, threadIdx.x, mem, got)) {
     const AttentionParams& again = params_again();
     const int same = opaque((int)threadIdx.x);
     gather_rows<D, GS, DT, WAVES, true>(again, rows_of<PASS>(again, same, scalar_again(blockIdx.x)), same, mem, got);
@@ -613,6 +683,31 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
   const Work work = own.work;
   const Extent ex = own.ex;
   const int head = work.head, r0 = own.r0;
+
+  auto partial = [&] { return PASS == kPrefix || (p.splits > 1 && (p.balanced || work.splits > 1)); };
+  // Of the results over the shared tokens each wave takes in every WAVES-th part: their loads overlap, and the join
+  // below is one for all (the parts one after the other behind it: 64 samples, 16 parts 23 us against 20).
+  [[maybe_unused]] int parts = 0;
+  if constexpr (PASS == kBoth) parts = shared.parts(params.prefix, shared.row(params.prefix, ex.q0, min(r0 + n, ex.rows - 1)));
+  if constexpr (PASS == kOwn) {
+    if (!partial()) {
+      const AttentionParams& prefix = params.prefix;
+      const int64_t row = shared.row(prefix, ex.q0, min(r0 + n, ex.rows - 1));
+      parts = shared.parts(prefix, row);
+      for (int s = wave; __any(s < parts); s += WAVES) {
+        if (s >= parts) continue;
+        const int64_t at = prefix_row(prefix, s, shared.group, head, (int)row);
+        const float2 ml = *reinterpret_cast<const float2*>(prefix.part_ml + 2 * at);
+        const float* from = prefix.part_o + at * D + 4 * g * J;  // dim (4 g + e) J + j
+        f32x4_t theirs[J];
+#pragma unroll
+        for (int i = 0; i < J; ++i) theirs[i] = *reinterpret_cast<const f32x4_t*>(from + 4 * i);
+        if (ml.y == 0.f) continue;  // saw nothing
+        // lanes of the other g hold zeros of the row's sum, which is added up below
+        take_in(o, m, l, got.unit, ml.x, g == 0 ? ml.y : 0.f, [&](int j, int e) { return theirs[(e * J + j) / 4][j % 4]; });
+      }
+    }
+  }
 
   // The waves' results joined: each brings its own to the common maximum, and wave w stores
   // every WAVES / 4-th part of dims (4 g + w % 4) D/16 .. of its lanes' rows.
@@ -638,10 +733,6 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
 #pragma unroll
     for (int e = 0; e < 4; ++e) o_lds[wave][4 * j + e][lane] = o[j][e] * mine;
   __syncthreads();
-  auto partial = [&] { return PASS == kPrefix || (p.splits > 1 && (p.balanced || work.splits > 1)); };
-  SharedRows shared;
-  if constexpr (PASS == kOwn)
-    if (!partial()) shared = SharedRows(params.prefix, ex, work.b, lane, threadIdx.x == 0);  // with all lanes
   if (r0 + n >= ex.rows) return;
   constexpr int PARTS = WAVES / 4 < J / 4 ? WAVES / 4 : J / 4;  // of a lane's J dims, four or more each
   constexpr int JP = J / PARTS;
@@ -668,25 +759,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
       *reinterpret_cast<f32x4_t*>(p.part_o + at * D + dim0 + j) = f32x4_t{y[j], y[j + 1], y[j + 2], y[j + 3]};
     return;
   }
-  if constexpr (PASS == kOwn) {
-    const AttentionParams& prefix = params.prefix;
-    if (!shared.has(row)) return;
-    const int parts = shared.parts(prefix, row);
-#pragma unroll 2
-    for (int s = 0; s < parts; ++s) {
-      const int64_t at = prefix_row(prefix, s, shared.group, head, (int)shared.first + row);
-      const float2 ml = *reinterpret_cast<const float2*>(prefix.part_ml + 2 * at);
-      f32x4_t o4[JP / 4];
-#pragma unroll
-      for (int j = 0; j < JP / 4; ++j) o4[j] = *reinterpret_cast<const f32x4_t*>(prefix.part_o + at * D + dim0 + 4 * j);
-      if (ml.y == 0.f) continue;  // saw nothing
-      const float top = fmaxf(mt, ml.x);
-      const float mine = mt == top ? 1.f : __builtin_amdgcn_exp2f(mt - top), other = ml.x == top ? 1.f : __builtin_amdgcn_exp2f(ml.x - top);
-      mt = top;
-      lt = lt * mine + ml.y * other;
-#pragma unroll
-      for (int j = 0; j < JP; ++j) y[j] = y[j] * mine + o4[j / 4][j % 4] * other;
-    }
+  if ((PASS == kOwn || PASS == kBoth) && parts < 0) {  // past the bound of its group's queries
+    if (p.status) *p.status = 1;
+    return;
   }
   const RowOf out_row(p, head, row);
   const float inv = lt == 0.f ? 0.f : 1.f / lt;
@@ -704,13 +779,14 @@ hipError_t launch_rows(const typename PassParams<PASS>::Type& p, unsigned workgr
   else
     hipLaunchKernelGGL((attention_rows_kernel<D, GS, 1, WAVES, PASS>), grid, block, 0, stream, p);
   static const char* const names[] = {"attention_rows_kernel<%d, %d, %d, %d>", "attention_rows_kernel<%d, %d, %d, %d, prefix>",
-                                      "attention_rows_kernel<%d, %d, %d, %d, own>"};
+                                      "attention_rows_kernel<%d, %d, %d, %d, own>", "attention_rows_kernel<%d, %d, %d, %d, both>"};
   launch_log(grid, block, sizeof(RowsLds<D, GS, WAVES>), names[PASS], D, GS, dtype, WAVES);
   return hipGetLastError();
 }
 
 template <int D, int GS, int PASS>
 hipError_t launch_waves(const typename PassParams<PASS>::Type& p, unsigned workgroups, int waves, int dtype, hipStream_t stream) {
+  if constexpr (PASS == kBoth) return launch_rows<D, GS, 8, PASS>(p, workgroups, dtype, stream);
   return waves == 4 ? launch_rows<D, GS, 4, PASS>(p, workgroups, dtype, stream)
                     : launch_rows<D, GS, 8, PASS>(p, workgroups, dtype, stream);
 }

@@ -38,11 +38,15 @@ __global__ __launch_bounds__(256) void attention_join_shared_kernel(SharedParams
   }
   if (r >= ex.rows) return;
   const int64_t row = part_row(p, first, head, r), all = part_row(p, step, 0, 0);
-  const SharedRows shared(prefix, ex, b, lane, threadIdx.x == 0);
-  if (!shared.has(r)) return;
-  const int shared_parts = shared.parts(prefix, r);
+  const SharedRows shared(prefix, b, lane);
+  const int64_t shared_row = shared.row(prefix, ex.q0, r);
+  const int shared_parts = shared.parts(prefix, shared_row);
+  if (shared_parts < 0) {  // past the bound of its group's queries
+    if (p.status && threadIdx.x == 0) *p.status = 1;
+    return;
+  }
   // A part's place among those of its pass.
-  auto at = [&](int s) { return s < parts ? s * all + row : prefix_row(prefix, s - parts, shared.group, head, (int)shared.first + r); };
+  auto at = [&](int s) { return s < parts ? s * all + row : prefix_row(prefix, s - parts, shared.group, head, (int)shared_row); };
   const int count = parts + shared_parts;
   float mt = neg_inf();
   for (int s = lane; s < count; s += 64) mt = fmaxf(mt, (s < parts ? p : prefix).part_ml[2 * at(s)]);
@@ -99,9 +103,31 @@ SharedPlan plan_attention_shared(int64_t groups, int64_t B, int64_t max_group_q,
                                  int64_t max_kv, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
   SharedPlan plan = {};
   plan.own = plan_attention(B, max_q, max_kv, q_heads, kv_heads, head_dim, 0, 0);
-  if (groups > 0 && max_group_q > 0) {
+  if (groups == 0 || max_group_q == 0) return plan;
+  // Where all sequences' workgroups run at once, two a CU, and tokens are few, each goes over the shared ones by itself:
+  // one launch, one chain of latencies. In us, this against two launches, 40 heads over 8 of 128 dims: four beams after 573
+  // tokens 13.5 and 16.1, after 1200 17.4 and 18.5, after 1600 20.8 and 19.8; 32 beams after 600 12.9 and 20.0; 16 groups
+  // of four after 600 19.4 and 25.0, after 1200 26.8 and 29.4, after 1600 32.5 and 32.2; 20 groups after 600 26.8 and
+  // 25.8. 16 heads over 4 of 256 dims, one group after 1200 25.2 and 23.2.
+  const int64_t row_tiles = (max_q * (q_heads / kv_heads) + kRows - 1) / kRows;
+  plan.both = B * kv_heads * row_tiles <= 512 && max_prefix <= (head_dim == 256 ? 1024 : 1280) && max_kv <= 1024;
+  if (plan.both) {
+    plan.own = {};
+    plan.own.row_tiles = (int)row_tiles;
+    plan.own.splits = 1;
+  } else {
     plan.prefix = plan_attention(groups, max_group_q, max_prefix, q_heads, kv_heads, head_dim, 0, 0);
     plan.prefix.balanced = false;
+    if (!plan.prefix.tiles) {
+      // Parts cost no launch here, and are joined by as many waves: four waves and two steps each, until the
+      // workgroups fill the chip (four beams after 573 tokens: 18.4 us unsplit, 16 in eight parts).
+      AttentionPlan& few = plan.prefix;
+      few.waves = 4;
+      const int64_t fill = (head_dim == 256 ? 2 : 4) * 256, tiles = groups * kv_heads * few.row_tiles;
+      few.splits = (int)std::max<int64_t>(1, std::min<int64_t>({fill / tiles, (max_prefix + 63) / 64, 128}));
+      few.tail_tiles = few.splits > 1 ? few.row_tiles : 0;
+      few.tail_rows = few.splits > 1 ? (int)(max_group_q * (q_heads / kv_heads)) : 0;
+    }
   }
   return plan;
 }
@@ -110,6 +136,8 @@ hipError_t launch_kv_attention_shared(SharedParams p, const SharedPlan& plan, in
   take(p.prefix, plan.prefix);
   take(p.own, plan.own);
   const Cache& c = p.own.cache;
+  if (plan.both)
+    return launch_attention_rows<kBoth>(p, c, (unsigned)((int64_t)p.own.B * c.kv_heads * p.own.row_tiles), 8, dtype, stream);
   if (plan.prefix.row_tiles > 0) {
     const unsigned n = (unsigned)plan.prefix.workgroups((int64_t)p.prefix.B * c.kv_heads);
     const hipError_t err = plan.prefix.tiles ? launch_attention_tiles_prefix(p.prefix, plan.prefix.rows_each, n, dtype, stream)

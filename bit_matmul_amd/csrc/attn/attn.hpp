@@ -117,16 +117,21 @@ struct SharedParams {
 };
 struct SharedPlan {
   AttentionPlan own, prefix;
+  bool both;  // in one launch, a workgroup for all tokens that a row tile sees
 };
-// A kernel's part in it: none, the pass over the shared tokens, whose results are all partial, or that over the own
-// ones, whose results take in the former's.
-enum Pass { kAlone = 0, kPrefix = 1, kOwn = 2 };
+// A kernel's part in it: none, the pass over the shared tokens, whose results are all partial, that over the own
+// ones, whose results take in the former's, or both in one, each sequence by itself.
+enum Pass { kAlone = 0, kPrefix = 1, kOwn = 2, kBoth = 3 };
 template <int PASS>
 struct PassParams {
   typedef AttentionParams Type;
 };
 template <>
 struct PassParams<kOwn> {
+  typedef SharedParams Type;
+};
+template <>
+struct PassParams<kBoth> {
   typedef SharedParams Type;
 };
 __device__ __forceinline__ const AttentionParams& params_of(const AttentionParams& p) { return p; }

@@ -1,6 +1,7 @@
 """Attention over shared and own tokens on the GPU, against attention over both in a row in 64 bits."""
 
 import math
+import re
 
 import pytest
 import torch
@@ -24,6 +25,8 @@ def _gpu():
 class Groups(U.Sequences):
     """Groups of sequences. groups: (shared tokens, [(queries, own tokens), ...]) of each; shared tokens of None:
     sequences of no group."""
+
+    wider = 0   # of the bound of the own tokens, more than there are
 
     def __init__(self, groups, *, q_heads, kv_heads, head_dim, group, page, dtype, seed=0, spare=2, counted=False):
         g = torch.Generator().manual_seed(seed)
@@ -99,7 +102,7 @@ class Groups(U.Sequences):
     def bounds(self):
         of_group = [sum(q for (q, _), p in zip(self.own, self.prefix_of) if p == g) for g in range(len(self.shared))]
         return dict(max_group_q=max(of_group + [0]), max_prefix=max(self.shared + [0]),
-                    max_q=max(q for q, _ in self.own), max_kv=max(n for _, n in self.own))
+                    max_q=max(q for q, _ in self.own), max_kv=max(n for _, n in self.own) + self.wider)
 
     def run(self, cache=None, q=None, **kw):
         """(out, lse, status word)"""
@@ -112,9 +115,9 @@ class Groups(U.Sequences):
         return out.cpu().double(), lse.cpu().double(), status.item()
 
 
-def check(s, out_dtype, scale=None):
+def check(s, out_dtype, scale=None, **kw):
     scale = 1 / math.sqrt(s.head_dim) if scale is None else scale
-    out, lse, status = s.run(out_dtype=out_dtype, scale=scale)
+    out, lse, status = s.run(out_dtype=out_dtype, scale=scale, **kw)
     want, want_lse, tol, tol_lse = s.reference(out_dtype, scale)
     assert status == 0
     assert ((out - want).abs() <= tol).all()
@@ -151,10 +154,34 @@ CASES = {  # groups, query heads, kv heads, dims, group, page, type, type of the
 }
 
 
+# Bounds decide which kernels run: small cases go through one launch as they are, through a pass over the shared
+# tokens and one over the own ones with a wide bound of the former, and with a wide bound of the latter through a join.
+WIDE = {"as they are": {}, "wide": dict(max_prefix=100000), "wide own": dict(max_prefix=3000, max_kv=50000)}
+
+
+@pytest.mark.parametrize("bounds", WIDE)
 @pytest.mark.parametrize("name", CASES)
-def test_against_64_bits(name):
+def test_against_64_bits(name, bounds):
     groups, hq, hk, D, group, page, dtype, out_dtype = CASES[name]
-    check(Groups(groups, q_heads=hq, kv_heads=hk, head_dim=D, group=group, page=page, dtype=dtype, seed=len(name)), out_dtype)
+    s = Groups(groups, q_heads=hq, kv_heads=hk, head_dim=D, group=group, page=page, dtype=dtype, seed=len(name))
+    check(s, out_dtype, **{k: max(v, s.bounds()[k]) for k, v in WIDE[bounds].items()})
+
+
+def test_what_runs():
+    """Each of the forms above is taken: by the names of the kernels of a call."""
+    kw = dict(q_heads=40, kv_heads=8, head_dim=128, group=64, page=64, dtype=BF)
+    small, many = Groups([(573, beams(4, 1, 29))], **kw), Groups([(2000, beams(64, 1, 29)), (10, [(70, 70)])], **kw)
+
+    def names(s, **bounds):
+        s.run(**bounds)
+        return [re.sub(r"<([^>]*)>.*", lambda m: " " + m[1].split(", ")[-1], line) for line in bm.bitmm_last_launches()]
+
+    assert names(small) == ["attention_rows_kernel both"]
+    assert names(small, max_prefix=1281) == ["attention_rows_kernel prefix", "attention_rows_kernel own"]
+    assert names(small, max_kv=20000) == ["attention_rows_kernel prefix", "attention_rows_kernel own", "attention_join_shared_kernel 128"]
+    assert names(many) == ["attention_tiles_kernel prefix", "attention_tiles_kernel own"]
+    chunk = Groups([(600, [(400, 400)])], **kw)
+    assert names(chunk, max_kv=20000)[1:] == ["attention_tiles_kernel own", "attention_join_shared_kernel 128"]
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
@@ -193,10 +220,12 @@ def test_every_token_counts_once(name):
             assert ((lse[at, head] - seen.double().log()).abs() <= 2.0 ** -18).all()
 
 
-def test_queries_before_their_own_tokens():
+@pytest.mark.parametrize("wide", [0, 2000])
+def test_queries_before_their_own_tokens(wide):
     """They see all that is shared, like a query with no tokens of its own."""
     kw = dict(q_heads=4, kv_heads=2, head_dim=64, group=32, page=16, dtype=BF, seed=3)
     s = Groups([(50, [(3, 1)])], **kw)
+    s.wider = wide
     out, lse, status = s.run(out_dtype=F32)
     alone = Groups([(50, [(1, 0), (1, 0), (1, 1)])], **kw)
     alone.sides, alone.q, alone.prefix_table = s.sides, s.q, s.prefix_table
@@ -223,18 +252,22 @@ def test_strides_and_rows_of_no_sequence():
     assert (whole[T:] == 5).all() and (whole[:, 0] == 5).all() and (whole[:, 7:] == 5).all() and (lse[T:] == 9).all()
 
 
+@pytest.mark.parametrize("wide", [0, 2000])
 @pytest.mark.parametrize("rows", [1, 40])
-def test_out_of_range(rows):
-    """What passes the bounds is cut and reported; pages outside the cache are seen by nobody."""
+def test_out_of_range(rows, wide):
+    """What passes the bounds is cut and reported; pages outside the cache are seen by nobody. wide: more of a bound of
+    the own tokens, for the kernels of two passes."""
     kw = dict(q_heads=8, kv_heads=2, head_dim=64, group=32, page=16, dtype=BF)
     groups = [(200, beams(rows, 1, 20)), (90, beams(rows, 1, 20))]
     s = Groups(groups, seed=5, **kw)
+    s.wider = wide
     full, _, ok = s.run()
     assert ok == 0
     n = rows * 1
     # a prefix longer than the bound: as if it were that long
     out, _, status = s.run(max_prefix=90)
     short = Groups([(90, groups[0][1]), groups[1]], seed=5, **kw)
+    short.wider = wide
     short.sides, short.q, short.page_table = s.sides, s.q, s.page_table
     short.prefix_table = s.prefix_table[:, :6].contiguous()
     assert status == 1 and torch.equal(out, short.run()[0])
@@ -275,10 +308,12 @@ def test_out_of_range(rows):
             assert near.abs().max() <= 2.0 ** -7 * full.abs().max()
 
 
+@pytest.mark.parametrize("wide", [0, 2000])
 @pytest.mark.parametrize("rows", [2, 40])
-def test_what_is_not_finite(rows):
+def test_what_is_not_finite(rows, wide):
     """A token whose scale is not finite makes NaN of the rows that see it, and slots that hold no token may hold anything."""
     s = Groups([(70, beams(rows, 1, 20)), (40, beams(rows, 1, 9))], q_heads=8, kv_heads=2, head_dim=128, group=64, page=16, dtype=BF, seed=6)
+    s.wider = wide
     clean, _, _ = s.run()
     page = s.prefix_table[0, 4].item()          # slots 6 and on of this page hold no token
     s.sides[0][1][page, :, 6:] = math.nan
