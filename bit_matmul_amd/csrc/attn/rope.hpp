@@ -6,7 +6,8 @@
 namespace bitmm {
 namespace attn {
 
-template <int D, bool INTERLEAVED, int DT>
+// AHEAD: how many turns ahead its heads are loaded.
+template <int D, bool INTERLEAVED, int DT, int AHEAD = 1>
 __device__ __forceinline__ void norm_rope_heads(const RopeParams& p, int64_t token64, int part, int lane) {
   constexpr int L = D / 8;        // lanes of a head
   constexpr int HPW = kWave / L;  // heads of a wave at a time
@@ -56,21 +57,23 @@ __device__ __forceinline__ void norm_rope_heads(const RopeParams& p, int64_t tok
   load_weight(p.k_weight, wk);
 
   const int heads = p.q_heads + p.kv_heads;
-  u32x2_t next_a = {0, 0}, next_b = {0, 0};
-  auto load = [&](int h) {
+  u32x2_t next_a[AHEAD] = {}, next_b[AHEAD] = {};
+  auto load = [&](int e, int h) {
     if (h >= heads) return;
     const uint16_t* src = h < p.q_heads ? p.q + token64 * p.q_stride + (int64_t)h * D
                                         : p.k + token64 * p.k_stride + (int64_t)(h - p.q_heads) * D;
-    next_a = *reinterpret_cast<const u32x2_t*>(src + a);
-    next_b = *reinterpret_cast<const u32x2_t*>(src + b);
+    next_a[e] = *reinterpret_cast<const u32x2_t*>(src + a);
+    next_b[e] = *reinterpret_cast<const u32x2_t*>(src + b);
   };
-  load(part * HPW + sub);
-  for (int h0 = part * HPW; h0 < heads; h0 += p.waves_per_token * HPW) {
+  const int each = p.waves_per_token * HPW;
+#pragma unroll
+  for (int e = 0; e < AHEAD; ++e) load(e, part * HPW + sub + e * each);
+  auto turn = [&](int h0, int e) {
     const int h = h0 + sub;
     const bool live = h < heads;
     const bool is_q = h < p.q_heads;
-    const u32x2_t xa = next_a, xb = next_b;
-    load(h + p.waves_per_token * HPW);  // the next heads while these are worked on
+    const u32x2_t xa = next_a[e], xb = next_b[e];
+    load(e, h + AHEAD * each);  // the next heads while these are worked on
     float x[8];
     unpack_half2<DT>(xa[0], x[0], x[1]);
     unpack_half2<DT>(xa[1], x[2], x[3]);
@@ -109,6 +112,11 @@ __device__ __forceinline__ void norm_rope_heads(const RopeParams& p, int64_t tok
       *reinterpret_cast<u32x2_t*>(dst + b) =
           u32x2_t{pack_half2<DT>(y[4], y[5]), pack_half2<DT>(y[6], y[7])};
     }
+  };
+  for (int h0 = part * HPW; h0 < heads; h0 += AHEAD * each) {
+#pragma unroll
+    for (int e = 0; e < AHEAD; ++e)
+      if (h0 + e * each < heads) turn(h0 + e * each, e);
   }
 }
 
