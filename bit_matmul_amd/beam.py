@@ -8,6 +8,7 @@ the outputs.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 from ._alloc import new as _new
@@ -141,17 +142,24 @@ def kv_attention_shared(q, cache: KVCache, prefix_table, prefix_lens, cu_groups,
 
 
 def _logits_code(t):
-    torch = _torch()
-    code = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}.get(t.dtype)
-    if code is None:
-        raise TypeError(f"logits must be bfloat16, float16 or float32, got {t.dtype}")
-    return code
+    torch, dtype = _torch(), t.dtype
+    if dtype is torch.bfloat16:
+        return 0
+    if dtype is torch.float32:
+        return 1
+    if dtype is torch.float16:
+        return 2
+    raise TypeError(f"logits must be bfloat16, float16 or float32, got {dtype}")
 
 
 def bitmm_beam_select_workspace_bytes(groups, beams, vocab, k, logits_dtype) -> int:
     """Of a call on logits [groups * beams, vocab] of a torch type."""
     torch = _torch()
-    code = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}[logits_dtype]
+    return _select_bytes(groups, beams, vocab, k, {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}[logits_dtype])
+
+
+@functools.lru_cache(maxsize=64)   # the sizes of a search are the same step after step
+def _select_bytes(groups, beams, vocab, k, code):
     return int(_lib().bitmm_beam_select_workspace_bytes(groups, beams, vocab, k, code))
 
 
@@ -165,25 +173,31 @@ def bitmm_beam_select(logits, scores, scores_out, parents, tokens, workspace, *,
     torch = _torch()
     if logits.dim() != 2 or parents.dim() != 2:
         raise ValueError("logits must have two dims (beams of all groups, vocabulary), and parents two (groups, places)")
-    (rows, vocab), (groups, k) = logits.shape, parents.shape
-    index, code = logits.get_device(), _logits_code(logits)
-    if rows != groups * beams:
-        raise ValueError(f"{rows} rows of logits are not {groups} groups of {beams} beams")
-    if vocab > 1 and logits.stride(1) != 1:
-        raise ValueError("the logits of a row must lie side by side")
-    row_stride = logits.stride(0) if rows > 1 else vocab
-    at = [_expect(scores, "scores", torch.float32, (rows,), index), _expect(scores_out, "scores_out", torch.float32, (groups, k), index),
-          _expect(parents, "parents", torch.int32, (groups, k), index), _expect(tokens, "tokens", torch.int32, (groups, k), index)]
-    done = None if finished is None else _expect(finished, "finished", torch.bool, (rows,), index)
-    done_out = None if finished_out is None else _expect(finished_out, "finished_out", torch.bool, (groups, k), index)
+    groups, k = shape = parents.shape
+    index = logits.get_device()
+    if logits.shape[0] != groups * beams:
+        raise ValueError(f"{logits.shape[0]} rows of logits are not {groups} groups of {beams} beams")
+    outs = (_expect(scores_out, "scores_out", torch.float32, shape, index), _expect(parents, "parents", torch.int32, shape, index),
+            _expect(tokens, "tokens", torch.int32, shape, index),
+            None if finished_out is None else _expect(finished_out, "finished_out", torch.bool, shape, index))
     if workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
-    st = _lib().bitmm_beam_select(logits.data_ptr(), row_stride, at[0], done, *at[1:], done_out, groups, beams, vocab, k, end_token,
-                                  code, workspace.data_ptr(), workspace.numel(), _status_word(status, index),
-                                  _stream(stream, index))
+    _select(logits, scores, finished, outs, groups, beams, k, end_token, workspace, status, stream)
+    return scores_out, parents, tokens, finished_out
+
+
+def _select(logits, scores, finished, outs, groups, beams, k, end_token, workspace, status, stream):
+    """The call, with its inputs checked. outs: the addresses of the outputs."""
+    torch = _torch()
+    (rows, vocab), (row_stride, step), index = logits.shape, logits.stride(), logits.get_device()
+    if vocab > 1 and step != 1:
+        raise ValueError("the logits of a row must lie side by side")
+    st = _lib().bitmm_beam_select(
+        logits.data_ptr(), row_stride if rows > 1 else vocab, _expect(scores, "scores", torch.float32, (rows,), index),
+        None if finished is None else _expect(finished, "finished", torch.bool, (rows,), index), *outs, groups, beams, vocab, k,
+        end_token, _logits_code(logits), workspace.data_ptr(), workspace.numel(), _status_word(status, index), _stream(stream, index))
     if st:
         _raise(st, "bitmm_beam_select")
-    return scores_out, parents, tokens, finished_out
 
 
 def beam_select(logits, scores, k: int, *, beams: int, finished=None, end_token: int = -1, workspace=None, status=None,
@@ -194,13 +208,16 @@ def beam_select(logits, scores, k: int, *, beams: int, finished=None, end_token:
     if beams < 1 or rows % beams:
         raise ValueError(f"{rows} rows of logits are not groups of {beams} beams")
     groups = rows // beams
-    out = [_new(logits, (groups, k), t, stream) for t in (torch.float32, torch.int32, torch.int32, torch.bool)]
+    best, ended = _new(logits, (groups, k), torch.float32, stream), _new(logits, (groups, k), torch.bool, stream)
+    parents, tokens = _new(logits, (2, groups, k), torch.int32, stream).unbind()
     if workspace is None:
-        need = int(_lib().bitmm_beam_select_workspace_bytes(groups, beams, vocab, k, _logits_code(logits)))
+        need = _select_bytes(groups, beams, vocab, k, _logits_code(logits))
         workspace = _new(logits, max(need, 16), torch.uint8, stream, returned=False)
-    bitmm_beam_select(logits, scores, *out[:3], workspace, beams=beams, finished=finished, finished_out=out[3],
-                      end_token=end_token, status=status, stream=stream)
-    return tuple(out)
+    elif workspace.dtype is not torch.uint8 or workspace.device != logits.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
+    outs = best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), ended.data_ptr()
+    _select(logits, scores, finished, outs, groups, beams, k, end_token, workspace, status, stream)
+    return best, parents, tokens, ended
 
 
 class KVLayers:
@@ -228,22 +245,31 @@ def bitmm_kv_beam_reorder(layers: KVLayers, page_table, lens, parents, page_tabl
     lens: int32 [groups * beams]; slots: int64 [groups * beams], where the next tokens go; lens_out counts
     them. Outputs may be their inputs. New pages come from the group's pool of pages_per_group pages; see
     include/bitmm_beam.h. workspace: uint8 of at least bitmm_kv_beam_reorder_workspace_bytes(...)."""
-    torch = _torch()
-    if parents.dim() != 2 or page_table.dim() != 2:
-        raise ValueError("parents must have two dims (groups, beams), and page_table two (rows, pages)")
-    (groups, beams), pages, index = parents.shape, page_table.shape[1], layers.device_index
-    rows, int32 = groups * beams, torch.int32
-    at = [_expect(page_table, "page_table", int32, (rows, pages), index), _expect(page_table_out, "page_table_out", int32, (rows, pages), index),
-          _expect(lens, "lens", int32, (rows,), index), _expect(lens_out, "lens_out", int32, (rows,), index),
-          _expect(parents, "parents", int32, (groups, beams), index), _expect(slots, "slots", torch.int64, (rows,), index)]
+    torch, index = _torch(), layers.device_index
+    if page_table.dim() != 2:
+        raise ValueError("page_table must have two dims (rows, pages)")
+    outs = (_expect(page_table_out, "page_table_out", torch.int32, page_table.shape, index),
+            _expect(lens_out, "lens_out", torch.int32, lens.shape, index), _expect(slots, "slots", torch.int64, lens.shape, index))
     if workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
-    st = _lib().bitmm_kv_beam_reorder(layers.desc, len(layers.caches), at[0], at[1], pages, *at[2:], groups, beams, first_page,
-                                      pages_per_group, workspace.data_ptr(), workspace.numel(), _status_word(status, index),
-                                      _stream(stream, index))
+    _reorder(layers, page_table, lens, parents, outs, workspace, first_page, pages_per_group, status, stream)
+    return page_table_out, lens_out, slots
+
+
+def _reorder(layers, page_table, lens, parents, outs, workspace, first_page, pages_per_group, status, stream):
+    """The call, with its inputs checked. outs: the addresses of the outputs, of the shapes of the inputs."""
+    int32, index = _torch().int32, layers.device_index
+    if parents.dim() != 2 or page_table.dim() != 2:
+        raise ValueError("parents must have two dims (groups, beams), and page_table two (rows, pages)")
+    (groups, beams), pages = parents.shape, page_table.shape[1]
+    rows = groups * beams
+    st = _lib().bitmm_kv_beam_reorder(
+        layers.desc, len(layers.caches), _expect(page_table, "page_table", int32, (rows, pages), index), outs[0], pages,
+        _expect(lens, "lens", int32, (rows,), index), outs[1], _expect(parents, "parents", int32, (groups, beams), index), outs[2],
+        groups, beams, first_page, pages_per_group, workspace.data_ptr(), workspace.numel(), _status_word(status, index),
+        _stream(stream, index))
     if st:
         _raise(st, "bitmm_kv_beam_reorder")
-    return page_table_out, lens_out, slots
 
 
 def kv_beam_reorder(layers: KVLayers, page_table, lens, parents, *, first_page: int, pages_per_group: int, workspace=None,
@@ -254,5 +280,8 @@ def kv_beam_reorder(layers: KVLayers, page_table, lens, parents, *, first_page: 
     slots = _new(lens, lens.shape, torch.int64, stream)
     if workspace is None:
         workspace = _new(lens, max(16 * lens.numel(), 16), torch.uint8, stream, returned=False)
-    return bitmm_kv_beam_reorder(layers, page_table, lens, parents, table, lens_out, slots, workspace, first_page=first_page,
-                                 pages_per_group=pages_per_group, status=status, stream=stream)
+    elif workspace.dtype is not torch.uint8 or workspace.device != lens.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
+    outs = table.data_ptr(), lens_out.data_ptr(), slots.data_ptr()
+    _reorder(layers, page_table, lens, parents, outs, workspace, first_page, pages_per_group, status, stream)
+    return table, lens_out, slots
