@@ -5,6 +5,10 @@
 // Two kernels. beam_plan_kernel, a workgroup a group of beams: the new table and lengths, which pages of the group's
 // pool no row holds (a bit each in LDS), the pages handed out, the slots of the next tokens and a list of copies.
 // beam_copy_kernel, a workgroup a row, layer and side: the copies.
+//
+// What bounds it: latency. Four beams through 40 layers of 8 heads of 128 dims: 4.5 us for the plan, whose loads of
+// parents, lengths and table wait for one another, 6.6 for the copies of 3 MB. 16 groups of eight beams through 24
+// layers: 6.9 and 17.0 us for 52 MB, 3.1 TB/s (a copy 5.2), in pieces of some hundred bytes of pairs and 2 KB of codes.
 #include "beam.hpp"
 
 namespace bitmm {
