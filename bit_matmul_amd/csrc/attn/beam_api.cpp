@@ -29,6 +29,7 @@ struct PartRows {
   int64_t prefix, own;
 };
 PartRows part_rows(const SharedPlan& plan, int64_t B, int64_t groups, int64_t max_group_q, int64_t q_heads, int64_t kv_heads) {
+  if (plan.both) return {0, 0};
   return {groups * kv_heads * (max_group_q * (q_heads / kv_heads) + (int64_t)std::max(plan.prefix.splits - 1, 0) * plan.prefix.tail_rows),
           plan.own.splits > 1 ? (int64_t)plan.own.splits * B * kv_heads * plan.own.tail_rows : 0};
 }

@@ -1,6 +1,7 @@
 // Reordering of the cached states of beams after a selection. Rows of the page table follow their parents, so
 // that full pages are shared by all that descend from them; of rows whose last page is partly filled and the same,
-// the first keeps it and the others get pages of their own with a copy of its tokens, in every layer.
+// the first keeps it, if it is of their pool, and the others get pages of their own with a copy of its tokens, in
+// every layer.
 //
 // Two kernels. beam_plan_kernel, a workgroup a group of beams: the new table and lengths, which pages of the group's
 // pool no row holds (a bit each in LDS), the pages handed out, the slots of the next tokens and a list of copies.
@@ -84,11 +85,14 @@ __global__ __launch_bounds__(kPlanThreads) void beam_plan_kernel(ReorderParams p
   __syncthreads();
   if (tid >= 64) return;
 
-  // A lane a row. Rows that need a page: those without a partly filled one, and those whose is an earlier row's.
+  // A lane a row. Rows that need a page: those without a partly filled one, and those whose is an earlier row's, or
+  // not the pool's: a prompt's pages are not written.
   const int n = tokens[tid], column = n >> p.page_shift, part = n & (size - 1), mine = last_page[tid];
   const bool live = parent[tid] >= 0;
   bool again = false;
   for (int j = 0; j < beams; ++j) again = again || (j < tid && last_page[j] == mine && tokens[j] & (size - 1));
+  const bool inside = (uint32_t)mine < (uint32_t)p.num_pages;
+  again = again || (inside && (uint32_t)(mine - base) >= (uint32_t)p.pages_per_group);
   const bool wants = live && (part == 0 || again) && column < p.pages_per_seq;
   const uint64_t all = __ballot(wants);
   const int want = __builtin_popcountll(all), place = __builtin_popcountll(all & ((1ull << tid) - 1));
@@ -116,7 +120,6 @@ __global__ __launch_bounds__(kPlanThreads) void beam_plan_kernel(ReorderParams p
   __builtin_amdgcn_s_waitcnt(0);
   if (tid < beams) {
     const int64_t row = row0 + tid;
-    const bool inside = (uint32_t)mine < (uint32_t)p.num_pages;
     Copy copy = {0, 0, 0, 0};
     int page = -1;
     if (wants && place < found) {

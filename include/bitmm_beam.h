@@ -112,8 +112,8 @@ bitmm_status bitmm_beam_select(const void* logits, int64_t row_stride, const flo
  * group (0 .. beams - 1; -1: none, an empty row) and one more, which is to be stored at slots[r]
  * (as bitmm_kv_append takes it) and which lens_out counts. Pages that are full are shared: rows of
  * the table name the same ones. A last page that is partly filled is kept by the first row that
- * has it; the others get a page each, to which the tokens are copied, in all `layers` caches (one for
- * each layer of a model, of the same sizes; their pages share one table). A row whose last page is full,
+ * has it, if it is of the group's pool; the others get a page each, to which the tokens are copied, in all
+ * `layers` caches (one for each layer of a model, of the same sizes; their pages share one table). A row whose last page is full,
  * or that is empty, gets a page for the next token.
  * New pages are the lowest ones of the group's pool that no row of the group holds afterwards, in the
  * order of the rows: pages [first_page + g * pages_per_group, + pages_per_group). A pool of beams *

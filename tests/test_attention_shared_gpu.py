@@ -362,3 +362,31 @@ def test_captured_on_another_stream(rows):
     s.q = q.cpu()
     want, _, tol, _ = s.reference(BF, 1 / math.sqrt(128))
     assert ((replayed.cpu().double() - want).abs() <= tol).all()
+
+
+def test_pages_past_32_bits():
+    """Codes more than 2^32 bytes into the cache are written, seen and copied like those of a small one."""
+    pages, far, page, D = 140, 139860, 256, 256
+    small, large = (bm.KVCache.empty(n, page, 1, D, 128) for n in (pages, far + pages))
+    assert large.k_codes.numel() * 4 > 2 ** 32 + 140 * page * 128
+    g = torch.Generator().manual_seed(9)
+    T, beams_n = 1500, 3
+    k, v = (torch.randn(T, 1, D, generator=g).to(BF).cuda() for _ in range(2))
+    q = torch.randn(beams_n, 4, D, generator=g).to(BF).cuda()
+    freq, _ = bm.rope_frequencies(D, device="cuda")
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    outs = []
+    for cache, base in ((small, 0), (large, far)):
+        order = torch.arange(6, device="cuda") * 20 + base + 3    # scattered pages, the last near the end
+        at = torch.arange(T, device="cuda")
+        bm.bitmm_qk_norm_rope_append(None, k, v, None, None, pos, freq, None, order[at // page] * page + at % page, cache)
+        table = (order[5:].int().expand(3) + torch.zeros(3, dtype=torch.int32, device="cuda"))[:, None].contiguous()
+        table, lens, slots = bm.kv_beam_reorder(bm.KVLayers([cache]), table, i32([200, 200, 200]), i32([[0, 1, 2]]), first_page=base + 100,
+                                                pages_per_group=40)
+        bm.bitmm_kv_append(k[:3], v[:3], slots, cache)
+        outs.append([table - base, slots - base * page] + [
+            bm.kv_attention_shared(q, cache, order[:5][None].int(), i32([1280]), i32([0, 3]), table, lens, i32([0, 1, 2, 3]),
+                                   max_group_q=3, max_prefix=bound, max_q=1, max_kv=201) for bound in (1024, 1280, 5000)])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    assert outs[0][-1].isfinite().all()

@@ -65,7 +65,8 @@ def plain(table, lens, parents, page, num_pages, first, each):
                 continue
             column, part = divmod(n[r], page)
             at = -1
-            if part and new[r][column] not in seen:
+            mine = base <= new[r][column] < base + each or not 0 <= new[r][column] < num_pages if part else False
+            if part and mine and new[r][column] not in seen:
                 seen.add(new[r][column])
                 at = new[r][column] if 0 <= new[r][column] < num_pages else -1
             elif column < width and free:
@@ -151,6 +152,14 @@ def test_beams_that_start_on_one_page():
     table = torch.tensor([[4, 7, 0]] * 3, dtype=torch.int32)
     got = check(layers, table, torch.tensor([20, 20, 20], dtype=torch.int32), torch.arange(3, dtype=torch.int32)[None], 1, 30)
     assert got[0][:, 1].tolist() == [7, 1, 2]
+
+
+def test_pages_of_a_prompt_are_not_written():
+    """Rows whose partly filled page lies outside their pool all copy it."""
+    layers = layers_of(2, 40, 16, 2, 64, 32)
+    table = torch.tensor([[4, 7, 0]] * 3, dtype=torch.int32)
+    got = check(layers, table, torch.tensor([20, 20, 20], dtype=torch.int32), torch.arange(3, dtype=torch.int32)[None], 10, 9)
+    assert got[0][:, 1].tolist() == [10, 11, 12] and got[0][:, 0].tolist() == [4, 4, 4]
 
 
 def test_a_pool_that_ends():
@@ -247,6 +256,6 @@ def test_other_stream_and_launches():
     got = bm.kv_beam_reorder(layers, table, lens, parents, first_page=10, pages_per_group=9, stream=stream)
     assert len(bm.bitmm_last_launches()) == 3   # the plan, and copies of up to 64 layers at a time
     torch.cuda.current_stream().wait_stream(stream)
-    assert got[0].tolist() == [[4, 7, 0], [4, 10, 0], [4, 11, 0]] and got[2].tolist() == [116, 164, 180]
+    assert got[0].tolist() == [[4, 10, 0], [4, 11, 0], [4, 12, 0]] and got[2].tolist() == [164, 180, 196]
     c = layers.caches[64]
     assert torch.equal(c.k_codes[11, :, :4], c.k_codes[7, :, :4])
