@@ -117,6 +117,18 @@ struct TileGathered {
   int unit;
 };
 
+// Of eight neighbouring dims of a row its two lanes hold 0, 1, 4, 5 and 2, 3, 6, 7: the second pair of the one for the
+// first of the other makes them four neighbours each, for one access of 16 bytes, and the other way round. 12 chunks behind
+// prompts, own pass: 51 -> 41 us against two accesses of 8 bytes.
+__device__ __forceinline__ void swap_pairs(f32x4_t& y) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(y[i]), __float_as_uint(y[i + 2]), false, false);
+    y[i] = __uint_as_float(r[0]);
+    y[i + 2] = __uint_as_float(r[1]);
+  }
+}
+
 // RW: waves that take rows of their own. Eight waves are eight row waves, or two for each of four: the one takes
 // the first 64 tokens of each tile, the other the rest, and they join at the end.
 // CAREFUL: with units that change and tokens that have their own. Without, the first tile's units have to do for
@@ -802,12 +814,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(typena
           for (int d = 0; d < DB; ++d)
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              const float* from = prefix.part_o + at * D + 32 * d + 2 * e + 2 * h;
-              const float2 a = *reinterpret_cast<const float2*>(from), b2 = *reinterpret_cast<const float2*>(from + 4);
-              o[d][e] = o[d][e] * own_part + a.x * other;
-              o[d][e + 2] = o[d][e + 2] * own_part + a.y * other;
-              o[d][e + 1] = o[d][e + 1] * own_part + b2.x * other;
-              o[d][e + 3] = o[d][e + 3] * own_part + b2.y * other;
+              f32x4_t y = *reinterpret_cast<const f32x4_t*>(prefix.part_o + at * D + 32 * d + 2 * e + 4 * h);
+              swap_pairs(y);
+              o[d][e] = o[d][e] * own_part + y[0] * other;
+              o[d][e + 2] = o[d][e + 2] * own_part + y[1] * other;
+              o[d][e + 1] = o[d][e + 1] * own_part + y[2] * other;
+              o[d][e + 3] = o[d][e + 3] * own_part + y[3] * other;
             }
         }
       }
@@ -827,6 +839,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_tiles_kernel(typena
     for (int d = 0; d < DB; ++d)
 #pragma unroll
       for (int e = 0; e < 16; e += 4) {
+        if constexpr (PASS != kAlone) {
+          f32x4_t y = {o[d][e] * out_scale, o[d][e + 2] * out_scale, o[d][e + 1] * out_scale, o[d][e + 3] * out_scale};
+          swap_pairs(y);
+          *reinterpret_cast<f32x4_t*>(p.part_o + at * D + 32 * d + 2 * e + 4 * h) = y;
+          continue;
+        }
         float* to = p.part_o + at * D + 32 * d + 2 * e + 2 * h;
         *reinterpret_cast<float2*>(to) = make_float2(o[d][e] * out_scale, o[d][e + 2] * out_scale);
         *reinterpret_cast<float2*>(to + 4) = make_float2(o[d][e + 1] * out_scale, o[d][e + 3] * out_scale);
