@@ -87,6 +87,7 @@ __device__ __forceinline__ void norm_rope_heads(const RopeParams& p, int64_t tok
     const float r = norm ? rsqrtf(sq * (1.f / D) + p.eps) : 1.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = x[i] * r * (is_q ? wq[i] : wk[i]);
+    // Which product is rounded is written out, so that every kernel with these turns gives the same bits.
     float y[8];
     if (!turned) {  // passed on, without rope_scale
 #pragma unroll
@@ -94,14 +95,14 @@ __device__ __forceinline__ void norm_rope_heads(const RopeParams& p, int64_t tok
     } else if constexpr (INTERLEAVED) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        y[2 * i] = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
-        y[2 * i + 1] = x[2 * i + 1] * c[i] + x[2 * i] * s[i];
+        y[2 * i] = fmaf(x[2 * i], c[i], -(x[2 * i + 1] * s[i]));
+        y[2 * i + 1] = fmaf(x[2 * i], s[i], x[2 * i + 1] * c[i]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        y[i] = x[i] * c[i] - x[4 + i] * s[i];
-        y[4 + i] = x[4 + i] * c[i] + x[i] * s[i];
+        y[i] = fmaf(x[i], c[i], -(x[4 + i] * s[i]));
+        y[4 + i] = fmaf(x[i], s[i], x[4 + i] * c[i]);
       }
     }
     if (live) {
