@@ -7,9 +7,9 @@
 // pool no row holds (a bit each in LDS), the pages handed out, the slots of the next tokens and a list of copies.
 // beam_copy_kernel, a workgroup a row, layer and side: the copies.
 //
-// What bounds it: latency. Four beams through 40 layers of 8 heads of 128 dims: 4.5 us for the plan, whose loads of
+// What bounds it: latency. Four beams through 40 layers of 8 heads of 128 dims: 4.8 us for the plan, whose loads of
 // parents, lengths and table wait for one another, 6.6 for the copies of 3 MB. 16 groups of eight beams through 24
-// layers: 6.9 and 17.0 us for 52 MB, 3.1 TB/s (a copy 5.2), in pieces of some hundred bytes of pairs and 2 KB of codes.
+// layers: 7.2 and 17.0 us for 52 MB, 3.1 TB/s (a copy 5.2), in pieces of some hundred bytes of pairs and 2 KB of codes.
 #include "beam.hpp"
 
 namespace bitmm {
@@ -86,13 +86,21 @@ __global__ __launch_bounds__(kPlanThreads) void beam_plan_kernel(ReorderParams p
   if (tid >= 64) return;
 
   // A lane a row. Rows that need a page: those without a partly filled one, and those whose is an earlier row's, or
-  // not the pool's: a prompt's pages are not written.
+  // a longer one's and full there (beside a row that once got no room), or not the pool's: a prompt's pages are not
+  // written.
   const int n = tokens[tid], column = n >> p.page_shift, part = n & (size - 1), mine = last_page[tid];
   const bool live = parent[tid] >= 0;
   bool again = false;
-  for (int j = 0; j < beams; ++j) again = again || (j < tid && last_page[j] == mine && tokens[j] & (size - 1));
+  int longest = 0;
+  for (int j = 0; j < beams; ++j) {
+    again = again || (j < tid && last_page[j] == mine && tokens[j] & (size - 1));
+    longest = max(longest, tokens[j]);
+  }
   const bool inside = (uint32_t)mine < (uint32_t)p.num_pages;
   again = again || (inside && (uint32_t)(mine - base) >= (uint32_t)p.pages_per_group);
+  if (part && inside && longest >> p.page_shift > column)  // mostly the rows are as long as each other
+    for (int j = 0; j < beams; ++j)
+      if (!again && tokens[j] >> p.page_shift > column) again = p.table_out[(row0 + j) * p.pages_per_seq + column] == mine;
   const bool wants = live && (part == 0 || again) && column < p.pages_per_seq;
   const uint64_t all = __ballot(wants);
   const int want = __builtin_popcountll(all), place = __builtin_popcountll(all & ((1ull << tid) - 1));

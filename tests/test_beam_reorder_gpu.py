@@ -57,7 +57,7 @@ def plain(table, lens, parents, page, num_pages, first, each):
                     new[r][c] = table[g * beams + p][c]
                     held.add(new[r][c])
         free = [x for x in range(base, base + each) if x not in held]
-        seen = set()
+        seen, table_at = set(), [list(r) for r in new]
         for r in rows:
             if n[r] < 0:
                 new_lens.append(0)
@@ -66,6 +66,9 @@ def plain(table, lens, parents, page, num_pages, first, each):
             column, part = divmod(n[r], page)
             at = -1
             mine = base <= new[r][column] < base + each or not 0 <= new[r][column] < num_pages if part else False
+            full = part and any(n[o] // page > column and table_at[o][column] == new[r][column] for o in rows)
+            if full and 0 <= new[r][column] < num_pages:
+                mine = False
             if part and mine and new[r][column] not in seen:
                 seen.add(new[r][column])
                 at = new[r][column] if 0 <= new[r][column] < num_pages else -1
@@ -170,6 +173,19 @@ def test_a_pool_that_ends():
         for parents in (torch.arange(4, dtype=torch.int32)[None], torch.tensor([[-1, 2, 1, 0]], dtype=torch.int32)):
             check(layers, table, lens, parents, 10, each)
             check(layers, table, torch.tensor([16, 32, 16, 16], dtype=torch.int32), parents, 10, each)
+
+
+def test_a_page_that_is_full_for_a_longer_row():
+    """Where a pool ended, one row got no room and the other filled the page that both have: it is copied."""
+    layers = layers_of(2, 40, 16, 2, 64, 32)
+    table = torch.tensor([[4, 7, 0]] * 2, dtype=torch.int32)
+    own = torch.tensor([[0, 1]], dtype=torch.int32)
+    t, n, slots = check(layers, table, torch.tensor([31, 31], dtype=torch.int32), own, 7, 1)
+    assert n.tolist() == [32, 31] and slots.tolist() == [7 * 16 + 15, -1]
+    for order in (own, own.flip(1)):
+        got = check(layers, t.cpu(), n.cpu(), order, 7, 9)
+        at = order[0].tolist().index(1)
+        assert got[0][at, 1].item() != 7 and got[0][1 - at, 1].item() == 7
 
 
 def test_out_of_range():
