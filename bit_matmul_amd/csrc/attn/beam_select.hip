@@ -10,17 +10,20 @@
 // exponentials and sums are f64: 2^z with z split into a whole and a fraction by an addition, and a polynomial of
 // degree 7 in the fraction whose relative error is 4e-11 (fitted for the smallest largest one). So sums agree with
 // exact ones to some 1e-11, and totals to that. Equal rows have equal sums: they are added up in the same order.
+// Differences of logits are taken before anything is done with them: two f32 numbers' is exact in f64, or far from
+// all that counts. (A reference's product with log2 e, rounded, is off by 2^-53 of it: for logits of 1e8 by more than the
+// exponentials, and past 5e18 by whole powers of two.)
 //
 // The k largest. A wave's threshold is a lower bound of its part's k-th largest logit: the k-th largest of the
 // lanes' largest ones at first, then the k-th of those found so far. Logits that pass it go to LDS as pairs
 // (order-preserving key, token inverted), one 64-bit number each, so that the pair's order is the candidates';
 // where they become many their ranks are counted and the first k stay.
 //
-// What bounds it: f64 arithmetic, 14 instructions a logit of 17, and the latency of the join. 256 rows of 131072 bf16
-// logits, a fifth of them not read: 38 us for 54 MB (a copy's rate: 10) with vector instructions issued in 52 % of the
+// What bounds it: f64 arithmetic, 15 instructions a logit of 18, and the latency of the join. 256 rows of 131072 bf16
+// logits, a fifth of them not read: 38.5 us for 54 MB (a copy's rate: 10) with vector instructions issued in 52 % of the
 // cycles, join 8. 24 % fewer instructions in the sums' loop, none of them f64, changed nothing, nor did a threshold
 // that the waves of a row share, nor 1536 or 2048 workgroups for 1024 (44, 50 and 48 us). Four rows of 32000 f32
-// logits: 6.8 and 4.8 us, two launches and their latencies.
+// logits: 7.4 and 4.9 us, two launches and their latencies.
 #include "beam.hpp"
 
 namespace bitmm {
@@ -196,7 +199,7 @@ __global__ __launch_bounds__(64 * kWaves) void beam_scan_kernel(SelectParams p) 
   found.k = p.k;
   found.lane = lane;
   float ref = -INFINITY;     // exponentials are of x - ref
-  double ref_z = 0., sum = 0.;
+  double ref64 = 0., sum = 0.;
   int positive = 0;          // the largest bit patterns of all, as signed and as unsigned numbers: NaN and
   uint32_t negative = 0;     // infinity lie above all others of their sign, but -infinity above all negative ones
 
@@ -218,14 +221,14 @@ __global__ __launch_bounds__(64 * kWaves) void beam_scan_kernel(SelectParams p) 
       }
     if (__any(most > ref + 300.f)) {  // the first ones, and much larger ones
       const float top = fminf(reduce_lanes<64>(most, Max()), -kLowest);
-      sum = ref == -INFINITY ? 0. : sum * exp2_f64(fmax(((double)ref - (double)top) * kLog2eF64, -1000.));
+      sum = ref == -INFINITY ? 0. : sum * exp2_f64(fmax((ref64 - (double)top) * kLog2eF64, -1000.));
       ref = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(top)));
-      ref_z = -(double)ref * kLog2eF64;
+      ref64 = (double)ref;
     }
     double a = 0., b = 0.;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i < n) (i & 1 ? b : a) += exp2_f64(fmax(fma((double)x[i], kLog2eF64, ref_z), -1000.));
+      if (i < n) (i & 1 ? b : a) += exp2_f64(fmax(((double)x[i] - ref64) * kLog2eF64, -1000.));
     sum += a + b;
     return most;
   };
@@ -347,7 +350,6 @@ __global__ __launch_bounds__(512) void beam_merge_kernel(SelectParams p) {
     uint64_t* mine = totals + b * p.k;
     if (lane < p.k) mine[lane] = 0;
     const bool odd = score != score || score == INFINITY;
-    double lse = 0.;
     bool bad = odd;
     if (!odd && !done && score != -INFINITY) {
       // the parts' sums, each of exponentials of x - ref
@@ -356,7 +358,7 @@ __global__ __launch_bounds__(512) void beam_merge_kernel(SelectParams p) {
       const double top = (double)reduce_lanes<64>((float)ref, Max());
       const double sum = add_lanes(part == 0. ? 0. : part * exp2_f64(fmax((ref - top) * kLog2eF64, -1000.)));
       bad = sum != sum;
-      lse = top + log(sum);
+      const double log_sum = log(sum);
       if (!bad && sum > 0.) {
         // The parts' lists are in order: the largest of their first ones, k times.
         const uint64_t* list = p.part_top + (row * p.parts + min(lane, p.parts - 1)) * p.k;
@@ -367,7 +369,7 @@ __global__ __launch_bounds__(512) void beam_merge_kernel(SelectParams p) {
           const uint64_t best = wave_max(now, at);
           if (best == 0) break;
           if (lane == at) {
-            mine[i] = order_of((double)score + ((double)float_of((uint32_t)(best >> 32)) - lse));
+            mine[i] = order_of((double)score + (((double)float_of((uint32_t)(best >> 32)) - top) - log_sum));
             tokens[b * p.k + i] = (int)~(uint32_t)best;
             ++taken;
             now = next;
