@@ -1,7 +1,8 @@
 // Reordering of the cached states of beams after a selection. Rows of the page table follow their parents, so
 // that full pages are shared by all that descend from them; of rows whose last page is partly filled and the same,
-// the first keeps it, if it is of their pool, and the others get pages of their own with a copy of its tokens, in
-// every layer.
+// the first of those with the most tokens on it keeps it, if it is of their pool, and the others get pages of their own
+// with a copy of its tokens, in every layer. So a row that gets no room keeps what it has: nothing is stored where it,
+// or a longer row, holds a token.
 //
 // Two kernels. beam_plan_kernel, a workgroup a group of beams: the new table and lengths, which pages of the group's
 // pool no row holds (a bit each in LDS), the pages handed out, the slots of the next tokens and a list of copies.
@@ -85,15 +86,16 @@ __global__ __launch_bounds__(kPlanThreads) void beam_plan_kernel(ReorderParams p
   __syncthreads();
   if (tid >= 64) return;
 
-  // A lane a row. Rows that need a page: those without a partly filled one, and those whose is an earlier row's, or
-  // a longer one's and full there (beside a row that once got no room), or not the pool's: a prompt's pages are not
-  // written.
+  // A lane a row. Rows that need a page: those without a partly filled one, and those whose is also that of a row with
+  // more tokens on it (the other once got no room) or of an earlier one with as many, or is full in a longer row, or is
+  // not the pool's: a prompt's pages are not written.
   const int n = tokens[tid], column = n >> p.page_shift, part = n & (size - 1), mine = last_page[tid];
   const bool live = parent[tid] >= 0;
   bool again = false;
   int longest = 0;
   for (int j = 0; j < beams; ++j) {
-    again = again || (j < tid && last_page[j] == mine && tokens[j] & (size - 1));
+    const int there = tokens[j] & (size - 1);
+    again = again || (there && last_page[j] == mine && (there > part || (there == part && j < tid)));
     longest = max(longest, tokens[j]);
   }
   const bool inside = (uint32_t)mine < (uint32_t)p.num_pages;

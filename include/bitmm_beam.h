@@ -111,10 +111,11 @@ bitmm_status bitmm_beam_select(const void* logits, int64_t row_stride, const flo
  * [groups * beams, pages_per_seq] names. After the call it has those of beam parents[r] of its
  * group (0 .. beams - 1; -1: none, an empty row) and one more, which is to be stored at slots[r]
  * (as bitmm_kv_append takes it) and which lens_out counts. Pages that are full are shared: rows of
- * the table name the same ones. A last page that is partly filled is kept by the first row that
- * has it, if it is of the group's pool and no longer row has it full in the same place; the others get a page each, to which the tokens are copied, in all
- * `layers` caches (one for each layer of a model, of the same sizes; their pages share one table). A row whose last page is full,
- * or that is empty, gets a page for the next token.
+ * the table name the same ones. A last page that is partly filled is kept by one row, if it
+ * is of the group's pool and no longer row has it full in the same place: that with the most tokens on it, the first of
+ * those with as many. The others get a page each, to which the tokens are copied, in all `layers` caches (one for each
+ * layer of a model, of the same sizes; their pages share one table). A row whose last page is full, or that is empty,
+ * gets a page for the next token.
  * New pages are the lowest ones of the group's pool that no row of the group holds afterwards, in the
  * order of the rows: pages [first_page + g * pages_per_group, + pages_per_group). A pool of beams *
  * pages_per_seq pages never ends. Pages outside it, as those of a prompt, may be named and are never written;
