@@ -122,7 +122,9 @@ bitmm_status bitmm_beam_select(const void* logits, int64_t row_stride, const flo
  * they lie in no other group's pool.
  * A row for which no page or no place in the table is left keeps its parent's tokens and gets no room:
  * its slot is -1, lens_out is its parent's, and *status is set, as it is by parents and lengths out of range
- * (taken as -1, and cut) and by a partly filled page outside the cache. Empty rows have slot -1 and a length of 0.
+ * (taken as -1, and cut) and by a partly filled page outside the cache, whose tokens are lost: the first row that has
+ * it gets no room, any other a page of its own, of which the slots before its next token hold what lay there before.
+ * Empty rows have slot -1 and a length of 0.
  * Entries of the table past a row's pages are passed on as they are. An output may be its input (same
  * pointer), otherwise they do not overlap.
  * beams 1 to 64, groups * beams up to 2^22, layers up to 4096, pages_per_seq up to 2^22, pages_per_group up to 2^18
