@@ -77,9 +77,9 @@ def bitmm_qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, 
 
 
 def qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, slots, cache: KVCache, *, stream=None, **options):
-    """Returns q_out, a new tensor."""
-    return bitmm_qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, _new(q, q.shape, q.dtype, stream),
-                                     slots, cache, stream=stream, **options)
+    """Returns q_out, a new tensor, or None if q is None."""
+    q_out = None if q is None else _new(q, q.shape, q.dtype, stream)
+    return bitmm_qk_norm_rope_append(q, k, v, q_weight, k_weight, positions, inv_freq, q_out, slots, cache, stream=stream, **options)
 
 
 def bitmm_kv_attention_shared_workspace_bytes(T, B, groups, max_group_q, max_prefix, max_q, max_kv, q_heads, kv_heads, head_dim) -> int:
