@@ -95,7 +95,7 @@ def bitmm_kv_attention_shared(q, cache: KVCache, prefix_table, prefix_lens, cu_g
     sequences of each group); page_table: int32 [B, pages], kv_lens: int32 [B], cu_q: int32 [B + 1] as in
     bitmm_kv_attention, of the own tokens. max_group_q: a bound of a group's queries, max_prefix of the
     shared tokens, max_q and max_kv of a sequence's queries and own tokens. out, lse, scale: as there;
-    workspace: uint8 of at least bitmm_kv_attention_shared_workspace_bytes(...)."""
+    workspace: uint8 of at least bitmm_kv_attention_shared_workspace_bytes(...), or None if that is 0."""
     torch = _torch()
     T, heads, D = shape = q.shape
     B, groups = kv_lens.shape[0], prefix_lens.shape[0]
@@ -114,12 +114,15 @@ def bitmm_kv_attention_shared(q, cache: KVCache, prefix_table, prefix_lens, cu_g
           _expect(page_table, "page_table", int32, (B, pages), index)]
     lens, cu = _expect(kv_lens, "kv_lens", int32, (B,), index), _expect(cu_q, "cu_q", int32, (B + 1,), index)
     prefix = _expect(prefix_table, "prefix_table", int32, (groups, prefix_pages), index)
-    if workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.dtype is not torch.uint8 or workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor on the same device")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
     st = _lib().bitmm_kv_attention_shared(
         q.data_ptr(), q_stride, cache.desc, prefix, prefix_pages, *at, pages, lens, cu, out.data_ptr(), out_stride,
         None if lse is None else _expect(lse, "lse", torch.float32, (T, heads), index), T, B, groups, heads, max_group_q, max_prefix,
-        max_q, max_kv, 1.0 / math.sqrt(D) if scale is None else scale, code, out_code, workspace.data_ptr(), workspace.numel(),
+        max_q, max_kv, 1.0 / math.sqrt(D) if scale is None else scale, code, out_code, ws, ws_bytes,
         _status_word(status, index), _stream(stream, index))
     if st:
         _raise(st, "bitmm_kv_attention_shared")
