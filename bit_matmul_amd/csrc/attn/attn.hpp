@@ -95,8 +95,6 @@ struct AttentionParams {
 struct AttentionPlan {
   bool tiles;      // the kernel for many query rows
   int waves;       // of a workgroup, in the kernel for few rows
-  int fill;        // workgroups at a time
-  int most;        // parts that a tile's tokens may be split into
   int rows_each;   // rows of a tile
   int row_tiles;
   int tail_tiles;  // 0 where nothing is split
