@@ -686,7 +686,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 2 : 4) void attention_rows_k
 
   auto partial = [&] { return PASS == kPrefix || (p.splits > 1 && (p.balanced || work.splits > 1)); };
   // Of the results over the shared tokens each wave takes in every WAVES-th part: their loads overlap, and the join
-  // below is one for all (the parts one after the other behind it: 64 samples, 16 parts 23 us against 20).
+  // below is one for all (the parts one after the other behind it: 64 samples, ten parts 23 us against 20).
   [[maybe_unused]] int parts = 0;
   if constexpr (PASS == kBoth) parts = shared.parts(params.prefix, shared.row(params.prefix, ex.q0, min(r0 + n, ex.rows - 1)));
   if constexpr (PASS == kOwn) {

@@ -7,14 +7,16 @@
 // over the parts s of both, added up in f32: by the second pass where it ends a row, else, where a row's own tokens
 // are split, by attention_join_shared_kernel.
 //
-// What bounds it. Few beams: latency, one chain of it in one launch where tokens are few (12.1 us for four beams after
-// 573 tokens, 9.6 of which attention of one sequence takes). Eight ragged groups of four beams after up to 4096: 21.7 us
-// for the shared tokens, three steps a wave behind a chain of loads (groups, rows, pages, codes), and 11.0 for the own
-// ones. 64 samples of 32768 tokens, 320 query rows a kv head: 82.6 us, of which 42 are products and softmax (matrix
-// cores busy in 20 % of the cycles), 9 the tiles' expansion, 9 the parts' stores, 12 begin and end; then 20.4 for the own
-// tokens, 16 parts taken in. Two tiles of 16 rows to a wave, which would share its expanded values, won nothing
-// (36.8 us against 39.3 for 60 rows: registers leave two waves a SIMD; with three they spill), nor did workgroups of four
-// waves, two a CU, for many rows (88 us against 87), nor fewer parts for a last tile with few rows (90 against 91).
+// What bounds it. Few beams: latency, one chain of it in one launch where tokens are few (12.2 us for four beams after
+// 573 tokens, 9.6 of which attention of one sequence takes). Eight ragged groups of four beams after up to 4096: 21.6 us
+// for the shared tokens, three steps a wave of the longest group behind a chain of loads (groups, rows, pages, codes); a
+// short group has as many parts as a long one, and 20 rows are a tile of 16 and one of 4, which goes over all again. Then
+// 11.1 for the own ones. 64 samples of 32768 tokens, 320 query rows a kv head: 82 to 84 us, of which 42 are products and
+// softmax (matrix cores busy in 20 % of the cycles), 9 the tiles' expansion, 9 the parts' stores and 12 begin and end;
+// some ten are not accounted for. Then 20.5 for the own tokens, ten parts of each row taken in. Two tiles of 16 rows to a
+// wave, which would share its expanded values, were not kept (registers leave two waves a SIMD; with three they spill);
+// nor did workgroups of four waves, two a CU, win for many rows (88 us against 87), nor fewer parts for a last tile
+// with few rows (90 against 91).
 #include "attention_rows.hpp"
 
 namespace bitmm {
@@ -114,10 +116,10 @@ SharedPlan plan_attention_shared(int64_t groups, int64_t B, int64_t max_group_q,
   plan.own = plan_attention(B, max_q, max_kv, q_heads, kv_heads, head_dim, 0, 0);
   if (groups == 0 || max_group_q == 0) return plan;
   // Where all sequences' workgroups run at once, two a CU, and tokens are few, each goes over the shared ones by itself:
-  // one launch, one chain of latencies. In us, this against two launches, 40 heads over 8 of 128 dims: four beams after 573
-  // tokens 13.5 and 16.1, after 1200 17.4 and 18.5, after 1600 20.8 and 19.8; 32 beams after 600 12.9 and 20.0; 16 groups
-  // of four after 600 19.4 and 25.0, after 1200 26.8 and 29.4, after 1600 32.5 and 32.2; 20 groups after 600 26.8 and
-  // 25.8. 16 heads over 4 of 256 dims, one group after 1200 25.2 and 23.2.
+  // one launch, one chain of latencies. Calls in us, this against two launches, 40 heads over 8 of 128 dims: four beams
+  // after 573 tokens 11.7 and 15.9, after 1200 17.4 and 18.4, after 1600 21.0 and 19.8; 32 beams after 600 13.6 and 21.3;
+  // 16 groups of four after 600 19.6 and 24.8, after 1200 26.8 and 29.4, after 1600 32.7 and 32.1; 20 groups after 600
+  // 26.9 and 25.7. 16 heads over 4 of 256 dims, one group after 900 22.2 and 21.7, after 1200 24.9 and 22.9.
   const int64_t row_tiles = (max_q * (q_heads / kv_heads) + kRows - 1) / kRows;
   plan.both = B * kv_heads * row_tiles <= 512 && max_prefix <= (head_dim == 256 ? 1024 : 1280) && max_kv <= 1024;
   if (plan.both) {

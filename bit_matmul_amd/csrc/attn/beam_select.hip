@@ -19,11 +19,12 @@
 // (order-preserving key, token inverted), one 64-bit number each, so that the pair's order is the candidates';
 // where they become many their ranks are counted and the first k stay.
 //
-// What bounds it: f64 arithmetic, 15 instructions a logit of 18, and the latency of the join. 256 rows of 131072 bf16
-// logits, a fifth of them not read: 38.5 us for 54 MB (a copy's rate: 10) with vector instructions issued in 52 % of the
-// cycles, join 8. 24 % fewer instructions in the sums' loop, none of them f64, changed nothing, nor did a threshold
+// What bounds it: f64 arithmetic, 15 instructions a logit of 18, and latency. 256 rows of 131072 bf16
+// logits, a fifth of them not read: 39 us for 54 MB (a copy's rate: 10) with vector instructions issued in 52 % of the
+// cycles, so that neither they nor HBM are full: waves wait for a load one turn ahead in a third of theirs. Join 8: each
+// of k picks waits for a load of its list. 24 % fewer instructions in the sums' loop, none of them f64, changed nothing, nor did a threshold
 // that the waves of a row share, nor 1536 or 2048 workgroups for 1024 (44, 50 and 48 us). Four rows of 32000 f32
-// logits: 7.4 and 4.9 us, two launches and their latencies.
+// logits: 7.1 and 5.0 us, two launches and their latencies.
 #include "beam.hpp"
 
 namespace bitmm {

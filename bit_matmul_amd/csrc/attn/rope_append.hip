@@ -10,9 +10,11 @@
 // instructions run at the rate of f32's here. Nothing is rounded but the group's scale and bias (to f32 and
 // bf16, as stored) and the code. Values are 16-bit numbers as they come and are quantized by cache.hip's steps.
 //
-// What bounds it: 8191 tokens of 40 + 8 heads of 128 dims, 211 MB: 61 us, 3.5 TB/s (a copy 41), the sum of queries
-// alone (38) and of keys and values alone (21, of it 5 for f64 arithmetic over the append's 16: scattered pieces of 64
-// and 8 bytes); mixing their workgroups made it 65. 8 tokens: 4.5 us, a launch and the latencies of slot, loads and stores.
+// What bounds it: 8191 tokens of 40 + 8 heads of 128 dims, 211 MB: 53 us, 4.0 TB/s (a copy 41). Calls take 55.8, where
+// queries alone take 38.0 (rope.hip's kernel) and keys and values alone 20.4 (of it 5 for f64 arithmetic over the append's
+// 16: scattered pieces of 64 and 8 bytes): the two overlap little, and mixing their workgroups made it slower. The two
+// calls one after the other take 68.0. 8 tokens: 4.4 us, a launch and the latencies of slot, loads and stores; calls
+// 8.7 against 13.4.
 #include "beam.hpp"
 #include "cache.hpp"
 #include "rope.hpp"
@@ -279,7 +281,7 @@ __global__ __launch_bounds__(256) void qk_norm_rope_append_kernel(RopeAppendPara
     const unsigned wave = (blockIdx.x - p.kv_blocks) * 4 + in_block, token = wave / (unsigned)p.rope.waves_per_token;
     if (token < (unsigned)p.rope.T)
       // five turns ahead: keys' registers let a SIMD hold half as many waves as rope.hip's kernel (8191 tokens of
-      // 40 + 8 heads of 128 dims: 77 us one turn ahead, 66 three, 61 five)
+      // 40 + 8 heads of 128 dims: 62.5 us one turn ahead, 54.0 three, 52.6 five; calls 64.7, 57.5, 55.7)
       norm_rope_heads<D, INTERLEAVED, DT, 5>(p.rope, token, (int)(wave - token * p.rope.waves_per_token), lane);
   }
 }

@@ -55,7 +55,8 @@ bitmm_status bitmm_qk_norm_rope_append(const void* q, int64_t q_stride, const vo
  * and its sequence's own ones up to its own position, which is that of bitmm_kv_attention over the own
  * tokens alone. A sequence of no group has its own tokens alone. The result is that of bitmm_kv_attention
  * over shared and own tokens in a row, with another order of sums; there is no window (the shared part of one
- * is short: use bitmm_kv_attention).
+ * is short: use bitmm_kv_attention). Where prefixes end with a page, bitmm_kv_attention over tables that name the shared
+ * pages gives that too, and is the faster of the two where sequences and tokens are few.
  * max_group_q bounds the queries of a group, max_prefix the shared tokens, max_q and max_kv the queries
  * and own tokens of a sequence; what passes them is cut and sets *status, and rows past them are not written.
  * `workspace`: bitmm_kv_attention_shared_workspace_bytes(...) bytes, 16-byte aligned, no initialisation
@@ -84,8 +85,8 @@ bitmm_status bitmm_kv_attention_shared(const void* q, int64_t q_stride, const bi
  *   total = scores[g, b] + (logits[r, t] - log sum_u exp(logits[r, u]))
  * Of each group the k candidates of the largest total come out, in order: scores_out, parents (the
  * beam, 0 .. beams - 1) and tokens, all [groups, k]. Equal totals go to the lowest (beam, token); of
- * one beam the order is that of its logits. Sums, totals and comparisons are f64 (exact to 1e-10),
- * scores_out is rounded once.
+ * one beam the order is that of its logits. Sums, totals and comparisons are f64 (sums exact to 2^-32 or so of
+ * themselves, whatever the logits' size), scores_out is rounded once.
  * A beam whose finished[r] (uint8 [groups, beams], or NULL for none) is not 0 has one candidate: end_token with
  * its score as it is; its logits are not read. finished_out (uint8 [groups, k], or NULL) is 1
  * where the parent was finished or the token is end_token (-1: no such token).
@@ -122,7 +123,7 @@ bitmm_status bitmm_beam_select(const void* logits, int64_t row_stride, const flo
  * they lie in no other group's pool.
  * A row for which no page or no place in the table is left keeps its parent's tokens and gets no room:
  * its slot is -1, lens_out is its parent's, and *status is set, as it is by parents and lengths out of range
- * (taken as -1, and cut) and by a partly filled page outside the cache, whose tokens are lost: the first row that has
+ * (taken as -1, and cut) and by a partly filled page outside the cache, whose tokens are lost: the row that would keep
  * it gets no room, any other a page of its own, of which the slots before its next token hold what lay there before.
  * Empty rows have slot -1 and a length of 0.
  * Entries of the table past a row's pages are passed on as they are. An output may be its input (same
